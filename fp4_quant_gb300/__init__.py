@@ -24,7 +24,23 @@ __all__ = [
     "GluQuantError", "fwd", "bwd", "library_path",
     "ACT_SILU", "ACT_GELU_TANH", "ACT_RELU", "ACT_IDENTITY", "ACT_GELU_ERF", "ACT_BF16_STEPS", "FMT_MXFP8", "FMT_NVFP4", "FMT_BF16", "FMT_FP32", "FMT_MXFP8_128X4",
     "MODE_ROW", "MODE_COL", "MODE_BOTH", "LAYOUT_SPLIT", "LAYOUT_INTERLEAVED",
+    "block_norm", "block_norm_bwd", "route", "dispatch", "dispatch_bwd", "combine", "combine_bwd", "linear", "linear_bwd",
+    "block_device_errors", "block_abi_version",
 ]
+
+#: The operators around the gated activation live in ``block``, which needs
+#: torch; they are looked up there on first use.
+_BLOCK = frozenset(__all__[__all__.index("block_norm"):])
+
+
+def __getattr__(name):
+    if name in _BLOCK:
+        from . import block
+        for n in _BLOCK:
+            globals()[n] = getattr(block, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
 
 ACT_SILU, ACT_GELU_TANH, ACT_RELU, ACT_IDENTITY, ACT_GELU_ERF = 0, 1, 2, 3, 4  # SiLU, GELU (tanh), ReLU (ReGLU), identity (bilinear), GELU (erf)
 ACT_BF16_STEPS = 16  # OR-ed into act (forward): the eager bf16 values RN_bf16(RN_bf16(act(g)) * up)

@@ -152,13 +152,24 @@ void sizes_for(int32_t fmt, int32_t mode, int64_t M, int64_t W, size_t s[4]) {
   }
 }
 
+int launched(cudaError_t e) {
+  if (e == cudaSuccess) return GLU_OK;
+  cudaGetLastError();  // the launch error is reported through the status
+  return GLU_ELAUNCH;
+}
+
+}  // namespace
+
 // Device gate: the kernels are built for sm_103a only.  Per-device facts are
 // cached after the first query (devices are never reconfigured at run time).
+namespace {
 constexpr int kMaxDev = 64;
 std::atomic<int> g_dev_state[kMaxDev];  // 0 unknown, 1 ok, -1 unsupported
 std::atomic<int> g_dev_sms[kMaxDev];
 
-int device_info(gq::DevInfo* info) {
+}  // namespace
+
+int gq::device_info(gq::DevInfo* info) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) {
     cudaGetLastError();  // clear the error this probe raised
@@ -183,19 +194,11 @@ int device_info(gq::DevInfo* info) {
   return GLU_OK;
 }
 
-int launched(cudaError_t e) {
-  if (e == cudaSuccess) return GLU_OK;
-  cudaGetLastError();  // the launch error is reported through the status
-  return GLU_ELAUNCH;
-}
-
-}  // namespace
-
 extern "C" int glu_quant_fwd(const glu_quant_fwd_args* a, void* stream) {
   int st = check_fwd(a);
   if (st != GLU_OK) return st;
   gq::DevInfo d;
-  st = device_info(&d);
+  st = gq::device_info(&d);
   if (st != GLU_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (a->fmt) {
@@ -212,7 +215,7 @@ extern "C" int glu_quant_fwd_nvfp4_gs(const glu_quant_fwd_args* a, const float* 
   int st = check_fwd(a);
   if (st != GLU_OK) return st;
   gq::DevInfo d;
-  st = device_info(&d);
+  st = gq::device_info(&d);
   if (st != GLU_OK) return st;
   return launched(gq::launch_fwd_nvfp4(*a, amax, static_cast<cudaStream_t>(stream), d));
 }
@@ -221,7 +224,7 @@ extern "C" int glu_quant_bwd(const glu_quant_bwd_args* a, void* stream) {
   int st = check_bwd(a);
   if (st != GLU_OK) return st;
   gq::DevInfo d;
-  st = device_info(&d);
+  st = gq::device_info(&d);
   if (st != GLU_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->fmt == GLU_FMT_MXFP8_E4M3 || a->fmt == GLU_FMT_MXFP8_E4M3_128X4 || a->fmt == GLU_FMT_NVFP4_E2M1)
@@ -233,7 +236,7 @@ extern "C" int glu_quant_gemm_fwd(const glu_quant_gemm_args* a, void* stream) {
   int st = check_gemm(a);
   if (st != GLU_OK) return st;
   gq::DevInfo d;
-  st = device_info(&d);
+  st = gq::device_info(&d);
   if (st != GLU_OK) return st;
   return launched(gq::launch_gemm_glu(*a, static_cast<cudaStream_t>(stream), d));
 }

@@ -47,9 +47,18 @@ __device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr) {
          (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
 
+// The same for an M/N-major operand tile (M or N contiguous): rows of 64
+// elements along M/N, one per k, 8-k atoms of 1024 bytes one after another
+// along K (stride byte offset), blocks of 64 along M/N `block_bytes` apart
+// (leading byte offset).  A 16-element K slice starts 2048 bytes further.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t block_bytes) {
+  return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(block_bytes >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
 // Instruction descriptor of tcgen05.mma kind::f16: D fp32 (bits 4-5 = 1),
-// A and B bf16 (bits 7-9, 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3
-// in bits 17-22, M >> 4 in bits 24-28.
+// A and B bf16 (bits 7-9, 10-12 = 1), both K-major (bits 15, 16 = 0; 1 for
+// M/N-major), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
 }
