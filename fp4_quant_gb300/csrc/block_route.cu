@@ -147,9 +147,15 @@ struct RowsP {
 
 constexpr int kRowWarps = 8;
 
-__device__ __forceinline__ int64_t slot_at(const RowsP& p, int64_t j) {
-  const int32_t v = p.slot[j];
-  return v >= 0 && v < p.R ? v : -1;
+__device__ __forceinline__ void put8(uint16_t* o, int n, const uint4& v) {
+  if (n >= 8) {
+    stg_once(o, v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) o[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+  }
 }
 
 // Zero rows of the places that no assignment has; warp `wid` of `warps`.
@@ -167,76 +173,125 @@ __device__ __forceinline__ void zero_rows(const RowsP& p, int64_t wid, int64_t w
   }
 }
 
-// One warp per token: its row is read once and stored at each of its places.
+// Eight places of a token at a time: lane j holds the j-th, and the weight.
+struct Places {
+  int32_t slot;
+  float w;
+};
+__device__ __forceinline__ Places places_of(const RowsP& p, int64_t t, int64_t k0, int lane) {
+  Places v = {-1, 1.0f};
+  if (lane < 8 && k0 + lane < p.K) {
+    const int64_t j = t * p.K + k0 + lane;
+    v.slot = p.slot[j];
+    if (v.slot >= p.R) v.slot = -1;
+    if (p.w) v.w = p.w[j];
+  }
+  return v;
+}
+
+// One warp per token and 256 C columns: its part of the row is read once, C
+// loads at a time, and stored at each of the token's places.
+template <int C>
 __global__ void __launch_bounds__(kRowWarps * 32) dispatch_kernel(const RowsP p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
-  for (int64_t t = wid; t < p.T; t += warps)
-    for (int c = 8 * lane; c < int(p.D); c += 256) {
-      float v[8];
-      load8(p.tokens_in + t * p.ld_tokens + c, int(p.D) - c, v);
-      for (int64_t k = 0; k < p.K; ++k) {
-        const int64_t q = slot_at(p, t * p.K + k);
-        if (q >= 0) store8(p.rows_out + q * p.ld_rows_out + c, int(p.D) - c, v);
+  const int64_t parts = (p.D + 256 * C - 1) / (256 * C);
+  for (int64_t u = wid; u < p.T * parts; u += warps) {
+    const int64_t t = u / parts;
+    const int c0 = int(u % parts) * 256 * C + 8 * lane, D = int(p.D);
+    uint4 v[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+      if (c0 + 256 * i < D) v[i] = raw8(p.tokens_in + t * p.ld_tokens + c0 + 256 * i, D - c0 - 256 * i);
+    for (int64_t k0 = 0; k0 < p.K; k0 += 8) {
+      const Places at = places_of(p, t, k0, lane);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int32_t q = __shfl_sync(0xFFFFFFFFu, at.slot, k);
+        if (q < 0) continue;
+        uint16_t* o = p.rows_out + q * p.ld_rows_out + c0;
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if (c0 + 256 * i < D) put8(o + 256 * i, D - c0 - 256 * i, v[i]);
       }
     }
+  }
   zero_rows(p, wid, warps);
 }
 
-// One warp per token and 256 columns.
+// One warp per token and 256 columns, eight rows' loads at a time.
 __global__ void __launch_bounds__(kRowWarps * 32) combine_kernel(const RowsP p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
   const int64_t parts = (p.D + 255) / 256;
   for (int64_t u = wid; u < p.T * parts; u += warps) {
     const int64_t t = u / parts;
-    const int c = int(u % parts) * 256 + 8 * lane;
-    if (c >= int(p.D)) continue;
+    const int c = int(u % parts) * 256 + 8 * lane, left = int(p.D) - c;
     float v[8] = {};
-    for (int64_t k = 0; k < p.K; ++k) {
-      const int64_t q = slot_at(p, t * p.K + k);
-      if (q < 0) continue;
-      const float w = p.w ? p.w[t * p.K + k] : 1.0f;
-      float x[8];
-      load8(p.rows_in + q * p.ld_rows + c, int(p.D) - c, x);
+    if (p.residual && left > 0) load8(p.residual + t * p.ld_residual + c, left, v);
+    for (int64_t k0 = 0; k0 < p.K; k0 += 8) {
+      const Places at = places_of(p, t, k0, lane);
+      uint4 x[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = fmaf(w, x[i], v[i]);
-    }
-    if (p.residual) {
-      float x[8];
-      load8(p.residual + t * p.ld_residual + c, int(p.D) - c, x);
+      for (int k = 0; k < 8; ++k) {
+        const int32_t q = __shfl_sync(0xFFFFFFFFu, at.slot, k);
+        x[k] = q >= 0 && left > 0 ? raw8(p.rows_in + q * p.ld_rows + c, left) : make_uint4(0, 0, 0, 0);
+      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += x[i];
+      for (int k = 0; k < 8; ++k) {
+        const int32_t q = __shfl_sync(0xFFFFFFFFu, at.slot, k);
+        const float w = __shfl_sync(0xFFFFFFFFu, at.w, k);
+        if (q < 0) continue;  // its weight may be anything
+        float f[8];
+        unpack8(x[k], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = fmaf(w, f[i], v[i]);
+      }
     }
-    store8(p.tokens_out + t * p.ld_tokens + c, int(p.D) - c, v);
+    if (left > 0) store8(p.tokens_out + t * p.ld_tokens + c, left, v);
   }
 }
 
 // One warp per token: dout's row goes out, weighted, to each of its places,
-// and its product with the row there is the weight's gradient.
+// and its product with the row there is the weight's gradient.  Eight rows'
+// loads at a time; dout is read once per eight choices.
 __global__ void __launch_bounds__(kRowWarps * 32) combine_bwd_kernel(const RowsP p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
   for (int64_t t = wid; t < p.T; t += warps)
-    for (int64_t k = 0; k < p.K; ++k) {
-      const int64_t j = t * p.K + k, q = slot_at(p, j);
-      float dot = 0.0f;
-      if (q >= 0) {
-        const float w = p.w[j];
-        for (int c = 8 * lane; c < int(p.D); c += 256) {
-          float d[8], x[8];
-          load8(p.tokens_in + t * p.ld_tokens + c, int(p.D) - c, d);
-          load8(p.rows_in + q * p.ld_rows + c, int(p.D) - c, x);
+    for (int64_t k0 = 0; k0 < p.K; k0 += 8) {
+      const Places at = places_of(p, t, k0, lane);
+      float dot[8] = {};
+      for (int c0 = 0; c0 < int(p.D); c0 += 256) {
+        const int c = c0 + 8 * lane, left = int(p.D) - c;  // left <= 0: this lane has none
+        uint4 x[8];
+        float d[8] = {};
+        if (left > 0) load8(p.tokens_in + t * p.ld_tokens + c, left, d);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int32_t q = __shfl_sync(0xFFFFFFFFu, at.slot, k);
+          x[k] = q >= 0 && left > 0 ? raw8(p.rows_in + q * p.ld_rows + c, left) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int32_t q = __shfl_sync(0xFFFFFFFFu, at.slot, k);
+          const float w = __shfl_sync(0xFFFFFFFFu, at.w, k);
+          if (q < 0 || left <= 0) continue;
+          float f[8];
+          unpack8(x[k], f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            dot = fmaf(d[i], x[i], dot);
-            d[i] *= w;
+            dot[k] = fmaf(d[i], f[i], dot[k]);
+            f[i] = w * d[i];
           }
-          store8(p.rows_out + q * p.ld_rows_out + c, int(p.D) - c, d);
+          store8(p.rows_out + q * p.ld_rows_out + c, left, f);
         }
-        dot = warp_sum(dot);
       }
-      if (lane == 0) p.dw[j] = dot;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float s = warp_sum(dot[k]);
+        if (lane == 0 && k0 + k < p.K) p.dw[t * p.K + k0 + k] = s;
+      }
     }
   zero_rows(p, wid, warps);
 }
@@ -297,7 +352,11 @@ cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s) {
 
 cudaError_t launch_dispatch(const glu_block_rows_args& a, cudaStream_t s, const DevInfo& d) {
   const RowsP p = rows_of(a);
-  return launch_kernel(dispatch_kernel, row_grid(p.T > p.R / 32 ? p.T : p.R / 32, d), kRowWarps * 32, 0, s, p);
+  // 1024 columns per warp (four loads in flight) where there are enough
+  // tokens to fill the SMs that way
+  if (p.T * ((p.D + 1023) / 1024) >= int64_t(d.sms) * 32)
+    return launch_kernel(dispatch_kernel<4>, row_grid(p.T * ((p.D + 1023) / 1024), d), kRowWarps * 32, 0, s, p);
+  return launch_kernel(dispatch_kernel<1>, row_grid(p.T * ((p.D + 255) / 256), d), kRowWarps * 32, 0, s, p);
 }
 
 cudaError_t launch_combine(const glu_block_rows_args& a, cudaStream_t s, const DevInfo& d) {

@@ -54,6 +54,15 @@ __device__ __forceinline__ void stg_once(void* p, const uint4& v) {
                : "memory");
 }
 
+// The first n (1..8) bf16 of a chunk as they are; the rest is 0.
+__device__ __forceinline__ uint4 raw8(const uint16_t* p, int n) {
+  if (n >= 8) return ldg_once(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = (2 * i < n ? uint32_t(p[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(p[2 * i + 1]) << 16 : 0u);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The first n (1..8) elements of a chunk; the rest of v is 0.
 __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
   if (n >= 8) {
@@ -119,26 +128,30 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums over the block of N values per thread, the same bits in every thread.
-// `buf` alternates between calls (two buffers), so one barrier per call is
-// enough: a buffer is written again only after the next call's barrier.
+// Sums over the first `threads` threads of the block (whole warps; the others
+// do not call) of N values each, the same bits in every thread.  `buf`
+// alternates between calls (two buffers), so one barrier per call is enough:
+// a buffer is written again only after the next call's barrier.
 template <int N>
 struct BlockSum {
   float part[2][32][N];
 };
 template <int N>
-__device__ __forceinline__ void block_sum(BlockSum<N>& s, uint32_t& buf, float (&v)[N]) {
-  const int warps = int(blockDim.x + 31) >> 5;
+__device__ __forceinline__ void block_sum(BlockSum<N>& s, uint32_t& buf, int threads, float (&v)[N]) {
+  const int warps = threads >> 5;
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = warp_sum(v[j]);
-  if (warps == 1) return;
+  if (warps == 1) {
+    __syncwarp();
+    return;
+  }
   float(&p)[32][N] = s.part[buf & 1u];
   ++buf;
   if ((threadIdx.x & 31) == 0) {
 #pragma unroll
     for (int j = 0; j < N; ++j) p[threadIdx.x >> 5][j] = v[j];
   }
-  __syncthreads();
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
 #pragma unroll
   for (int j = 0; j < N; ++j) v[j] = 0.0f;
   for (int w = 0; w < warps; ++w) {
