@@ -12,6 +12,7 @@ constexpr int kMaxExperts = 1024;
 
 cudaError_t launch_norm_fwd(const glu_block_norm_fwd_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s);
+cudaError_t read_err_norm(uint32_t* v, bool clear);
 size_t norm_bwd_workspace(int64_t M, int64_t D, int64_t gates);
 
 cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s);

@@ -6,14 +6,91 @@
 // Both directions are a single pass over the rows.  Per element they read 2
 // to 4 numbers and compute a few tens of operations, so DRAM bounds them:
 // the forward moves x, branch, r and y once (8 bytes per element with a bf16
-// stream), the backward r, branch, dy, dr, dx and dbranch (12 bytes).  A row
-// stays in the registers of one block between its statistics and its
-// outputs.
+// stream), the backward r, branch, dy, dr, dx and dbranch (12 bytes).  Rows
+// come through a ring of stages in shared memory, copied there in bulk, so
+// that the loads of the next rows are in flight while a row's sums are joined
+// across the block.  A stage is refilled after a barrier that those sums need
+// anyway: by then every thread is done with the row it held.
 #include "block.h"
 #include "block_util.cuh"
+#include "tma.cuh"
 
 namespace gq {
 namespace {
+
+__device__ uint32_t g_err_norm;
+
+constexpr int kMaxStages = 8;
+constexpr int kSmemMost = 232448;  // shared memory per block
+constexpr int kCtlBytes = 2048;    // of it, ahead of the stages
+
+template <int N>
+struct RingCtl {
+  uint64_t full[kMaxStages];
+  BlockSum<N> sums;
+  int64_t item, row, end;  // the backward's next row to load, its item, the end of that item's rows
+};
+static_assert(sizeof(RingCtl<3>) <= kCtlBytes, "ring control block");
+
+// Waits that gave up leave a mark and are not repeated: what follows runs on
+// with whatever the stage holds, within its bounds, to its end.
+struct RingWait {
+  bool dead = false;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (dead) return;
+    if (!mbar_wait(bar, parity)) {
+      dead = true;
+      atomicOr(&g_err_norm, kErrWaitFull);
+    }
+  }
+};
+
+__device__ __forceinline__ void row_barrier(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
+
+// A chunk of eight columns (from column c) of a staged row.  RAGGED: where the
+// width D ends inside it, its first ones from row m itself (the copies take
+// whole chunks), the rest 0.
+template <bool RAGGED>
+__device__ __forceinline__ F8 staged8(const uint8_t* stage, const uint16_t* base, int64_t m, int64_t ld, int c, int D) {
+  if (!RAGGED || c + 8 <= D) return pairs(*reinterpret_cast<const uint4*>(stage + 2 * c));
+  return pairs(raw8(base + m * ld + c, D - c));
+}
+template <bool RAGGED>
+__device__ __forceinline__ F8 staged8(const uint8_t* stage, const float* base, int64_t m, int64_t ld, int c, int D) {
+  if (!RAGGED || c + 8 <= D) {
+    const float4 a = *reinterpret_cast<const float4*>(stage + 4 * c), b = *reinterpret_cast<const float4*>(stage + 4 * c + 16);
+    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+  }
+  float v[8];
+  load8(base + m * ld + c, D - c, v);
+  return pairs(v);
+}
+template <typename T>
+__device__ __forceinline__ F8 direct8(const T* row, int c, int n) {
+  float v[8];
+  load8(row + c, n, v);
+  return pairs(v);
+}
+
+// w + o of a chunk of a weight vector, times `scale`, times the gate's if there is one.
+__device__ __forceinline__ F8 weight8(const void* w, bool f32, float o, float scale, const uint16_t* gate, int c, int n) {
+  float v[8];
+  if (w) {
+    vec8(w, f32, c, n, o, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = scale;
+  }
+  if (gate) {
+    float g[8];
+    vec8(gate, false, c, n, 0.0f, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= g[i];
+  }
+  return pairs(v);
+}
 
 struct NormFwdP {
   const void* x;
@@ -26,108 +103,229 @@ struct NormFwdP {
   int64_t M, D, rows_per_gate;
   int64_t ld_x, ld_branch, ld_gate, ld_r, ld_y;
   float alpha, w_offset, eps;
-  int w32;
+  int w32, stages, stage_bytes;
+  int stream_gate;  // the gate's row is staged with each row (few rows share one)
 };
 
-__device__ __forceinline__ float rstd_of(float sum, int64_t D, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fdiv_rn(sum, float(D)) + eps));
+// 1 / sqrt(sum / D + eps), with the reciprocal of D.
+__device__ __forceinline__ float rstd_of(float sum, float per_d, float eps) {
+  return __frcp_rn(__fsqrt_rn(fmaf(sum, per_d, eps)));
 }
 
-// One block per row (grid-stride over the rows), V chunks of eight columns
-// per thread: chunk k of thread t starts at column 8 (t + k * threads).
-template <typename XT, int V>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const NormFwdP p) {
-  __shared__ BlockSum<1> sums;
-  uint32_t buf = 0;
-  const int D = int(p.D);
-  for (int64_t m = blockIdx.x; m < p.M; m += gridDim.x) {
-    float r[V][8], b[V][8];
-    const XT* xr = static_cast<const XT*>(p.x) + m * p.ld_x;
+// Outputs of row m from V chunks per thread (chunk k of thread t starts at
+// column 8 (t + k * threads)): r holds x on entry, b the branch times f =
+// alpha gate (w_post + o), sq the thread's sum of the branch's squares.  Only
+// a product and a conversion per element wait for each sum.  `met` is called
+// once, behind a barrier that every thread reached with its chunks in
+// registers.
+template <typename XT, int V, bool RAGGED, typename W, typename Met>
+__device__ __forceinline__ void norm_row(const NormFwdP& p, int64_t m, int threads, BlockSum<1>& sums, uint32_t& buf,
+                                         F8 (&r)[V], F8 (&b)[V], float sq, float per_d, W w_pre, Met met) {
+  const int D = int(p.D), tid = threadIdx.x;
+  if (p.branch) {
+    float rs = 1.0f;
+    if (p.w_post) {
+      float s[1] = {sq};
+      block_sum(sums, buf, threads, s);
+      met();
+      rs = rstd_of(s[0], per_d, p.eps);
+      if (tid == 0) p.rstd_post[m] = rs;
+    }
+    XT* rr = static_cast<XT*>(p.r) + m * p.ld_r;
 #pragma unroll
     for (int k = 0; k < V; ++k) {
-      const int c = 8 * int(threadIdx.x + k * blockDim.x);
-      if (c < D) {
-        load8(xr + c, D - c, r[k]);
-        if (p.branch) load8(p.branch + m * p.ld_branch + c, D - c, b[k]);
+      const int c = 8 * (tid + k * threads);
+      if (c >= D) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[k].v[i] = fma_2(b[k].v[i], both(rs), r[k].v[i]);
+      store8<RAGGED>(rr + c, D - c, r[k]);
+    }
+  }
+  if (p.w_pre) {
+    float2 s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c >= D) continue;
+      const F8 w = w_pre(k, c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s2 = fma_2(r[k].v[i], r[k].v[i], s2);
+        r[k].v[i] = mul_2(r[k].v[i], w.v[i]);
       }
     }
+    float s[1] = {sum2(s2)};
+    block_sum(sums, buf, threads, s);
+    if (!p.w_post) met();
+    const float rs = rstd_of(s[0], per_d, p.eps);
+    if (tid == 0) p.rstd_pre[m] = rs;
+    uint16_t* yr = p.y + m * p.ld_y;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c >= D) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[k].v[i] = mul_2(r[k].v[i], both(rs));
+      store8<RAGGED>(yr + c, D - c, r[k]);
+    }
+  } else if (!p.w_post) {
+    row_barrier(threads);
+    met();
+  }
+}
+
+// Few rows: one block per row, one chunk per thread, straight from memory.
+template <typename XT>
+__global__ void __launch_bounds__(1024) norm_fwd_row_kernel(const NormFwdP p) {
+  __shared__ BlockSum<1> sums;
+  uint32_t buf = 0;
+  const int D = int(p.D), c = 8 * int(threadIdx.x);
+  const int64_t m = blockIdx.x;
+  F8 r[1] = {zeros()}, b[1] = {zeros()}, w = zeros();
+  float2 sq = make_float2(0.0f, 0.0f);
+  if (c < D) {
+    r[0] = direct8(static_cast<const XT*>(p.x) + m * p.ld_x, c, D - c);
+    if (p.w_pre) w = weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c);
     if (p.branch) {
-      if (p.w_post) {
-        float s[1] = {0.0f};
+      b[0] = direct8(p.branch + m * p.ld_branch, c, D - c);
+      const F8 f = weight8(p.w_post, p.w32, p.w_offset, p.alpha, p.gate ? p.gate + (m / p.rows_per_gate) * p.ld_gate : nullptr, c, D - c);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-          if (8 * int(threadIdx.x + k * blockDim.x) >= D) continue;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] = fmaf(b[k][i], b[k][i], s[0]);
-        }
-        block_sum(sums, buf, s);
-        const float rs = rstd_of(s[0], p.D, p.eps);
-        if (threadIdx.x == 0) p.rstd_post[m] = rs;
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = 8 * int(threadIdx.x + k * blockDim.x);
-          if (c >= D) continue;
-          float w[8];
-          vec8(p.w_post, p.w32, c, D - c, p.w_offset, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[k][i] = b[k][i] * rs * w[i];
-        }
-      }
-      XT* rr = static_cast<XT*>(p.r) + m * p.ld_r;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-        if (c >= D) continue;
-        if (p.gate) {
-          float g[8];
-          vec8(p.gate + (m / p.rows_per_gate) * p.ld_gate, false, c, D - c, 0.0f, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) b[k][i] *= g[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[k][i] = i < D - c ? fmaf(p.alpha, b[k][i], r[k][i]) : 0.0f;
-        store8(rr + c, D - c, r[k]);
-      }
-    }
-    if (p.w_pre) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        if (8 * int(threadIdx.x + k * blockDim.x) >= D) continue;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(r[k][i], r[k][i], s[0]);
-      }
-      block_sum(sums, buf, s);
-      const float rs = rstd_of(s[0], p.D, p.eps);
-      if (threadIdx.x == 0) p.rstd_pre[m] = rs;
-      uint16_t* yr = p.y + m * p.ld_y;
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-        if (c >= D) continue;
-        float w[8];
-        vec8(p.w_pre, p.w32, c, D - c, p.w_offset, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = r[k][i] * rs * w[i];
-        store8(yr + c, D - c, w);
+      for (int i = 0; i < 4; ++i) {
+        sq = fma_2(b[0].v[i], b[0].v[i], sq);
+        b[0].v[i] = mul_2(b[0].v[i], f.v[i]);
       }
     }
   }
+  norm_row<XT, 1, true>(p, m, blockDim.x, sums, buf, r, b, sum2(sq), __frcp_rn(float(D)), [&](int, int) { return w; }, [] {});
+}
+
+// Many rows: each block takes consecutive ones through a ring of staged rows.
+// Up to V = 2 chunks per thread (D <= 8192) the weights of a thread's columns
+// stay in its registers, wider rows fetch them again.
+template <typename XT, int V, bool RAGGED>
+__global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  RingCtl<1>* ctl = reinterpret_cast<RingCtl<1>*>(smem);
+  uint8_t* stages = smem + kCtlBytes;
+  const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
+  const uint32_t whole = uint32_t(D / 8) * 16, xb = whole / 2 * sizeof(XT), at_g = xb + (p.branch ? whole : 0u);
+  const int64_t m0 = p.M * blockIdx.x / gridDim.x, m1 = p.M * (blockIdx.x + 1) / gridDim.x;
+  // loads row m into stage s (one thread)
+  auto load = [&](int64_t m, int s) {
+    uint8_t* st = stages + s * p.stage_bytes;
+    mbar_arrive_expect_tx(&ctl->full[s], uint32_t(p.stage_bytes));
+    if (whole == 0) return;
+    bulk_load(st, static_cast<const XT*>(p.x) + m * p.ld_x, xb, &ctl->full[s]);
+    if (p.branch) bulk_load(st + xb, p.branch + m * p.ld_branch, whole, &ctl->full[s]);
+    if (p.stream_gate) bulk_load(st + at_g, p.gate + m / p.rows_per_gate * p.ld_gate, whole, &ctl->full[s]);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], 1);
+    fence_barrier_init();
+    for (int s = 0; s < p.stages; ++s)
+      if (m0 + s < m1) load(m0 + s, s);
+  }
+  __syncthreads();
+  constexpr bool kHold = V <= 2;
+  F8 w[kHold ? V : 1], f[kHold ? V : 1];
+  if (kHold && p.w_pre) {
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c < D) w[kHold ? k : 0] = weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c);
+    }
+  }
+  RingWait wait;
+  int s = 0;
+  uint32_t parity = 0, buf = 0;
+  const float per_d = __frcp_rn(float(D));
+  int64_t grp = 0, g_end = m0;  // the gate row, and the first row past its rows
+  int64_t f_end = m0;           // first row that f does not hold for
+  for (int64_t m = m0; m < m1; ++m) {
+    if (m >= g_end) {
+      grp = m / p.rows_per_gate;
+      g_end = (grp + 1) * p.rows_per_gate;
+    }
+    const uint16_t* gate_row = p.gate + grp * p.ld_gate;
+    auto factors = [&](int c) {
+      return weight8(p.w_post, p.w32, p.w_offset, p.alpha, p.gate && !p.stream_gate ? gate_row : nullptr, c, D - c);
+    };
+    if (kHold && p.branch && m >= f_end) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = 8 * (tid + k * threads);
+        if (c < D) f[kHold ? k : 0] = factors(c);
+      }
+      f_end = p.gate && !p.stream_gate ? g_end : m1;
+    }
+    const uint8_t* st = stages + s * p.stage_bytes;
+    wait(&ctl->full[s], parity);
+    F8 r[V], b[V];
+    float2 sq = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c >= D) continue;
+      r[k] = staged8<RAGGED>(st, static_cast<const XT*>(p.x), m, p.ld_x, c, D);
+      if (!p.branch) continue;
+      b[k] = staged8<RAGGED>(st + xb, p.branch, m, p.ld_branch, c, D);
+      const F8 fk = kHold ? f[kHold ? k : 0] : factors(c);
+      F8 g = zeros();
+      if (p.stream_gate) g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sq = fma_2(b[k].v[i], b[k].v[i], sq);
+        b[k].v[i] = mul_2(b[k].v[i], fk.v[i]);
+        if (p.stream_gate) b[k].v[i] = mul_2(b[k].v[i], g.v[i]);
+      }
+    }
+    norm_row<XT, V, RAGGED>(p, m, threads, ctl->sums, buf, r, b, sum2(sq), per_d,
+                    [&](int k, int c) { return kHold ? w[kHold ? k : 0] : weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c); },
+                    [&] {
+                      if (tid == 0 && m + p.stages < m1) load(m + p.stages, s);
+                    });
+    if (++s == p.stages) s = 0, parity ^= 1u;
+  }
+}
+
+int row_threads(int64_t chunks, int V) { return int(((chunks + V - 1) / V + 31) / 32 * 32); }
+int row_chunks(int64_t chunks) { return chunks <= 32 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8; }  // per thread
+
+// The ring's stages for `blocks` blocks per SM.
+int ring_stages(int stage_bytes, int blocks) {
+  const int room = (blocks == 1 ? kSmemMost : 228 * 1024 / blocks - 1024) - kCtlBytes;
+  const int n = stage_bytes == 0 ? 1 : room / stage_bytes;
+  return n > kMaxStages ? kMaxStages : n < 1 ? 1 : n;
+}
+// Blocks per SM: 512 threads with 128 registers each.
+int ring_blocks(int threads) { return 512 / threads; }
+
+template <typename XT, int V>
+cudaError_t launch_fwd_rows(NormFwdP p, cudaStream_t s, const DevInfo& d) {
+  const int threads = row_threads((p.D + 7) / 8, V), blocks = ring_blocks(threads);
+  // a gate row shared by few rows comes with each (where one stage has room
+  // for it), else its factors are fetched when it changes
+  p.stream_gate = p.gate != nullptr && p.rows_per_gate < 16 && p.D * int64_t(sizeof(XT) + 4) + kCtlBytes <= kSmemMost;
+  p.stage_bytes = int(p.D / 8 * 8 * (sizeof(XT) + (p.branch ? 2 : 0) + (p.stream_gate ? 2 : 0)));
+  p.stages = ring_stages(p.stage_bytes, blocks);
+  const int smem = kCtlBytes + p.stages * p.stage_bytes;
+  if (smem > kSmemMost) return cudaErrorInvalidValue;
+  auto kern = p.D % 8 != 0 ? norm_fwd_kernel<XT, V, true> : norm_fwd_kernel<XT, V, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t most = int64_t(d.sms) * blocks;
+  return launch_kernel(kern, int(p.M < most ? p.M : most), threads, smem, s, p);
 }
 
 template <typename XT>
 cudaError_t launch_fwd_t(const NormFwdP& p, cudaStream_t s, const DevInfo& d) {
   const int64_t chunks = (p.D + 7) / 8;
-  // chunks per thread: one where there are fewer rows than the SMs hold
-  // blocks (the row's latency counts), else blocks of about 256 threads
-  const int V = chunks > 1024 ? 4 : (p.M <= 2 * d.sms || chunks <= 256) ? 1 : chunks <= 512 ? 2 : 4;
-  const int threads = int(((chunks + V - 1) / V + 31) / 32 * 32);
-  const int64_t most = int64_t(d.sms) * (threads > 512 ? 2 : 2048 / threads > 32 ? 32 : 2048 / threads);
-  const int grid = int(p.M < most ? p.M : most);
-  switch (V) {
-    case 1: return launch_kernel(norm_fwd_kernel<XT, 1>, grid, threads, 0, s, p);
-    case 2: return launch_kernel(norm_fwd_kernel<XT, 2>, grid, threads, 0, s, p);
-    default: return launch_kernel(norm_fwd_kernel<XT, 4>, grid, threads, 0, s, p);
+  if (p.M <= 2 * d.sms && chunks <= 1024) return launch_kernel(norm_fwd_row_kernel<XT>, int(p.M), row_threads(chunks, 1), 0, s, p);
+  switch (row_chunks(chunks)) {
+    case 1: return launch_fwd_rows<XT, 1>(p, s, d);
+    case 2: return launch_fwd_rows<XT, 2>(p, s, d);
+    case 4: return launch_fwd_rows<XT, 4>(p, s, d);
+    default: return launch_fwd_rows<XT, 8>(p, s, d);
   }
 }
 
@@ -140,177 +338,296 @@ struct NormBwdP {
   const float *rstd_pre, *rstd_post;
   void* dx;
   uint16_t* dbranch;
-  float *part_pre, *part_post;  // [gridDim.x, D]
-  float* part_gate;             // [items, D] (dgate itself where a gate row is one item)
+  float* part_pre;   // [gridDim.x, D]
+  float* part_x;     // [items, D], or NULL
+  float* part_post;  // [gridDim.x, D], or NULL
+  float* dgate;      // written here where an item is a whole gate row's rows
   int64_t M, D, rows_per_gate, pieces, items;  // an item: one of `pieces` parts of a gate row's rows
   int64_t ld_r, ld_dr, ld_branch, ld_gate, ld_dy, ld_dx, ld_dbranch;
   float alpha, w_offset;
-  int w32;
+  int w32, stages, stage_bytes;
 };
 
-// Sums over the rows are kept in registers: a thread has the same columns of
-// every row of its block.  A block takes whole items (consecutive rows that
-// share a gate row), so dgate's partial sums never mix gate rows.
-template <typename XT, int V>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const NormBwdP p) {
-  __shared__ BlockSum<1> sums;
-  uint32_t buf = 0;
-  const int D = int(p.D);
-  float a_pre[V][8], a_post[V][8], a_gate[V][8];
+// A thread has the same columns of every row of its block, so the sums over
+// rows stay in its registers.  With w = w_pre + o, h = alpha gate (w_post + o)
+// (or alpha gate), t = dr + rstd_pre dy w and b = branch:
+//   dR = t - r rstd_pre^2 S1 / D,                     S1 = sum rstd_pre dy w r
+//   dbranch = rstd_post h dR - b rstd_post^2 S / D,   S = sum h dR rstd_post b
+// S is had with S1 in one exchange across the block:
+//   S = rstd_post (S2 - rstd_pre^2 (S1 / D) S3),  S2 = sum h b t,  S3 = sum h b r.
+// dw_pre sums dy r rstd_pre.  dgate and dw_post are both multiples of X = sum
+// over the rows of one gate row of dR b rstd_post: dgate = alpha (w_post + o)
+// X, dw_post = sum over gate rows of alpha gate X.  A block takes whole items
+// (consecutive rows that share a gate row).  MANY: an item is all the rows of
+// a gate row, the gate's row is staged with them, and the block finishes dgate
+// and sums dw_post itself; else X goes out per item and the join does both.
+//
+// At 8191 x 8192 (bf16) one block of 16 warps per SM has three 64 KB stages:
+// two rows in flight while one is worked on.
+template <typename XT, int V, bool MANY, bool RAGGED>
+__global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  RingCtl<3>* ctl = reinterpret_cast<RingCtl<3>*>(smem);
+  uint8_t* stages = smem + kCtlBytes;
+  const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
+  const uint32_t whole = uint32_t(D / 8) * 16, xb = whole / 2 * sizeof(XT);
+  const bool pre = p.w_pre != nullptr, post = p.w_post != nullptr, br = p.branch != nullptr, has_dr = p.dr != nullptr;
+  // a stage: r, dy (pre), dr (given), branch (given), gate (MANY)
+  const uint32_t at_dy = pre ? xb : 0u, at_dr = at_dy + (pre ? whole : 0u), at_b = at_dr + (has_dr ? xb : 0u), at_g = at_b + whole;
+  // loads the next row of this block's items into stage s, if there is one (one thread)
+  auto load_next = [&](int s) {
+    while (ctl->row >= ctl->end) {
+      if (ctl->item >= p.items) return;
+      const int64_t base = ctl->item / p.pieces * p.rows_per_gate, piece = ctl->item % p.pieces;
+      ctl->row = base + piece * p.rows_per_gate / p.pieces;
+      ctl->end = base + (piece + 1) * p.rows_per_gate / p.pieces;
+      ctl->item += gridDim.x;
+    }
+    const int64_t m = ctl->row++;
+    uint8_t* st = stages + s * p.stage_bytes;
+    uint64_t* bar = &ctl->full[s];
+    mbar_arrive_expect_tx(bar, uint32_t(p.stage_bytes));
+    if (whole == 0) return;
+    if (pre) {
+      bulk_load(st, static_cast<const XT*>(p.r) + m * p.ld_r, xb, bar);
+      bulk_load(st + at_dy, p.dy + m * p.ld_dy, whole, bar);
+    }
+    if (has_dr) bulk_load(st + at_dr, static_cast<const XT*>(p.dr) + m * p.ld_dr, xb, bar);
+    if (br) bulk_load(st + at_b, p.branch + m * p.ld_branch, whole, bar);
+    if (MANY) bulk_load(st + at_g, p.gate + m / p.rows_per_gate * p.ld_gate, whole, bar);
+  };
+  if (tid == 0) {
+    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], 1);
+    fence_barrier_init();
+    ctl->item = blockIdx.x;
+    ctl->row = ctl->end = 0;
+    for (int s = 0; s < p.stages; ++s) load_next(s);
+  }
+  __syncthreads();
+  F8 a_pre[V], a_x[V], a_post[MANY ? V : 1];
 #pragma unroll
-  for (int k = 0; k < V; ++k)
+  for (int k = 0; k < V; ++k) a_pre[k] = a_x[k] = a_post[MANY ? k : 0] = zeros();
+  // w and h (MANY: without the gate) of this thread's columns: in registers for
+  // up to two chunks, fetched again for every row otherwise
+  constexpr bool kHold = V <= 2;
+  F8 w[kHold ? V : 1], h[kHold ? V : 1];
+  auto fetch_w = [&](int c) { return weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c); };
+  auto fetch_h = [&](int64_t grp, int c) {
+    return weight8(p.w_post, p.w32, p.w_offset, p.alpha, !MANY && p.gate ? p.gate + grp * p.ld_gate : nullptr, c, D - c);
+  };
+  if (kHold) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a_pre[k][i] = a_post[k][i] = a_gate[k][i] = 0.0f;
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c < D && pre) w[kHold ? k : 0] = fetch_w(c);
+      if (c < D && br && MANY) h[kHold ? k : 0] = fetch_h(0, c);
+    }
+  }
+  const float per_d = __frcp_rn(float(D));
+  RingWait wait;
+  int s = 0, last = -1;  // the stage of the row before this one
+  uint32_t parity = 0, buf = 0;
   for (int64_t it = blockIdx.x; it < p.items; it += gridDim.x) {
-    const int64_t grp = it / p.pieces, piece = it % p.pieces;
-    const int64_t m0 = grp * p.rows_per_gate + piece * p.rows_per_gate / p.pieces;
-    const int64_t m1 = grp * p.rows_per_gate + (piece + 1) * p.rows_per_gate / p.pieces;
-    for (int64_t m = m0; m < m1; ++m) {
-      float dR[V][8], n[V][8], u[V][8];
+    const int64_t grp = it / p.pieces, base = grp * p.rows_per_gate, piece = it % p.pieces;
+    const int64_t m1 = base + (piece + 1) * p.rows_per_gate / p.pieces;
+    if (kHold && br && !MANY) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) dR[k][i] = 0.0f;
-        if (c < D && p.dr) load8(static_cast<const XT*>(p.dr) + m * p.ld_dr + c, D - c, dR[k]);
-      }
-      if (p.w_pre) {
-        const float rs = p.rstd_pre[m];
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-          const int c = 8 * int(threadIdx.x + k * blockDim.x);
-          if (c >= D) continue;
-          float w[8];
-          load8(static_cast<const XT*>(p.r) + m * p.ld_r + c, D - c, n[k]);
-          load8(p.dy + m * p.ld_dy + c, D - c, u[k]);
-          vec8(p.w_pre, p.w32, c, D - c, p.w_offset, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            n[k][i] *= rs;
-            a_pre[k][i] = fmaf(u[k][i], n[k][i], a_pre[k][i]);
-            u[k][i] *= w[i];
-            s[0] = fmaf(u[k][i], n[k][i], s[0]);
-          }
-        }
-        block_sum(sums, buf, s);
-        const float mean = __fdiv_rn(s[0], float(D));
-#pragma unroll
-        for (int k = 0; k < V; ++k)
-          if (8 * int(threadIdx.x + k * blockDim.x) < D) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) dR[k][i] = fmaf(rs, fmaf(-n[k][i], mean, u[k][i]), dR[k][i]);
-          }
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-        if (c < D) store8(static_cast<XT*>(p.dx) + m * p.ld_dx + c, D - c, dR[k]);
-      }
-      if (!p.branch) continue;
-      const float rs = p.w_post ? p.rstd_post[m] : 1.0f;
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-        if (c >= D) continue;
-        float w[8], g[8];
-        load8(p.branch + m * p.ld_branch + c, D - c, n[k]);
-        if (p.w_post) vec8(p.w_post, p.w32, c, D - c, p.w_offset, w);
-        if (p.gate) vec8(p.gate + grp * p.ld_gate, false, c, D - c, 0.0f, g);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float ad = p.alpha * dR[k][i];
-          n[k][i] *= rs;
-          if (p.gate) a_gate[k][i] = fmaf(ad, p.w_post ? n[k][i] * w[i] : n[k][i], a_gate[k][i]);
-          u[k][i] = p.gate ? ad * g[i] : ad;  // d
-          if (p.w_post) {
-            a_post[k][i] = fmaf(u[k][i], n[k][i], a_post[k][i]);
-            u[k][i] *= w[i];
-            s[0] = fmaf(u[k][i], n[k][i], s[0]);
-          }
-        }
-      }
-      float mean = 0.0f;
-      if (p.w_post) {
-        block_sum(sums, buf, s);
-        mean = __fdiv_rn(s[0], float(D));
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
-        if (c >= D) continue;
-        if (p.w_post) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) u[k][i] = rs * fmaf(-n[k][i], mean, u[k][i]);
-        }
-        store8(p.dbranch + m * p.ld_dbranch + c, D - c, u[k]);
+        const int c = 8 * (tid + k * threads);
+        if (c < D) h[kHold ? k : 0] = fetch_h(grp, c);
       }
     }
-    if (p.gate) {
+    const int64_t m0 = base + piece * p.rows_per_gate / p.pieces;
+    XT* dx = static_cast<XT*>(p.dx) + m0 * p.ld_dx;
+    uint16_t* db = p.dbranch + m0 * p.ld_dbranch;
+    for (int64_t m = m0; m < m1; ++m, dx += p.ld_dx, db += p.ld_dbranch) {
+      const uint8_t* st = stages + s * p.stage_bytes;
+      const float rs = pre ? p.rstd_pre[m] : 0.0f, rp = post ? p.rstd_post[m] : 1.0f;
+      auto h_of = [&](int k, int c) {
+        F8 f = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
+        if (MANY) {
+          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) f.v[i] = mul_2(f.v[i], g.v[i]);
+        }
+        return f;
+      };
+      wait(&ctl->full[s], parity);
+      F8 t[V];
+      float2 s1 = make_float2(0.0f, 0.0f), s2 = s1, s3 = s1;
 #pragma unroll
       for (int k = 0; k < V; ++k) {
-        const int c = 8 * int(threadIdx.x + k * blockDim.x);
+        const int c = 8 * (tid + k * threads);
+        if (c >= D) continue;
+        t[k] = has_dr ? staged8<RAGGED>(st + at_dr, static_cast<const XT*>(p.dr), m, p.ld_dr, c, D) : zeros();
+        F8 r = zeros();
+        if (pre) {
+          r = staged8<RAGGED>(st, static_cast<const XT*>(p.r), m, p.ld_r, c, D);
+          F8 v = staged8<RAGGED>(st + at_dy, p.dy, m, p.ld_dy, c, D);
+          const F8 wk = kHold ? w[kHold ? k : 0] : fetch_w(c);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (c + i < D) p.part_gate[it * D + c + i] = a_gate[k][i];
-          a_gate[k][i] = 0.0f;
+          for (int i = 0; i < 4; ++i) {
+            v.v[i] = mul_2(v.v[i], both(rs));
+            a_pre[k].v[i] = fma_2(v.v[i], r.v[i], a_pre[k].v[i]);
+            v.v[i] = mul_2(v.v[i], wk.v[i]);
+            s1 = fma_2(v.v[i], r.v[i], s1);
+            t[k].v[i] = add_2(v.v[i], t[k].v[i]);
+          }
         }
+        if (post) {
+          const F8 b = staged8<RAGGED>(st + at_b, p.branch, m, p.ld_branch, c, D), hk = h_of(k, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 q = mul_2(b.v[i], hk.v[i]);
+            s2 = fma_2(q, t[k].v[i], s2);
+            if (pre) s3 = fma_2(q, r.v[i], s3);
+          }
+        }
+      }
+      float sum[3] = {sum2(s1), sum2(s2), sum2(s3)};
+      if (pre || post) block_sum(ctl->sums, buf, threads, sum);
+      else row_barrier(threads);
+      // every thread is done with the row before this one
+      if (tid == 0 && last >= 0) load_next(last);
+      const float k1 = -rs * rs * per_d * sum[0];
+      const float k2 = -rp * rp * rp * per_d * fmaf(k1, sum[2], sum[1]);
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = 8 * (tid + k * threads);
+        if (c >= D) continue;
+        if (pre) {
+          const F8 r = staged8<RAGGED>(st, static_cast<const XT*>(p.r), m, p.ld_r, c, D);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[k].v[i] = fma_2(r.v[i], both(k1), t[k].v[i]);
+        }
+        store8<RAGGED>(dx + c, D - c, t[k]);
+        if (!br) continue;
+        F8 b = staged8<RAGGED>(st + at_b, p.branch, m, p.ld_branch, c, D);
+        const F8 hk = h_of(k, c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = post ? mul_2(t[k].v[i], both(rp)) : t[k].v[i];
+          a_x[k].v[i] = fma_2(e, b.v[i], a_x[k].v[i]);
+          b.v[i] = post ? fma_2(b.v[i], both(k2), mul_2(e, hk.v[i])) : mul_2(e, hk.v[i]);
+        }
+        store8<RAGGED>(db + c, D - c, b);
+      }
+      if (MANY && m + 1 == m1) {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          const int c = 8 * (tid + k * threads);
+          if (c >= D) continue;
+          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D), hk = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
+          float out[8];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            a_post[MANY ? k : 0].v[i] = fma_2(mul_2(g.v[i], both(p.alpha)), a_x[k].v[i], a_post[MANY ? k : 0].v[i]);
+            const float2 q = mul_2(hk.v[i], a_x[k].v[i]);
+            out[2 * i] = q.x;
+            out[2 * i + 1] = q.y;
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (c + i < D) p.dgate[grp * D + c + i] = out[i];
+          a_x[k] = zeros();
+        }
+      }
+      last = s;
+      if (p.stages == 1) {  // a row's load follows the row before it
+        row_barrier(threads);
+        if (tid == 0) load_next(0);
+        last = -1;
+      }
+      if (++s == p.stages) s = 0, parity ^= 1u;
+    }
+    if (!MANY && p.part_x) {
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = 8 * (tid + k * threads);
+        const float v[8] = {a_x[k].v[0].x, a_x[k].v[0].y, a_x[k].v[1].x, a_x[k].v[1].y, a_x[k].v[2].x, a_x[k].v[2].y, a_x[k].v[3].x, a_x[k].v[3].y};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (c + i < D) p.part_x[it * D + c + i] = v[i];
+        a_x[k] = zeros();
       }
     }
   }
 #pragma unroll
   for (int k = 0; k < V; ++k) {
-    const int c = 8 * int(threadIdx.x + k * blockDim.x);
+    const int c = 8 * (tid + k * threads);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (c + i >= D) continue;
-      if (p.w_pre) p.part_pre[int64_t(blockIdx.x) * D + c + i] = a_pre[k][i];
-      if (p.w_post) p.part_post[int64_t(blockIdx.x) * D + c + i] = a_post[k][i];
+      if (pre) p.part_pre[int64_t(blockIdx.x) * D + c + i] = (i & 1) ? a_pre[k].v[i / 2].y : a_pre[k].v[i / 2].x;
+      if (MANY && post)
+        p.part_post[int64_t(blockIdx.x) * D + c + i] = (i & 1) ? a_post[MANY ? k : 0].v[i / 2].y : a_post[MANY ? k : 0].v[i / 2].x;
     }
   }
 }
 
-// out[g, c] = sum of the n rows of `part` from row g * n on.  32 columns per
-// block, 16 threads per column, joined in a fixed order.
+// The sums over blocks and items, in a fixed order: 32 columns per block, 16
+// threads per column.  blockIdx.y: dw_pre, dw_post, then the gate rows.
 struct JoinP {
-  const float* part[3];
-  float* out[3];
-  int n[3];        // rows joined into one
-  int64_t first[3];  // first value of blockIdx.y of each
-  int64_t D;
+  const float *part_pre, *part_post, *part_x;
+  const uint16_t* gate;
+  const void* w_post;
+  float *dw_pre, *dw_post, *dgate;
+  int64_t D, ld_gate, items, pieces;
+  int blocks, w32;
+  float alpha, w_offset;
 };
 __global__ void __launch_bounds__(512) join_kernel(const JoinP p) {
-  __shared__ float s[16][33];
-  const int j = blockIdx.y >= p.first[2] ? 2 : blockIdx.y >= p.first[1] ? 1 : 0;
-  const int64_t g = blockIdx.y - p.first[j];
+  __shared__ float sh[16][33];
+  int64_t y = blockIdx.y;
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x;
+  int what = 2;  // 0: dw_pre, 1: dw_post, 2: gate row y
+  if (p.dw_pre) what = y-- == 0 ? 0 : 2;
+  if (what == 2 && p.dw_post) what = y-- == 0 ? 1 : 2;
   float v = 0.0f;
   if (c < p.D) {
-    const float* q = p.part[j] + g * p.n[j] * p.D + c;
-    for (int i = threadIdx.y; i < p.n[j]; i += 16) v += q[int64_t(i) * p.D];
+    if (what == 2) {
+      for (int64_t i = threadIdx.y; i < p.pieces; i += 16) v += p.part_x[(y * p.pieces + i) * p.D + c];
+    } else if (what == 1 && p.part_x) {
+      for (int64_t i = threadIdx.y; i < p.items; i += 16) {
+        const float x = p.part_x[i * p.D + c];
+        v = p.gate ? fmaf(bf16_of_bits(p.gate[i / p.pieces * p.ld_gate + c]), x, v) : v + x;
+      }
+    } else {
+      const float* q = what == 0 ? p.part_pre : p.part_post;
+      for (int64_t i = threadIdx.y; i < p.blocks; i += 16) v += q[i * p.D + c];
+    }
   }
-  s[threadIdx.y][threadIdx.x] = v;
+  sh[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
   if (threadIdx.y != 0 || c >= p.D) return;
   v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v += s[i][threadIdx.x];
-  p.out[j][g * p.D + c] = v;
+  for (int i = 0; i < 16; ++i) v += sh[i][threadIdx.x];
+  if (what == 0) {
+    p.dw_pre[c] = v;
+  } else if (what == 1) {
+    p.dw_post[c] = p.part_x ? p.alpha * v : v;
+  } else {
+    float w = p.alpha;
+    if (p.w_post)
+      w *= (p.w32 ? static_cast<const float*>(p.w_post)[c] : bf16_of_bits(static_cast<const uint16_t*>(p.w_post)[c])) + p.w_offset;
+    p.dgate[y * p.D + c] = w * v;
+  }
 }
 
 // The backward's split, a function of the shape alone (for GB300's 152 SMs).
 struct NormBwdPlan {
-  int V, threads, grid;
+  int V, threads, per_sm, grid;
   int64_t pieces, items;
+  bool many;
 };
 NormBwdPlan norm_bwd_plan(int64_t M, int64_t D, int64_t gates) {
   NormBwdPlan q;
   const int64_t chunks = (D + 7) / 8;
-  q.V = chunks <= 512 ? 1 : chunks <= 1024 ? 2 : 4;
-  q.threads = int(((chunks + q.V - 1) / q.V + 31) / 32 * 32);
-  const int per_sm = q.threads >= 512 ? 1 : 512 / q.threads > 8 ? 8 : 512 / q.threads;
-  const int64_t blocks = 152 * per_sm;
+  q.V = row_chunks(chunks);
+  q.threads = row_threads(chunks, q.V);
+  q.per_sm = ring_blocks(q.threads);
+  const int64_t blocks = 152 * q.per_sm;
   const int64_t groups = gates > 0 ? gates : 1, rows = M / groups;
   // parts per gate row: the choice among those of 1 to 4 items per block
   // with the fewest rows on the busiest block
@@ -324,13 +641,36 @@ NormBwdPlan norm_bwd_plan(int64_t M, int64_t D, int64_t gates) {
   }
   q.items = groups * q.pieces;
   q.grid = int(q.items < blocks ? q.items : blocks);
+  q.many = gates > 1 && q.pieces == 1;
   return q;
+}
+
+template <typename XT, int V, bool MANY>
+cudaError_t launch_bwd_v(NormBwdP p, const NormBwdPlan& q, cudaStream_t s) {
+  p.stage_bytes =
+      int(p.D / 8 * 8 * ((p.w_pre ? sizeof(XT) + 2 : 0) + (p.dr ? sizeof(XT) : 0) + (p.branch ? 2 : 0) + (MANY ? 2 : 0)));
+  p.stages = ring_stages(p.stage_bytes, q.per_sm);
+  const int smem = kCtlBytes + p.stages * p.stage_bytes;
+  if (smem > kSmemMost) return cudaErrorInvalidValue;
+  auto kern = p.D % 8 != 0 ? norm_bwd_kernel<XT, V, MANY, true> : norm_bwd_kernel<XT, V, MANY, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, q.grid, q.threads, smem, s, p);
+}
+
+template <typename XT, bool MANY>
+cudaError_t launch_bwd_t(const NormBwdP& p, const NormBwdPlan& q, cudaStream_t s) {
+  switch (q.V) {
+    case 1: return launch_bwd_v<XT, 1, MANY>(p, q, s);
+    case 2: return launch_bwd_v<XT, 2, MANY>(p, q, s);
+    default: return launch_bwd_v<XT, 4, MANY>(p, q, s);
+  }
 }
 
 }  // namespace
 
 cudaError_t launch_norm_fwd(const glu_block_norm_fwd_args& a, cudaStream_t s, const DevInfo& d) {
-  NormFwdP p;
+  NormFwdP p = {};
   p.x = a.x;
   p.branch = static_cast<const uint16_t*>(a.branch);
   p.gate = static_cast<const uint16_t*>(a.gate);
@@ -357,21 +697,12 @@ cudaError_t launch_norm_fwd(const glu_block_norm_fwd_args& a, cudaStream_t s, co
 
 size_t norm_bwd_workspace(int64_t M, int64_t D, int64_t gates) {
   const NormBwdPlan q = norm_bwd_plan(M, D, gates);
-  return size_t(D) * 4 * (2 * size_t(q.grid) + (gates > 0 && q.pieces > 1 ? size_t(q.items) : 0));
-}
-
-template <typename XT>
-static cudaError_t launch_bwd_t(const NormBwdP& p, const NormBwdPlan& q, cudaStream_t s) {
-  switch (q.V) {
-    case 1: return launch_kernel(norm_bwd_kernel<XT, 1>, q.grid, q.threads, 0, s, p);
-    case 2: return launch_kernel(norm_bwd_kernel<XT, 2>, q.grid, q.threads, 0, s, p);
-    default: return launch_kernel(norm_bwd_kernel<XT, 4>, q.grid, q.threads, 0, s, p);
-  }
+  return size_t(D) * 4 * (size_t(q.grid) + size_t(q.many ? q.grid : q.items));
 }
 
 cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s) {
   const NormBwdPlan q = norm_bwd_plan(a.M, a.D, a.gates);
-  NormBwdP p;
+  NormBwdP p = {};
   p.r = a.r;
   p.dr = a.dr;
   p.branch = static_cast<const uint16_t*>(a.branch);
@@ -384,8 +715,10 @@ cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s) {
   p.dx = a.dx;
   p.dbranch = static_cast<uint16_t*>(a.dbranch);
   p.part_pre = static_cast<float*>(a.workspace);
-  p.part_post = p.part_pre + int64_t(q.grid) * a.D;
-  p.part_gate = q.pieces > 1 ? p.part_post + int64_t(q.grid) * a.D : a.dgate;
+  float* second = p.part_pre + int64_t(q.grid) * a.D;
+  if (q.many) p.part_post = second;
+  else if (a.dw_post || a.dgate) p.part_x = second;
+  p.dgate = a.dgate;
   p.M = a.M;
   p.D = a.D;
   p.rows_per_gate = a.gates > 0 ? a.M / a.gates : a.M;
@@ -401,19 +734,38 @@ cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s) {
   p.alpha = a.alpha;
   p.w_offset = a.w_offset;
   p.w32 = a.w_fmt == GLU_FMT_FP32;
-  cudaError_t e = a.x_fmt == GLU_FMT_FP32 ? launch_bwd_t<float>(p, q, s) : launch_bwd_t<uint16_t>(p, q, s);
+  const cudaError_t e = a.x_fmt == GLU_FMT_FP32 ? (q.many ? launch_bwd_t<float, true>(p, q, s) : launch_bwd_t<float, false>(p, q, s))
+                                                : (q.many ? launch_bwd_t<uint16_t, true>(p, q, s) : launch_bwd_t<uint16_t, false>(p, q, s));
   if (e != cudaSuccess) return e;
-  JoinP j;
-  int64_t rows = 0;
-  j.part[0] = p.part_pre, j.out[0] = a.dw_pre, j.n[0] = q.grid, j.first[0] = 0;
-  rows += a.dw_pre ? 1 : 0;
-  j.part[1] = p.part_post, j.out[1] = a.dw_post, j.n[1] = q.grid, j.first[1] = rows;
-  rows += a.dw_post ? 1 : 0;
-  j.part[2] = p.part_gate, j.out[2] = a.dgate, j.n[2] = int(q.pieces), j.first[2] = rows;
-  rows += a.dgate && q.pieces > 1 ? a.gates : 0;
+  JoinP j = {};
+  j.part_pre = p.part_pre;
+  j.part_post = p.part_post;
+  j.part_x = p.part_x;
+  j.gate = p.gate;
+  j.w_post = a.w_post;
+  j.dw_pre = a.dw_pre;
+  j.dw_post = a.dw_post;
+  j.dgate = q.many ? nullptr : a.dgate;
   j.D = a.D;
+  j.ld_gate = a.ld_gate;
+  j.items = q.items;
+  j.pieces = q.pieces;
+  j.blocks = q.grid;
+  j.w32 = p.w32;
+  j.alpha = a.alpha;
+  j.w_offset = a.w_offset;
+  const int64_t rows = (a.dw_pre ? 1 : 0) + (a.dw_post ? 1 : 0) + (j.dgate ? a.gates : 0);
   if (rows == 0) return cudaSuccess;
   return launch_kernel(join_kernel, dim3(unsigned((a.D + 31) / 32), unsigned(rows)), dim3(32, 16), 0, s, j);
+}
+
+cudaError_t read_err_norm(uint32_t* v, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(v, g_err_norm, sizeof(uint32_t));
+  if (e == cudaSuccess && clear) {
+    const uint32_t z = 0;
+    e = cudaMemcpyToSymbol(g_err_norm, &z, sizeof(uint32_t));
+  }
+  return e;
 }
 
 }  // namespace gq

@@ -122,42 +122,123 @@ __device__ __forceinline__ void vec8(const void* base, bool f32, int64_t c, int 
   for (int i = 0; i < 8; ++i) v[i] += add;
 }
 
+// Eight values as pairs for the two-wide fp32 instructions.
+struct F8 {
+  float2 v[4];
+};
+__device__ __forceinline__ uint64_t pair_bits(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair_of(uint64_t r) {
+  float2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ float2 fma_2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)), "l"(pair_bits(c)));
+  return pair_of(r);
+}
+__device__ __forceinline__ float2 mul_2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(r);
+}
+__device__ __forceinline__ float2 add_2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pair_bits(a)), "l"(pair_bits(b)));
+  return pair_of(r);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+__device__ __forceinline__ F8 pairs(const float (&v)[8]) {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = make_float2(v[2 * i], v[2 * i + 1]);
+  return f;
+}
+__device__ __forceinline__ F8 zeros() {
+  F8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = make_float2(0.0f, 0.0f);
+  return f;
+}
+__device__ __forceinline__ F8 pairs(const uint4& w) {
+  F8 f;
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f.v[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
+  return f;
+}
+// RAGGED: the width may end inside the chunk (n elements of it are stored).
+template <bool RAGGED, typename T>
+__device__ __forceinline__ void store8(T* p, int n, const F8& f) {
+  const float v[8] = {f.v[0].x, f.v[0].y, f.v[1].x, f.v[1].y, f.v[2].x, f.v[2].y, f.v[3].x, f.v[3].y};
+  store8(p, RAGGED ? n : 8, v);
+}
+__device__ __forceinline__ float sum2(float2 a) { return a.x + a.y; }
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
 
-// Sums over the first `threads` threads of the block (whole warps; the others
-// do not call) of N values each, the same bits in every thread.  `buf`
-// alternates between calls (two buffers), so one barrier per call is enough:
-// a buffer is written again only after the next call's barrier.
+// Sums over the block's `threads` threads (whole warps) of N = 1 or 3 values
+// each, the same bits in every thread.  `buf` alternates between calls (two
+// buffers), so one barrier per call is enough: a buffer is written again only
+// after the next call's barrier.  Three values share the exchanges inside a
+// warp: halves of it first swap values, so that each quarter then sums one
+// (6 exchanges instead of 15, and 10 instead of 15 across up to 16 warps).
 template <int N>
 struct BlockSum {
-  float part[2][32][N];
+  float part[2][N][32];
 };
-template <int N>
-__device__ __forceinline__ void block_sum(BlockSum<N>& s, uint32_t& buf, int threads, float (&v)[N]) {
-  const int warps = threads >> 5;
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = warp_sum(v[j]);
+__device__ __forceinline__ void block_sum(BlockSum<1>& s, uint32_t& buf, int threads, float (&v)[1]) {
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
+  v[0] = warp_sum(v[0]);
   if (warps == 1) {
     __syncwarp();
     return;
   }
-  float(&p)[32][N] = s.part[buf & 1u];
+  float* q = s.part[buf & 1u][0];
   ++buf;
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int j = 0; j < N; ++j) p[threadIdx.x >> 5][j] = v[j];
-  }
+  if (lane == 0) q[threadIdx.x >> 5] = v[0];
   asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  v[0] = warp_sum(lane < warps ? q[lane] : 0.0f);
+}
+__device__ __forceinline__ void block_sum(BlockSum<3>& s, uint32_t& buf, int threads, float (&v)[3]) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int warps = threads >> 5, lane = threadIdx.x & 31;  // at most 16 warps
+  const bool hi = lane & 16, up = lane & 8;
+  float a = hi ? v[2] : v[0], b = hi ? 0.0f : v[1];
+  a += __shfl_xor_sync(kAll, hi ? v[0] : v[2], 16);
+  b += __shfl_xor_sync(kAll, hi ? v[1] : 0.0f, 16);
+  float x = (up ? b : a) + __shfl_xor_sync(kAll, up ? a : b, 8);  // lanes 0-7: v[0], 8-15: v[1], 16-23: v[2]
 #pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = 0.0f;
-  for (int w = 0; w < warps; ++w) {
+  for (int o = 4; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+  if (warps == 1) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] += p[w][j];
+    for (int j = 0; j < 3; ++j) v[j] = __shfl_sync(kAll, x, 8 * j);
+    return;
   }
+  float(&q)[3][32] = s.part[buf & 1u];
+  ++buf;
+  if ((lane & 7) == 0 && lane < 24) q[lane >> 3][threadIdx.x >> 5] = x;
+  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  const int w = lane & 15;
+  a = w < warps ? q[lane >> 4][w] : 0.0f;
+  b = w < warps ? q[2][w] : 0.0f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(kAll, a, o);
+    b += __shfl_xor_sync(kAll, b, o);
+  }
+  v[0] = __shfl_sync(kAll, a, 0);
+  v[1] = __shfl_sync(kAll, a, 16);
+  v[2] = b;
 }
 
 }  // namespace gq
