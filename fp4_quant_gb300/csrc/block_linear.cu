@@ -1,26 +1,39 @@
 // Linear layers, dense or by expert, forward and backward (glu_block.h), on
 // the tcgen05 tensor cores:
 //
-//   y  = act(x W^T + b) + residual   rows x columns = tokens x N, summed over K
-//   dx = dz W                        tokens x K, summed over N
-//   dw = dz^T x                      N x K, summed over the tokens
+//   y  = act(x W^T + b) + residual   summed over K
+//   dx = dz W                        summed over N
+//   dw = dz^T x                      summed over the tokens
 //
-// One kernel computes D[i, j] = sum_k A[i, k] B[j, k] for the three.  An
-// operand whose contiguous dimension is the summed one (x and W forward, dz
+// One kernel computes D[i, j] = sum_k A[i, k] B[j, k] for the three, in tiles
+// of 256 rows by up to 256 columns, each by a pair of CTAs (cta_group::2): a
+// CTA loads 128 rows of A and half of B's columns, and holds the accumulators
+// of its own rows.  So each SM moves 32 KB per 64-wide slice of the sum instead
+// of the 48 KB of a 128 x 256 tile of its own, and a ring of six stages fits.
+//
+// For y and dx, A is the weight and B the tokens, i.e. the tile is computed
+// transposed: the tokens are then the dimension whose size the instruction
+// leaves free (32 to 256 in steps of 32), and an expert's last rows cost what
+// they are, not a whole tile.  The accumulator's rows come back with one
+// output column per thread; quads of lanes swap 4 x 4 blocks so that each
+// stores four consecutive ones.  For dw, A is dz and B is x.
+//
+// An operand whose contiguous dimension is the summed one (x and W forward, dz
 // for dx) is loaded as a K-major tile, the others (W for dx, dz and x for
 // dw) as M/N-major ones: TMA fetches boxes of 64 contiguous elements by rows
 // in both cases, and the matrix descriptors say which way they run, so
 // nothing is transposed in memory.
 //
-// By expert the rows are cut at offsets[e]: a tile of dx or y has rows of one
-// expert (those of the next one that its box also fetched are not stored), a
-// tile of dw sums over one expert's rows (those of the next one are zeroed in
-// shared memory before the product, so that what they hold, NaN included,
-// does not count).
+// By expert the rows are cut at offsets[e]: a tile of y or dx has tokens of
+// one expert (those of the next one that its boxes also fetched are not
+// stored); a tile of dw sums over one expert's rows (those of the next one are
+// zeroed in shared memory before the product, so that what they hold, NaN
+// included, does not count).
 //
-// Ten warps per block, as the gate/up GEMM: one issues the loads into a ring
-// of stages, one the products into one of two accumulators in tensor memory,
-// eight read the other accumulator and store it.  Every wait is bounded.
+// Ten warps per CTA: one issues the loads, one (of CTA 0) the products into
+// one of two accumulators in tensor memory, eight read the other accumulator
+// and store it.  Every wait is bounded.
+#include <atomic>
 #include <cstring>
 
 #include "block.h"
@@ -31,20 +44,28 @@
 namespace gq {
 namespace {
 
-constexpr int kBM = 128, kBN = 256, kBK = 64, kStages = 4;
-constexpr int kABytes = kBM * kBK * 2, kBBytes = kBN * kBK * 2, kStageBytes = kABytes + kBBytes;
-constexpr int kBox = 64 * kBK * 2;  // one M/N-major box: 64 elements by 64 k
+constexpr int kTile = 256;           // rows of D per pair, and most columns
+constexpr int kHalf = kTile / 2;     // rows of A and most columns of B per CTA
+constexpr int kBK = 64, kStages = 6;
+constexpr int kOperand = kHalf * kBK * 2;  // 16 KB
+constexpr int kStageBytes = 2 * kOperand;
+constexpr int kBox = 64 * kBK * 2;   // one M/N-major box: 64 elements by 64 k
+constexpr int kStep = 32;            // granularity of a tile's columns
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
-constexpr uint32_t kTmemCols = 2 * kBN;
-constexpr uint32_t kIdescK = tc::idesc_bf16_f32(kBM, kBN);
+constexpr uint32_t kTmemCols = 2 * kTile;
+constexpr uint32_t kIdescK = tc::idesc_bf16_f32(kTile, 0);  // the columns are added per tile
 
 enum Product { kForward, kGradX, kGradW };
 
 struct Ctl {
-  uint64_t full[kStages], empty[kStages];
-  uint64_t tfull[2], tempty[2];
-  uint64_t done;
+  uint64_t full[kStages];   // CTA 0's: its arrival and the bytes of both CTAs
+  uint64_t empty[kStages];  // each CTA's own: the products on its stage are done
+  uint64_t tfull[2];        // each CTA's own: the accumulator is complete
+  uint64_t tempty[2];       // CTA 0's: both CTAs' warps have read it
+  uint64_t tail[kStages];   // each CTA's own: a slice to be cut short has landed
+  uint64_t other[kStages];  // CTA 0's: CTA 1 has cut its part of it
+  uint64_t done;            // each CTA's own: all products are done
   uint32_t tmem;
   int32_t cut[kMaxExperts + 1];    // first row of each expert, in range and not falling
   int32_t first[kMaxExperts + 1];  // tiles before each expert's
@@ -55,13 +76,14 @@ static_assert(kSmem <= 232448, "shared memory per CTA exceeds 227 KB");
 __device__ uint32_t g_err_linear;
 
 struct LinearP {
-  CUtensorMap ta, tb;
-  const int32_t* offsets;  // NULL: dense
-  int32_t E;               // experts (dense: 1)
-  int32_t rows;            // of x and dy
-  int32_t M, N, K;         // the product's own: D [M, N] (kForward, kGradX: M = rows), sum over K (kGradW: rows)
-  int32_t n_nt;            // column tiles of D
-  int32_t n_mt;            // row tiles of D (kGradW; dense)
+  CUtensorMap ta, tb, tb16;  // tb: boxes of 128 rows, tb16: of 16 (tiles with fewer columns)
+  const int32_t* offsets;    // NULL: dense
+  int32_t E;                 // experts (dense: 1)
+  int32_t rows;              // of x and dy
+  int32_t width;             // rows of D: N, K (kGradX) or N
+  int32_t cols;              // columns of D of a dw (K)
+  int32_t depth;             // summed over (kForward: K, kGradX: N)
+  int32_t n_at;              // tiles of 256 rows of D
   int64_t ld_out, stride_out, ld_residual, ld_z;
   uint16_t *out, *z;
   const uint16_t* residual;
@@ -84,20 +106,25 @@ __device__ __forceinline__ float act_value(int act, float z) {
 }
 
 struct Tile {
-  int32_t e, m0, n0;       // expert; first row and column of D
-  int32_t m_end;           // rows of D below this one are stored
+  int32_t e, a0;           // expert; first row of D
+  int32_t b0, b_end;       // columns of D: tokens, or columns of a dw
+  int32_t n;               // columns computed (b_end - b0 rounded up)
   int32_t k0, k_end, nk;   // summed range and its 64-wide blocks
 };
 
-// Tile t of the walk.  Dense: bands of 16 row tiles, columns inside, so that
-// the tiles at work share a band's rows of A and a few columns of B in L2.
+// `rows` tokens in equal tiles of at most 256.
+__device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kTile - 1) / kTile; }
+
+// Tile t of the walk: bands of eight row tiles of D, the columns inside, so
+// that the pairs at work share a band's rows of A and a few columns of B in
+// L2.
 template <int PROD>
 __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_t t) {
   Tile x;
   x.e = 0;
-  int32_t lo = 0, rows0 = 0, rows1 = p.rows, n_mt = p.n_mt;
+  int32_t rows0 = 0, rows1 = p.rows;
   if (p.offsets) {
-    int32_t hi = p.E - 1;  // last expert whose first tile is not after t
+    int32_t lo = 0, hi = p.E - 1;  // last expert whose first tile is not after t
     while (lo < hi) {
       const int32_t mid = (lo + hi + 1) >> 1;
       if (ctl->first[mid] <= t) lo = mid;
@@ -107,23 +134,26 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
     t -= ctl->first[lo];
     rows0 = ctl->cut[lo];
     rows1 = ctl->cut[lo + 1];
-    if (PROD != kGradW) n_mt = (rows1 - rows0 + kBM - 1) / kBM;
   }
-  constexpr int32_t kBand = 16;
-  const int32_t band = t / (kBand * p.n_nt), rem = t - band * kBand * p.n_nt;
-  const int32_t high = min(kBand, n_mt - band * kBand);
-  const int32_t nt = rem / high, mt = band * kBand + rem % high;
-  x.n0 = nt * kBN;
+  const int32_t n_bt = PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(rows1 - rows0);
+  constexpr int32_t kBand = 8;
+  const int32_t band = t / (kBand * n_bt), rem = t - band * kBand * n_bt;
+  const int32_t high = min(kBand, p.n_at - band * kBand);
+  const int32_t bt = rem / high, at = band * kBand + rem % high;
+  x.a0 = at * kTile;
   if (PROD == kGradW) {
-    x.m0 = mt * kBM;
-    x.m_end = p.M;
+    x.b0 = bt * kTile;
+    x.b_end = p.cols;
+    x.n = kTile;
     x.k0 = rows0;
     x.k_end = rows1;
   } else {
-    x.m0 = rows0 + mt * kBM;
-    x.m_end = rows1;
+    const int32_t each = ((rows1 - rows0 + n_bt - 1) / n_bt + kStep - 1) / kStep * kStep;
+    x.b0 = rows0 + bt * each;
+    x.b_end = min(rows1, x.b0 + each);
+    x.n = min(each, (x.b_end - x.b0 + kStep - 1) / kStep * kStep);
     x.k0 = 0;
-    x.k_end = p.K;
+    x.k_end = p.depth;
   }
   x.nk = (x.k_end - x.k0 + kBK - 1) / kBK;
   return x;
@@ -133,7 +163,7 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
 template <int PROD>
 __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane) {
   if (!p.offsets) {
-    if (lane == 0) ctl->first[1] = p.n_mt * p.n_nt;
+    if (lane == 0) ctl->first[1] = p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(p.rows));
     return;
   }
   int32_t row = 0, tiles = 0;
@@ -149,7 +179,7 @@ __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane)
     end = max(end, row);
     int32_t start = __shfl_up_sync(0xFFFFFFFFu, end, 1);
     if (lane == 0) start = row;
-    int32_t n = e >= p.E ? 0 : PROD == kGradW ? p.n_mt * p.n_nt : (end - start + kBM - 1) / kBM * p.n_nt;
+    int32_t n = e >= p.E ? 0 : p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(end - start));
     const int32_t own = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -169,25 +199,105 @@ __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane)
   }
 }
 
+// The 4 x 4 block that a quad of lanes holds (lane l: four 16-bit values, two
+// per word) transposed: value j of lane l becomes value l % 4 of lane j.
+__device__ __forceinline__ void quad_transpose(uint32_t& w0, uint32_t& w1, int lane) {
+  const bool odd = lane & 1, up = lane & 2;
+  const uint32_t even_half = __byte_perm(w0, w1, 0x5410), odd_half = __byte_perm(w0, w1, 0x7632);
+  const uint32_t keep = odd ? odd_half : even_half;
+  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? even_half : odd_half, 1);
+  const uint32_t first = odd ? got : keep, second = odd ? keep : got;  // of the even and the odd lane
+  const uint32_t a = __byte_perm(first, second, 0x5410), b = __byte_perm(first, second, 0x7632);
+  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 2);
+  w0 = up ? other : a;
+  w1 = up ? b : other;
+}
+
+// Four consecutive bf16 of an output row (8-byte aligned) or its first n.
+__device__ __forceinline__ void store4(uint16_t* o, int n, uint32_t w0, uint32_t w1) {
+  if (n >= 4) {
+    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(o), "r"(w0), "r"(w1) : "memory");
+  } else {
+    if (n > 0) o[0] = uint16_t(w0);
+    if (n > 1) o[1] = uint16_t(w0 >> 16);
+    if (n > 2) o[2] = uint16_t(w1);
+  }
+}
+
+// 32 tokens of y or dx (kForward, kGradX): thread `lane` has output column
+// col0 + lane of tokens token0 ..; those below token_end are stored.
 template <int PROD>
-__global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearP p) {
-  constexpr bool kAmn = PROD == kGradW, kBmn = PROD != kForward;
+__device__ __forceinline__ void store_tokens(const LinearP& p, const uint32_t (&r)[32], float bias, int32_t token0,
+                                             int32_t token_end, int32_t col0, int lane) {
+  const int32_t col = col0 + (lane & ~3), left = p.width - col;
+#pragma unroll
+  for (int q = 0; q < 32; q += 4) {
+    const int32_t m = token0 + q + (lane & 3);
+    const bool row_ok = m < token_end;
+    float v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r[q + j]);
+    if (PROD == kForward) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] += bias;
+      if (p.z) {
+        uint32_t w0 = bf16x2_of(v[0], v[1]), w1 = bf16x2_of(v[2], v[3]);
+        quad_transpose(w0, w1, lane);
+        if (row_ok) store4(p.z + int64_t(m) * p.ld_z + col, left, w0, w1);
+      }
+      if (p.act != GLU_ACT_IDENTITY) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = act_value(p.act, v[j]);
+      }
+      if (p.residual) {
+        uint32_t w0 = 0, w1 = 0;
+        if (row_ok) {
+          const uint16_t* s = p.residual + int64_t(m) * p.ld_residual + col;
+          if (left >= 4) {
+            const uint2 t = *reinterpret_cast<const uint2*>(s);
+            w0 = t.x, w1 = t.y;
+          } else {
+            if (left > 0) w0 = s[0];
+            if (left > 1) w0 |= uint32_t(s[1]) << 16;
+            if (left > 2) w1 = s[2];
+          }
+        }
+        quad_transpose(w0, w1, lane);
+        v[0] += __uint_as_float(w0 << 16);
+        v[1] += __uint_as_float(w0 & 0xFFFF0000u);
+        v[2] += __uint_as_float(w1 << 16);
+        v[3] += __uint_as_float(w1 & 0xFFFF0000u);
+      }
+    }
+    uint32_t w0 = bf16x2_of(v[0], v[1]), w1 = bf16x2_of(v[2], v[3]);
+    quad_transpose(w0, w1, lane);
+    if (row_ok) store4(p.out + int64_t(m) * p.ld_out + col, left, w0, w1);
+  }
+}
+
+template <int PROD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearP p) {
+  constexpr bool kAmn = PROD != kForward, kBmn = PROD == kGradW;
   constexpr uint32_t kIdesc = kIdescK | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(stages + kStages * kStageBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 32) {
     prefetch_tensormap(&p.ta);
     prefetch_tensormap(&p.tb);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->other[s], 1);
       mbar_init(&ctl->empty[s], 1);
+      mbar_init(&ctl->tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->tfull[b], 1);
-      mbar_init(&ctl->tempty[b], kEpiWarps);
+      mbar_init(&ctl->tempty[b], 2 * kEpiWarps);
     }
     mbar_init(&ctl->done, 1);
     fence_barrier_init();
@@ -195,11 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
   if (warp == 0) plan_tiles<PROD>(p, ctl, lane);
   if (warp == 1) {
     __syncwarp();
-    tc::tmem_alloc(&ctl->tmem, kTmemCols);
-    tc::tmem_relinquish();
+    tc::pair_alloc(&ctl->tmem, kTmemCols);
+    tc::pair_relinquish();
   }
   tc::fence_before();
-  __syncthreads();
+  cluster_sync();
   tc::fence_after();
   const uint32_t tmem = ctl->tmem;
   const int32_t tiles = ctl->first[p.offsets ? p.E : 1];
@@ -209,8 +319,10 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     if (lane == 0) {
       int64_t it = 0;
       bool ok = true;
-      for (int32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+      for (int32_t t = pair; t < tiles && ok; t += pairs) {
         const Tile x = tile_at<PROD>(p, ctl, t);
+        const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
+        const uint32_t bytes = uint32_t(kOperand + half * kBK * 2);
         for (int32_t kb = 0; kb < x.nk; ++kb, ++it) {
           const int s = int(it % kStages);
           if (!mbar_wait(&ctl->empty[s], (uint32_t(it / kStages) & 1u) ^ 1u)) {
@@ -219,85 +331,111 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
             break;
           }
           uint8_t* a = stages + s * kStageBytes;
-          uint8_t* b = a + kABytes;
-          uint64_t* bar = &ctl->full[s];
-          mbar_arrive_expect_tx(bar, kStageBytes);
+          uint8_t* b = a + kOperand;
           const int32_t k = x.k0 + kb * kBK;
-          if (kAmn) {
-            for (int i = 0; i < kBM / 64; ++i) tma_load_2d(a + i * kBox, &p.ta, x.m0 + 64 * i, k, bar);
-          } else {
-            tma_load_2d(a, &p.ta, k, x.m0, bar);
-          }
+          // a slice that another expert's rows follow lands on this CTA's own
+          // barrier, to be cut short by warp 1
+          const bool cut = PROD == kGradW && k + kBK > x.k_end;
+          const uint32_t bar = cut ? smem_u32(&ctl->tail[s]) : peer_addr(&ctl->full[s], 0);
+          if (cut) mbar_arrive_expect_tx(&ctl->tail[s], bytes);
+          else if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
           if (PROD == kForward) {
-            tma_load_3d(b, &p.tb, k, x.n0, x.e, bar);
+            pair_load_3d(a, &p.ta, k, a0, x.e, bar);
           } else if (PROD == kGradX) {
-            for (int i = 0; i < kBN / 64; ++i) tma_load_3d(b + i * kBox, &p.tb, x.n0 + 64 * i, k, x.e, bar);
+            for (int i = 0; i < kHalf / 64; ++i) pair_load_3d(a + i * kBox, &p.ta, a0 + 64 * i, k, x.e, bar);
           } else {
-            for (int i = 0; i < kBN / 64; ++i) tma_load_2d(b + i * kBox, &p.tb, x.n0 + 64 * i, k, bar);
+            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(a + i * kBox, &p.ta, a0 + 64 * i, k, bar);
+          }
+          if (PROD == kGradW) {
+            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(b + i * kBox, &p.tb, b0 + 64 * i, k, bar);
+          } else if (half == kHalf) {
+            pair_load_2d(b, &p.tb, k, b0, bar);
+          } else {
+            for (int i = 0; i < half; i += 16) pair_load_2d(b + i * kBK * 2, &p.tb16, k, b0 + i, bar);
           }
         }
       }
-      // never leave with loads in flight
+      // never leave with loads in flight: the products on the last stages
+      // (which waited for their loads) are done
       for (int64_t j = it - kStages; j < it; ++j) {
         if (j < 0) continue;
-        if (!mbar_wait(&ctl->full[j % kStages], uint32_t(j / kStages) & 1u)) atomicOr(&g_err_linear, kErrDrain);
+        if (!mbar_wait(&ctl->empty[j % kStages], uint32_t(j / kStages) & 1u)) atomicOr(&g_err_linear, kErrDrain);
       }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA --
     int64_t it = 0;
     int32_t i = 0;
+    uint32_t cuts = 0;  // bit s: parity of the next cut slice of stage s
     bool ok = true;
-    for (int32_t t = blockIdx.x; t < tiles && ok; t += gridDim.x) {
+    for (int32_t t = pair; t < tiles && ok; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
       if (x.nk == 0) continue;  // an expert without rows: the epilogue stores zeros
       const int b = i & 1;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
-      if (!ok) {
-        if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
-        break;
+      if (rank == 0) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+          break;
+        }
+        tc::fence_after();
       }
-      tc::fence_after();
-      const uint32_t d = tmem + uint32_t(b * kBN);
+      const uint32_t d = tmem + uint32_t(b * kTile);
+      const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
       for (int32_t kb = 0; kb < x.nk; ++kb, ++it) {
         const int s = int(it % kStages);
+        uint8_t* stage = stages + s * kStageBytes;
+        const int32_t have = x.k_end - x.k0 - kb * kBK;
+        if (PROD == kGradW && have < kBK) {
+          // zero the rows past this expert's: whole 128-byte rows of every box
+          // (the swizzle moves 16-byte pieces inside a row only)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
+          cuts ^= 1u << s;
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+            break;
+          }
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          const int32_t n = (kBK - have) * 8;  // 16-byte pieces per box
+          for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
+            *reinterpret_cast<uint4*>(stage + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
+          fence_proxy_async();
+          __syncwarp();
+          if (rank != 0) {
+            if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
+          } else {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], ((cuts >> s) & 1u) ^ 1u));
+            if (!ok) {
+              if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+              break;
+            }
+            if (lane == 0) mbar_arrive(&ctl->full[s]);  // both parts are there
+          }
+        }
+        if (rank != 0) continue;
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], uint32_t(it / kStages) & 1u));
         if (!ok) {
           if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
           break;
         }
-        uint8_t* stage = stages + s * kStageBytes;
-        if (PROD == kGradW) {
-          // rows past this expert's: whole 128-byte rows of every box (the
-          // swizzle moves 16-byte pieces inside a row only)
-          const int32_t have = x.k_end - x.k0 - kb * kBK;
-          if (have < kBK) {
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const int32_t n = (kBK - have) * 8;  // 16-byte pieces per box
-            for (int32_t q = lane; q < n * ((kBM + kBN) / 64); q += 32)
-              *reinterpret_cast<uint4*>(stage + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
-            fence_proxy_async();
-          }
-          __syncwarp();
-        }
         tc::fence_after();
         if (lane == 0) {
-          const uint32_t a_addr = smem_u32(stage), b_addr = a_addr + kABytes;
+          const uint32_t a_addr = smem_u32(stage), b_addr = a_addr + kOperand;
           const uint64_t ad = kAmn ? tc::sw128_mnmajor_desc(a_addr, kBox) : tc::sw128_kmajor_desc(a_addr);
           const uint64_t bd = kBmn ? tc::sw128_mnmajor_desc(b_addr, kBox) : tc::sw128_kmajor_desc(b_addr);
 #pragma unroll
           for (int k = 0; k < kBK / 16; ++k)
-            tc::mma_bf16(d, ad + k * (kAmn ? 128 : 2), bd + k * (kBmn ? 128 : 2), kIdesc, uint32_t(kb | k));
-          tc::commit(&ctl->empty[s]);
+            tc::pair_mma_bf16(d, ad + k * (kAmn ? 128 : 2), bd + k * (kBmn ? 128 : 2), idesc, uint32_t(kb | k));
+          tc::pair_commit(&ctl->empty[s]);
         }
         __syncwarp();
       }
       if (!ok) break;
-      if (lane == 0) tc::commit(&ctl->tfull[b]);
+      if (rank == 0 && lane == 0) tc::pair_commit(&ctl->tfull[b]);
       ++i;
     }
     if (lane == 0) {
-      tc::commit(&ctl->done);
+      if (rank == 0) tc::pair_commit(&ctl->done);
       if (!mbar_wait(&ctl->done, 0)) atomicOr(&g_err_linear, kErrDrain);
     }
     __syncwarp();
@@ -305,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
     // ---------------------------------------------------------- epilogue --
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     int32_t i = 0;
-    for (int32_t t = blockIdx.x; t < tiles; t += gridDim.x) {
+    for (int32_t t = pair; t < tiles; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
       const int b = i & 1;
       if (x.nk > 0) {
@@ -317,12 +455,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
         tc::fence_after();
         ++i;
       }
-      const int32_t row = x.m0 + quarter * 32 + lane;
-      const bool row_ok = row < x.m_end;
-      uint16_t* out = p.out + (PROD == kGradW ? x.e * p.stride_out : 0) + int64_t(row) * p.ld_out;
-      const uint32_t tbase = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(b * kBN);
+      const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
+      const uint32_t tbase = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(b * kTile);
+      float bias = 0.0f;
+      if (PROD == kForward && p.bias && row0 + lane < p.width) {
+        const int64_t at = int64_t(x.e) * p.width + row0 + lane;
+        bias = p.b32 ? __ldg(static_cast<const float*>(p.bias) + at) : bf16_of_bits(__ldg(static_cast<const uint16_t*>(p.bias) + at));
+      }
 #pragma unroll 1
-      for (int c = half * (kBN / 2); c < (half + 1) * (kBN / 2); c += 32) {
+      for (int c = half * 32; c < x.n; c += 64) {
         uint32_t r[32];
         if (x.nk > 0) {
           tc::ld32(tbase + uint32_t(c), r);
@@ -331,64 +472,74 @@ __global__ void __launch_bounds__(kThreads, 1) linear_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
-        const int32_t n = x.n0 + c;
-        if (!row_ok || n >= p.N) continue;
+        if (PROD != kGradW) {
+          store_tokens<PROD>(p, r, bias, x.b0 + c, x.b_end, row0, lane);
+        } else if (row0 + lane < p.width) {
+          uint16_t* out = p.out + x.e * p.stride_out + int64_t(row0 + lane) * p.ld_out + x.b0 + c;
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-          const int32_t left = p.N - n - j;
-          if (left <= 0) break;
-          float v[8];
+          for (int j = 0; j < 32; j += 8) {
+            const int32_t left = x.b_end - x.b0 - c - j;
+            if (left <= 0) break;
+            float v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[j + q]);
-          if (PROD == kForward) {
-            if (p.bias) {
-              const int64_t at = int64_t(x.e) * p.N + n + j;
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                if (q < left)
-                  v[q] += p.b32 ? __ldg(static_cast<const float*>(p.bias) + at + q)
-                                : bf16_of_bits(__ldg(static_cast<const uint16_t*>(p.bias) + at + q));
-            }
-            if (p.z) store8(p.z + int64_t(row) * p.ld_z + n + j, left, v);
-            if (p.act != GLU_ACT_IDENTITY) {
-#pragma unroll
-              for (int q = 0; q < 8; ++q) v[q] = act_value(p.act, v[q]);
-            }
-            if (p.residual) {
-              float s[8];
-              load8(p.residual + int64_t(row) * p.ld_residual + n + j, left, s);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) v[q] += s[q];
-            }
+            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[j + q]);
+            store8(out + j, left, v);
           }
-          store8(out + n + j, left, v);
         }
       }
       if (x.nk > 0) {
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->tempty[b]);
+        if (lane == 0) peer_arrive(peer_addr(&ctl->tempty[b], 0));
       }
     }
     // rows that no expert has
     if (PROD != kGradW && p.offsets) {
       const float zero[8] = {};
-      const int64_t chunks = (p.N + 7) / 8, first = ctl->cut[p.E];
+      const int64_t chunks = (p.width + 7) / 8, first = ctl->cut[p.E];
       for (int64_t q = int64_t(blockIdx.x) * kEpiWarps * 32 + threadIdx.x - 64; q < (p.rows - first) * chunks;
            q += int64_t(gridDim.x) * kEpiWarps * 32) {
         const int64_t m = first + q / chunks;
         const int32_t c = int32_t(q % chunks) * 8;
-        store8(p.out + m * p.ld_out + c, p.N - c, zero);
-        if (PROD == kForward && p.z) store8(p.z + m * p.ld_z + c, p.N - c, zero);
+        store8(p.out + m * p.ld_out + c, p.width - c, zero);
+        if (PROD == kForward && p.z) store8(p.z + m * p.ld_z + c, p.width - c, zero);
       }
     }
   }
+  __syncwarp();
   tc::fence_before();
-  __syncthreads();
+  cluster_sync();
   if (warp == 1) {
     tc::fence_after();
-    tc::tmem_dealloc(tmem, kTmemCols);
+    tc::pair_dealloc(tmem, kTmemCols);
   }
+}
+
+// Pairs that the current device runs at once: fewer than half its SMs where a
+// GPC's SMs do not all pair up, and a pair more than that would run as a
+// second wave.  Asked once per device (devices are never reconfigured).
+cudaError_t pairs_at_once(const void* kern, const DevInfo& d, int* pairs) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *pairs = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*pairs > 0) return cudaSuccess;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = 2;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(d.sms / 2 * 2));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(pairs, kern, &cfg);
+  if (e != cudaSuccess) return e;
+  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+  if (dev < 64) known[dev].store(*pairs, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 template <int PROD>
@@ -396,14 +547,16 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   auto kern = linear_kernel<PROD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  p.n_mt = (p.M + kBM - 1) / kBM;
-  p.n_nt = (p.N + kBN - 1) / kBN;
-  // by expert the device counts the tiles: no more than one row tile per
+  p.n_at = (p.width + kTile - 1) / kTile;
+  // by expert the device counts the tiles: no more than one token tile per
   // expert above the dense count
-  const int64_t most = PROD == kGradW ? int64_t(p.n_mt) * p.n_nt * p.E
-                                      : (int64_t(p.n_mt) + (p.offsets ? p.E : 0)) * p.n_nt;
-  const int grid = int(most < d.sms ? most : d.sms);
-  return launch_kernel(kern, grid, kThreads, kSmem, s, p);
+  const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
+                                      : p.n_at * ((int64_t(p.rows) + kTile - 1) / kTile + (p.offsets ? p.E : 0));
+  int pairs = 0;
+  e = pairs_at_once(reinterpret_cast<const void*>(kern), d, &pairs);
+  if (e != cudaSuccess) return e;
+  if (most < pairs) pairs = int(most);
+  return launch_kernel(kern, 2 * pairs, kThreads, kSmem, s, p);
 }
 
 // ------------------------------------------------------- dz and its sums --
@@ -542,15 +695,15 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   LinearP p;
   memset(&p, 0, sizeof p);
   const int64_t E = a.E > 0 ? a.E : 1;
-  cudaError_t e = make_tile_map(&p.ta, a.x, 2, a.K, a.M, a.ld_x * 2, kBK, kBM, 128);
-  if (e == cudaSuccess)
-    e = make_stack_map(&p.tb, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kBN);
+  cudaError_t e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kHalf);
+  if (e == cudaSuccess) e = make_tile_map(&p.tb, a.x, 2, a.K, a.M, a.ld_x * 2, kBK, kHalf, 128);
+  if (e == cudaSuccess) e = make_tile_map(&p.tb16, a.x, 2, a.K, a.M, a.ld_x * 2, kBK, 16, 128);
   if (e != cudaSuccess) return e;
   p.offsets = a.E > 0 ? a.offsets : nullptr;
   p.E = int32_t(E);
-  p.rows = p.M = int32_t(a.M);
-  p.N = int32_t(a.N);
-  p.K = int32_t(a.K);
+  p.rows = int32_t(a.M);
+  p.width = int32_t(a.N);
+  p.depth = int32_t(a.K);
   p.out = static_cast<uint16_t*>(a.y);
   p.ld_out = a.ld_y;
   p.z = static_cast<uint16_t*>(a.z);
@@ -599,13 +752,12 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
   p.E = int32_t(E);
   p.rows = int32_t(a.M);
   if (a.dx) {
-    e = make_tile_map(&p.ta, dz, 2, a.N, a.M, ld_dz * 2, kBK, kBM, 128);
-    if (e == cudaSuccess)
-      e = make_stack_map(&p.tb, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kBK);
+    e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kBK);
+    if (e == cudaSuccess) e = make_tile_map(&p.tb, dz, 2, a.N, a.M, ld_dz * 2, kBK, kHalf, 128);
+    if (e == cudaSuccess) e = make_tile_map(&p.tb16, dz, 2, a.N, a.M, ld_dz * 2, kBK, 16, 128);
     if (e != cudaSuccess) return e;
-    p.M = int32_t(a.M);
-    p.N = int32_t(a.K);
-    p.K = int32_t(a.N);
+    p.width = int32_t(a.K);
+    p.depth = int32_t(a.N);
     p.out = static_cast<uint16_t*>(a.dx);
     p.ld_out = a.ld_dx;
     e = launch_t<kGradX>(p, s, d);
@@ -615,9 +767,8 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     e = make_tile_map(&p.ta, dz, 2, a.N, a.M, ld_dz * 2, 64, kBK, 128);
     if (e == cudaSuccess) e = make_tile_map(&p.tb, a.x, 2, a.K, a.M, a.ld_x * 2, 64, kBK, 128);
     if (e != cudaSuccess) return e;
-    p.M = int32_t(a.N);
-    p.N = int32_t(a.K);
-    p.K = int32_t(a.M);
+    p.width = int32_t(a.N);
+    p.cols = int32_t(a.K);
     p.out = static_cast<uint16_t*>(a.dw);
     p.ld_out = a.ld_dw;
     p.stride_out = a.stride_dw;
