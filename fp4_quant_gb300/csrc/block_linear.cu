@@ -76,7 +76,7 @@ static_assert(kSmem <= 232448, "shared memory per CTA exceeds 227 KB");
 __device__ uint32_t g_err_linear;
 
 struct LinearP {
-  CUtensorMap ta, tb, tb16;  // tb: boxes of 128 rows, tb16: of 16 (tiles with fewer columns)
+  CUtensorMap ta, tb[3];     // tb[i]: boxes of 128 >> i rows, for tiles with fewer columns
   const int32_t* offsets;    // NULL: dense
   int32_t E;                 // experts (dense: 1)
   int32_t rows;              // of x and dy
@@ -88,21 +88,33 @@ struct LinearP {
   uint16_t *out, *z;
   const uint16_t* residual;
   const void* bias;
-  int32_t b32, act;
+  int32_t b32;
 };
 
+// The normal distribution function, from Abramowitz and Stegun's formula
+// 7.1.26 for erf (absolute error below 1.5e-7): with v = |z| / sqrt 2 and t = 1
+// / (1 + 0.3275911 v), 1 - Phi(|z|) = t (a1 + t (a2 + ...)) exp(-v^2) / 2.
+__device__ __forceinline__ float normal_cdf(float z, float exp_half_sq) {
+  const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q = 0.5f * q * t * exp_half_sq;
+  return z < 0.0f ? q : 1.0f - q;
+}
+
 // act(z), for values that are rounded to bf16 next.
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case GLU_ACT_SILU: return __fdividef(z, 1.0f + __expf(-z));
-    case GLU_ACT_GELU_TANH: {
-      const float u = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);  // 2 sqrt(2 / pi) (z + 0.044715 z^3)
-      return __fdividef(z, 1.0f + __expf(-u));                              // z sigmoid(u) = z (1 + tanh(u / 2)) / 2
-    }
-    case GLU_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case GLU_ACT_GELU_ERF: return z * normcdff(z);
-    default: return z;
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if (ACT == GLU_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
+  if (ACT == GLU_ACT_GELU_TANH) {
+    const float u = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);  // 2 sqrt(2 / pi) (z + 0.044715 z^3)
+    return __fdividef(z, 1.0f + __expf(-u));                              // z sigmoid(u) = z (1 + tanh(u / 2)) / 2
   }
+  if (ACT == GLU_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
+  if (ACT == GLU_ACT_GELU_ERF) return z * normal_cdf(z, __expf(-0.5f * z * z));
+  return z;
 }
 
 struct Tile {
@@ -199,83 +211,96 @@ __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane)
   }
 }
 
-// The 4 x 4 block that a quad of lanes holds (lane l: four 16-bit values, two
-// per word) transposed: value j of lane l becomes value l % 4 of lane j.
-__device__ __forceinline__ void quad_transpose(uint32_t& w0, uint32_t& w1, int lane) {
+// Four 16-bit values per lane (two per word) of N independent 4 x 4 blocks,
+// each held by a quad of lanes, transposed: value j of lane l becomes value l %
+// 4 of lane j.  The blocks go through the exchanges together, so that their
+// latencies overlap.
+template <int N>
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[N][2], int lane) {
   const bool odd = lane & 1, up = lane & 2;
-  const uint32_t even_half = __byte_perm(w0, w1, 0x5410), odd_half = __byte_perm(w0, w1, 0x7632);
-  const uint32_t keep = odd ? odd_half : even_half;
-  const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? even_half : odd_half, 1);
-  const uint32_t first = odd ? got : keep, second = odd ? keep : got;  // of the even and the odd lane
-  const uint32_t a = __byte_perm(first, second, 0x5410), b = __byte_perm(first, second, 0x7632);
-  const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 2);
-  w0 = up ? other : a;
-  w1 = up ? b : other;
+  uint32_t keep[N], got[N];
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const uint32_t even_half = __byte_perm(w[q][0], w[q][1], 0x5410), odd_half = __byte_perm(w[q][0], w[q][1], 0x7632);
+    keep[q] = odd ? odd_half : even_half;
+    got[q] = __shfl_xor_sync(0xFFFFFFFFu, odd ? even_half : odd_half, 1);
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    const uint32_t first = odd ? got[q] : keep[q], second = odd ? keep[q] : got[q];  // of the even and the odd lane
+    const uint32_t a = __byte_perm(first, second, 0x5410), b = __byte_perm(first, second, 0x7632);
+    keep[q] = up ? b : a;
+    got[q] = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 2);
+  }
+#pragma unroll
+  for (int q = 0; q < N; ++q) {
+    w[q][0] = up ? got[q] : keep[q];
+    w[q][1] = up ? keep[q] : got[q];
+  }
 }
 
-// Four consecutive bf16 of an output row (8-byte aligned) or its first n.
-__device__ __forceinline__ void store4(uint16_t* o, int n, uint32_t w0, uint32_t w1) {
+// Four consecutive bf16 of an output row (8-byte aligned), or its first n.
+__device__ __forceinline__ void store4(uint16_t* o, int n, const uint32_t (&w)[2]) {
   if (n >= 4) {
-    asm volatile("st.global.v2.u32 [%0], {%1, %2};" ::"l"(o), "r"(w0), "r"(w1) : "memory");
+    *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
   } else {
-    if (n > 0) o[0] = uint16_t(w0);
-    if (n > 1) o[1] = uint16_t(w0 >> 16);
-    if (n > 2) o[2] = uint16_t(w1);
+    if (n > 0) o[0] = uint16_t(w[0]);
+    if (n > 1) o[1] = uint16_t(w[0] >> 16);
+    if (n > 2) o[2] = uint16_t(w[1]);
   }
 }
 
-// 32 tokens of y or dx (kForward, kGradX): thread `lane` has output column
-// col0 + lane of tokens token0 ..; those below token_end are stored.
-template <int PROD>
-__device__ __forceinline__ void store_tokens(const LinearP& p, const uint32_t (&r)[32], float bias, int32_t token0,
-                                             int32_t token_end, int32_t col0, int lane) {
-  const int32_t col = col0 + (lane & ~3), left = p.width - col;
+// Where a warp's 32 tokens of y, z or the residual begin: the lane's token of
+// each quad, and its four columns.
+struct TokenView {
+  int32_t left;  // of the row from the lane's first column on
+  int32_t rows;  // of the tokens from the lane's first one on
+};
+__device__ __forceinline__ void store_quads(uint16_t* o, int64_t ld, const TokenView& t, uint32_t (&w)[8][2], int lane) {
+  quad_transpose(w, lane);
 #pragma unroll
-  for (int q = 0; q < 32; q += 4) {
-    const int32_t m = token0 + q + (lane & 3);
-    const bool row_ok = m < token_end;
-    float v[4];
+  for (int q = 0; q < 8; ++q)
+    if (4 * q < t.rows) store4(o + 4 * q * ld, t.left, w[q]);
+}
+__device__ __forceinline__ void load_quads(const uint16_t* s, int64_t ld, const TokenView& t, uint32_t (&w)[8][2]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(r[q + j]);
-    if (PROD == kForward) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] += bias;
-      if (p.z) {
-        uint32_t w0 = bf16x2_of(v[0], v[1]), w1 = bf16x2_of(v[2], v[3]);
-        quad_transpose(w0, w1, lane);
-        if (row_ok) store4(p.z + int64_t(m) * p.ld_z + col, left, w0, w1);
-      }
-      if (p.act != GLU_ACT_IDENTITY) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = act_value(p.act, v[j]);
-      }
-      if (p.residual) {
-        uint32_t w0 = 0, w1 = 0;
-        if (row_ok) {
-          const uint16_t* s = p.residual + int64_t(m) * p.ld_residual + col;
-          if (left >= 4) {
-            const uint2 t = *reinterpret_cast<const uint2*>(s);
-            w0 = t.x, w1 = t.y;
-          } else {
-            if (left > 0) w0 = s[0];
-            if (left > 1) w0 |= uint32_t(s[1]) << 16;
-            if (left > 2) w1 = s[2];
-          }
-        }
-        quad_transpose(w0, w1, lane);
-        v[0] += __uint_as_float(w0 << 16);
-        v[1] += __uint_as_float(w0 & 0xFFFF0000u);
-        v[2] += __uint_as_float(w1 << 16);
-        v[3] += __uint_as_float(w1 & 0xFFFF0000u);
-      }
+  for (int q = 0; q < 8; ++q) {
+    w[q][0] = w[q][1] = 0;
+    if (4 * q >= t.rows) continue;
+    const uint16_t* v = s + 4 * q * ld;
+    if (t.left >= 4) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(v));
+      w[q][0] = x.x, w[q][1] = x.y;
+    } else {
+      if (t.left > 0) w[q][0] = v[0];
+      if (t.left > 1) w[q][0] |= uint32_t(v[1]) << 16;
+      if (t.left > 2) w[q][1] = v[2];
     }
-    uint32_t w0 = bf16x2_of(v[0], v[1]), w1 = bf16x2_of(v[2], v[3]);
-    quad_transpose(w0, w1, lane);
-    if (row_ok) store4(p.out + int64_t(m) * p.ld_out + col, left, w0, w1);
   }
 }
 
-template <int PROD>
+// The 4 x 4 block of 16-byte pieces that a quad of lanes holds (lane l: pieces
+// 0 .. 3 of a row in w[0..3], w[4..7], ...) transposed: lane l then has piece l
+// % 4 of the quad's four rows.
+__device__ __forceinline__ void piece_transpose(uint32_t (&w)[16], int lane) {
+  const bool odd = lane & 1, up = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // pieces 0, 1 and 2, 3 between neighbours
+    const int lo = (i / 4) * 8 + i % 4, hi = lo + 4;
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[lo] : w[hi], 1);
+    if (odd) w[lo] = got;
+    else w[hi] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {  // pieces 0, 2 and 1, 3 between pairs
+    const int lo = i, hi = i + 8;
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[lo] : w[hi], 2);
+    if (up) w[lo] = got;
+    else w[hi] = got;
+  }
+}
+
+template <int PROD, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearP p) {
   constexpr bool kAmn = PROD != kForward, kBmn = PROD == kGradW;
   constexpr uint32_t kIdesc = kIdescK | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
@@ -288,7 +313,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 
   if (threadIdx.x == 32) {
     prefetch_tensormap(&p.ta);
-    prefetch_tensormap(&p.tb);
+    prefetch_tensormap(&p.tb[0]);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->other[s], 1);
@@ -322,7 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       for (int32_t t = pair; t < tiles && ok; t += pairs) {
         const Tile x = tile_at<PROD>(p, ctl, t);
         const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
-        const uint32_t bytes = uint32_t(kOperand + half * kBK * 2);
+        // the smallest box with the half's columns (more than it needs are not
+        // multiplied)
+        const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
+        const uint32_t bytes = uint32_t(kOperand + (kHalf >> box) * kBK * 2);
         for (int32_t kb = 0; kb < x.nk; ++kb, ++it) {
           const int s = int(it % kStages);
           if (!mbar_wait(&ctl->empty[s], (uint32_t(it / kStages) & 1u) ^ 1u)) {
@@ -347,11 +375,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
             for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(a + i * kBox, &p.ta, a0 + 64 * i, k, bar);
           }
           if (PROD == kGradW) {
-            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(b + i * kBox, &p.tb, b0 + 64 * i, k, bar);
-          } else if (half == kHalf) {
-            pair_load_2d(b, &p.tb, k, b0, bar);
+            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(b + i * kBox, &p.tb[0], b0 + 64 * i, k, bar);
           } else {
-            for (int i = 0; i < half; i += 16) pair_load_2d(b + i * kBK * 2, &p.tb16, k, b0 + i, bar);
+            pair_load_2d(b, &p.tb[box], k, b0, bar);
           }
         }
       }
@@ -465,6 +491,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 #pragma unroll 1
       for (int c = half * 32; c < x.n; c += 64) {
         uint32_t r[32];
+        // y and dx: this lane has column row0 + lane of 32 tokens in r, and
+        // after the transposition four columns of every fourth token
+        const int32_t token = x.b0 + c + (lane & 3), col = row0 + (lane & ~3);
+        const TokenView view = {p.width - col, x.b_end - token};
+        uint32_t res[8][2];
+        if (PROD == kForward && p.residual)
+          load_quads(p.residual + int64_t(token) * p.ld_residual + col, p.ld_residual, view, res);
         if (x.nk > 0) {
           tc::ld32(tbase + uint32_t(c), r);
           tc::wait_ld();
@@ -473,18 +506,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
         if (PROD != kGradW) {
-          store_tokens<PROD>(p, r, bias, x.b0 + c, x.b_end, row0, lane);
-        } else if (row0 + lane < p.width) {
-          uint16_t* out = p.out + x.e * p.stride_out + int64_t(row0 + lane) * p.ld_out + x.b0 + c;
+          uint32_t w[8][2];
+          if (PROD == kForward) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 8) {
-            const int32_t left = x.b_end - x.b0 - c - j;
-            if (left <= 0) break;
-            float v[8];
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) + bias);
+            if (p.z) {
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = __uint_as_float(r[j + q]);
-            store8(out + j, left, v);
+              for (int q = 0; q < 8; ++q) {
+                w[q][0] = bf16x2_of(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]));
+                w[q][1] = bf16x2_of(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+              }
+              store_quads(p.z + int64_t(token) * p.ld_z + col, p.ld_z, view, w, lane);
+            }
+            if (ACT != GLU_ACT_IDENTITY) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(act_value<ACT>(__uint_as_float(r[j])));
+            }
+            if (p.residual) {
+              quad_transpose(res, lane);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t v = res[j / 4][(j / 2) & 1];
+                r[j] = __float_as_uint(__uint_as_float(r[j]) + __uint_as_float((j & 1) ? (v & 0xFFFF0000u) : (v << 16)));
+              }
+            }
           }
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            w[q][0] = bf16x2_of(__uint_as_float(r[4 * q]), __uint_as_float(r[4 * q + 1]));
+            w[q][1] = bf16x2_of(__uint_as_float(r[4 * q + 2]), __uint_as_float(r[4 * q + 3]));
+          }
+          store_quads(p.out + int64_t(token) * p.ld_out + col, p.ld_out, view, w, lane);
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = bf16x2_of(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+          piece_transpose(w, lane);
+          const int32_t row = row0 + (lane & ~3), left = x.b_end - x.b0 - c - 8 * (lane & 3);
+          uint16_t* out = p.out + x.e * p.stride_out + int64_t(row) * p.ld_out + x.b0 + c + 8 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (row + j < p.width && left > 0)
+              put8(out + j * p.ld_out, left, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
         }
       }
       if (x.nk > 0) {
@@ -542,9 +605,9 @@ cudaError_t pairs_at_once(const void* kern, const DevInfo& d, int* pairs) {
   return cudaSuccess;
 }
 
-template <int PROD>
+template <int PROD, int ACT>
 cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
-  auto kern = linear_kernel<PROD>;
+  auto kern = linear_kernel<PROD, ACT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   p.n_at = (p.width + kTile - 1) / kTile;
@@ -570,26 +633,28 @@ struct DzP {
   float* db;
   const int32_t* offsets;
   int64_t ld_dy, ld_z, ld_dz;
-  int32_t rows, N, E, act, slots;
+  int32_t rows, N, E, slots;
 };
 
-__device__ __forceinline__ float act_grad(int act, float z) {
-  switch (act) {
-    case GLU_ACT_SILU: {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-z)), q = __fdividef(1.0f, 1.0f + __expf(z));
-      return s * fmaf(z, q, 1.0f);
-    }
-    case GLU_ACT_GELU_TANH: {
-      const float z2 = z * z;
-      const float u = 1.5957691216057308f * fmaf(0.044715f * z2, z, z);
-      const float du = 1.5957691216057308f * fmaf(0.134145f, z2, 1.0f);
-      const float s = __fdividef(1.0f, 1.0f + __expf(-u)), q = __fdividef(1.0f, 1.0f + __expf(u));
-      return s * fmaf(z * q, du, 1.0f);
-    }
-    case GLU_ACT_RELU: return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    case GLU_ACT_GELU_ERF: return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z), normcdff(z));
-    default: return 1.0f;
+template <int ACT>
+__device__ __forceinline__ float act_grad(float z) {
+  if (ACT == GLU_ACT_SILU) {
+    const float s = __fdividef(1.0f, 1.0f + __expf(-z)), q = __fdividef(1.0f, 1.0f + __expf(z));
+    return s * fmaf(z, q, 1.0f);
   }
+  if (ACT == GLU_ACT_GELU_TANH) {
+    const float z2 = z * z;
+    const float u = 1.5957691216057308f * fmaf(0.044715f * z2, z, z);
+    const float du = 1.5957691216057308f * fmaf(0.134145f, z2, 1.0f);
+    const float s = __fdividef(1.0f, 1.0f + __expf(-u)), q = __fdividef(1.0f, 1.0f + __expf(u));
+    return s * fmaf(z * q, du, 1.0f);
+  }
+  if (ACT == GLU_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if (ACT == GLU_ACT_GELU_ERF) {
+    const float e = __expf(-0.5f * z * z);
+    return fmaf(z * 0.3989422804014327f, e, normal_cdf(z, e));
+  }
+  return 1.0f;
 }
 
 __device__ __forceinline__ int32_t cut_at(const int32_t* offsets, int32_t e, int32_t rows) {
@@ -597,9 +662,16 @@ __device__ __forceinline__ int32_t cut_at(const int32_t* offsets, int32_t e, int
 }
 
 // Slots of the sums: expert e has those from floor(cut[e] / kDzRows) + e on,
-// enough for its rows in parts of kDzRows.  One block per slot and 512
-// columns; a thread has two columns of a part's rows.
+// enough for its rows in parts of kDzRows.  One block per slot and 256
+// columns: 32 threads of eight columns each by eight rows at a time, four
+// rows' loads in flight per thread; the eight sums of a column are joined in
+// a fixed order.  Bound by DRAM: dy and z read, dz written, 6 bytes per
+// element.
+constexpr int kDzCols = 256, kDzDeep = 4;
+
+template <int ACT>
 __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
+  __shared__ float sh[8][kDzCols + 8];
   const int32_t slot = blockIdx.x;
   int32_t e = 0, r0 = 0, r1 = p.rows, part = slot;
   if (p.offsets) {
@@ -616,43 +688,45 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
   }
   const int32_t m0 = r0 + part * kDzRows, m1 = min(r1, m0 + kDzRows);
   if (part < 0 || m0 >= m1) return;
-  const int32_t c = blockIdx.y * 512 + 2 * threadIdx.x;
-  if (c >= p.N) return;
-  const bool two = c + 1 < p.N;
-  float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 4
-  for (int32_t m = m0; m < m1; ++m) {
-    float a, b = 0.0f;
-    const uint16_t* q = p.dy + m * p.ld_dy + c;
-    if (two) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(q);
-      a = __uint_as_float(w << 16);
-      b = __uint_as_float(w & 0xFFFF0000u);
-    } else {
-      a = bf16_of_bits(*q);
-    }
-    if (p.act != GLU_ACT_IDENTITY) {
-      const uint16_t* zq = p.z + m * p.ld_z + c;
-      if (two) {
-        const uint32_t w = *reinterpret_cast<const uint32_t*>(zq);
-        a *= act_grad(p.act, __uint_as_float(w << 16));
-        b *= act_grad(p.act, __uint_as_float(w & 0xFFFF0000u));
-      } else {
-        a *= act_grad(p.act, bf16_of_bits(*zq));
+  const int32_t c = blockIdx.y * kDzCols + 8 * threadIdx.x, left = p.N - c;
+  F8 sum = zeros();
+  if (left > 0) {
+    for (int32_t m = m0 + threadIdx.y; m < m1; m += 8 * kDzDeep) {
+      uint4 a[kDzDeep], z[kDzDeep];
+#pragma unroll
+      for (int i = 0; i < kDzDeep; ++i) {
+        const int64_t row = m + 8 * i;
+        if (row >= m1) continue;
+        a[i] = raw8(p.dy + row * p.ld_dy + c, left);
+        if (ACT != GLU_ACT_IDENTITY) z[i] = raw8(p.z + row * p.ld_z + c, left);
+      }
+#pragma unroll
+      for (int i = 0; i < kDzDeep; ++i) {
+        const int64_t row = m + 8 * i;
+        if (row >= m1) continue;
+        F8 d = pairs(a[i]);
+        if (ACT != GLU_ACT_IDENTITY) {
+          const F8 v = pairs(z[i]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) d.v[q] = mul_2(d.v[q], make_float2(act_grad<ACT>(v.v[q].x), act_grad<ACT>(v.v[q].y)));
+          // kept in L2: the products read it next
+          if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.ld_dz + c) = packed(d);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) sum.v[q] = add_2(sum.v[q], d.v[q]);
       }
     }
-    if (p.dz) {
-      uint16_t* o = p.dz + m * p.ld_dz + c;
-      if (two) *reinterpret_cast<uint32_t*>(o) = bf16x2_of(a, b);
-      else *o = bits_of_bf16(a);
-    }
-    s0 += a;
-    s1 += b;
   }
-  if (p.part) {
-    p.part[int64_t(slot) * p.N + c] = s0;
-    if (two) p.part[int64_t(slot) * p.N + c + 1] = s1;
-  }
+  if (!p.part) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) *reinterpret_cast<float2*>(&sh[threadIdx.y][8 * threadIdx.x + 2 * q]) = sum.v[q];
+  __syncthreads();
+  const int32_t t = threadIdx.y * 32 + threadIdx.x, col = blockIdx.y * kDzCols + t;
+  if (col >= p.N) return;
+  float v = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v += sh[i][t];
+  p.part[int64_t(slot) * p.N + col] = v;
 }
 
 // db[e] from the slots of expert e.
@@ -691,13 +765,28 @@ size_t linear_bwd_workspace(const glu_block_linear_bwd_args& a) {
   return dz_bytes(a) + (a.db ? size_t(dz_slots(a)) * a.N * 4 : 0);
 }
 
+static cudaError_t launch_dz(int act, const DzP& q, cudaStream_t s) {
+  auto kern = act == GLU_ACT_SILU        ? dz_kernel<GLU_ACT_SILU>
+              : act == GLU_ACT_GELU_TANH ? dz_kernel<GLU_ACT_GELU_TANH>
+              : act == GLU_ACT_RELU      ? dz_kernel<GLU_ACT_RELU>
+              : act == GLU_ACT_GELU_ERF  ? dz_kernel<GLU_ACT_GELU_ERF>
+                                         : dz_kernel<GLU_ACT_IDENTITY>;
+  return launch_kernel(kern, dim3(unsigned(q.slots), unsigned((q.N + kDzCols - 1) / kDzCols)), dim3(32, 8), 0, s, q);
+}
+
+// Maps of the tokens' rows (64-wide slices), in boxes of 128, 64 and 32 rows.
+static cudaError_t token_maps(LinearP& p, const void* t, int64_t cols, int64_t rows, int64_t ld) {
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = make_tile_map(&p.tb[i], t, 2, cols, rows, ld * 2, kBK, kHalf >> i, 128);
+  return e;
+}
+
 cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s, const DevInfo& d) {
   LinearP p;
   memset(&p, 0, sizeof p);
   const int64_t E = a.E > 0 ? a.E : 1;
   cudaError_t e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kHalf);
-  if (e == cudaSuccess) e = make_tile_map(&p.tb, a.x, 2, a.K, a.M, a.ld_x * 2, kBK, kHalf, 128);
-  if (e == cudaSuccess) e = make_tile_map(&p.tb16, a.x, 2, a.K, a.M, a.ld_x * 2, kBK, 16, 128);
+  if (e == cudaSuccess) e = token_maps(p, a.x, a.K, a.M, a.ld_x);
   if (e != cudaSuccess) return e;
   p.offsets = a.E > 0 ? a.offsets : nullptr;
   p.E = int32_t(E);
@@ -712,8 +801,13 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   p.ld_residual = a.ld_residual;
   p.bias = a.bias;
   p.b32 = a.b_fmt == GLU_FMT_FP32;
-  p.act = a.act;
-  return launch_t<kForward>(p, s, d);
+  switch (a.act) {
+    case GLU_ACT_SILU: return launch_t<kForward, GLU_ACT_SILU>(p, s, d);
+    case GLU_ACT_GELU_TANH: return launch_t<kForward, GLU_ACT_GELU_TANH>(p, s, d);
+    case GLU_ACT_RELU: return launch_t<kForward, GLU_ACT_RELU>(p, s, d);
+    case GLU_ACT_GELU_ERF: return launch_t<kForward, GLU_ACT_GELU_ERF>(p, s, d);
+    default: return launch_t<kForward, GLU_ACT_IDENTITY>(p, s, d);
+  }
 }
 
 cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s, const DevInfo& d) {
@@ -736,9 +830,8 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     q.rows = int32_t(a.M);
     q.N = int32_t(a.N);
     q.E = int32_t(E);
-    q.act = a.act;
     q.slots = int32_t(dz_slots(a));
-    e = launch_kernel(dz_kernel, dim3(unsigned(q.slots), unsigned((a.N + 511) / 512)), 256, 0, s, q);
+    e = launch_dz(a.act, q, s);
     if (e != cudaSuccess) return e;
     if (a.db) {
       e = launch_kernel(db_kernel, dim3(unsigned((a.N + 31) / 32), unsigned(E)), dim3(32, 16), 0, s, q);
@@ -753,26 +846,25 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
   p.rows = int32_t(a.M);
   if (a.dx) {
     e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kBK);
-    if (e == cudaSuccess) e = make_tile_map(&p.tb, dz, 2, a.N, a.M, ld_dz * 2, kBK, kHalf, 128);
-    if (e == cudaSuccess) e = make_tile_map(&p.tb16, dz, 2, a.N, a.M, ld_dz * 2, kBK, 16, 128);
+    if (e == cudaSuccess) e = token_maps(p, dz, a.N, a.M, ld_dz);
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.K);
     p.depth = int32_t(a.N);
     p.out = static_cast<uint16_t*>(a.dx);
     p.ld_out = a.ld_dx;
-    e = launch_t<kGradX>(p, s, d);
+    e = launch_t<kGradX, GLU_ACT_IDENTITY>(p, s, d);
     if (e != cudaSuccess) return e;
   }
   if (a.dw) {
     e = make_tile_map(&p.ta, dz, 2, a.N, a.M, ld_dz * 2, 64, kBK, 128);
-    if (e == cudaSuccess) e = make_tile_map(&p.tb, a.x, 2, a.K, a.M, a.ld_x * 2, 64, kBK, 128);
+    if (e == cudaSuccess) e = make_tile_map(&p.tb[0], a.x, 2, a.K, a.M, a.ld_x * 2, 64, kBK, 128);
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.N);
     p.cols = int32_t(a.K);
     p.out = static_cast<uint16_t*>(a.dw);
     p.ld_out = a.ld_dw;
     p.stride_out = a.stride_dw;
-    e = launch_t<kGradW>(p, s, d);
+    e = launch_t<kGradW, GLU_ACT_IDENTITY>(p, s, d);
   }
   return e;
 }

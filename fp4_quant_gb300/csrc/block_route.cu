@@ -147,17 +147,6 @@ struct RowsP {
 
 constexpr int kRowWarps = 8;
 
-__device__ __forceinline__ void put8(uint16_t* o, int n, const uint4& v) {
-  if (n >= 8) {
-    stg_once(o, v);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) o[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
 // Zero rows of the places that no assignment has; warp `wid` of `warps`.
 __device__ __forceinline__ void zero_rows(const RowsP& p, int64_t wid, int64_t warps) {
   const int lane = threadIdx.x & 31;

@@ -102,6 +102,18 @@ __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
   }
 }
 
+// The first n (up to 8) of eight bf16 as they are.
+__device__ __forceinline__ void put8(uint16_t* o, int n, const uint4& v) {
+  if (n >= 8) {
+    stg_once(o, v);
+  } else {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) o[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
 // Eight elements of a vector operand (bf16 or fp32, 16-byte aligned base) from
 // element c on, kept in L1; `add` is added to each.
 __device__ __forceinline__ void vec8(const void* base, bool f32, int64_t c, int n, float add, float (&v)[8]) {
@@ -171,6 +183,10 @@ __device__ __forceinline__ F8 pairs(const uint4& w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) f.v[i] = make_float2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xFFFF0000u));
   return f;
+}
+__device__ __forceinline__ uint4 packed(const F8& f) {
+  return make_uint4(bf16x2_of(f.v[0].x, f.v[0].y), bf16x2_of(f.v[1].x, f.v[1].y), bf16x2_of(f.v[2].x, f.v[2].y),
+                    bf16x2_of(f.v[3].x, f.v[3].y));
 }
 // RAGGED: the width may end inside the chunk (n elements of it are stored).
 template <bool RAGGED, typename T>
