@@ -342,7 +342,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
   if (warp == 0) {
     // ---------------------------------------------------------- producer --
     if (lane == 0) {
-      int64_t it = 0;
+      // one thread's latency per stage counts here and in the issuing warp:
+      // stage and parity are counted, addresses formed once
+      int s = 0, held = 0;  // held: stages ever filled, up to all
+      uint32_t parity = 0;
+      const uint32_t full0 = peer_addr(&ctl->full[0], 0);
       bool ok = true;
       for (int32_t t = pair; t < tiles && ok; t += pairs) {
         const Tile x = tile_at<PROD>(p, ctl, t);
@@ -351,20 +355,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
         // multiplied)
         const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
         const uint32_t bytes = uint32_t(kOperand + (kHalf >> box) * kBK * 2);
-        for (int32_t kb = 0; kb < x.nk; ++kb, ++it) {
-          const int s = int(it % kStages);
-          if (!mbar_wait(&ctl->empty[s], (uint32_t(it / kStages) & 1u) ^ 1u)) {
+        for (int32_t k = x.k0; k < x.k_end; k += kBK) {
+          if (!mbar_wait(&ctl->empty[s], parity ^ 1u)) {
             atomicOr(&g_err_linear, kErrWaitEmpty);
             ok = false;
             break;
           }
           uint8_t* a = stages + s * kStageBytes;
           uint8_t* b = a + kOperand;
-          const int32_t k = x.k0 + kb * kBK;
           // a slice that another expert's rows follow lands on this CTA's own
           // barrier, to be cut short by warp 1
           const bool cut = PROD == kGradW && k + kBK > x.k_end;
-          const uint32_t bar = cut ? smem_u32(&ctl->tail[s]) : peer_addr(&ctl->full[s], 0);
+          const uint32_t bar = cut ? smem_u32(&ctl->tail[s]) : full0 + 8u * uint32_t(s);
           if (cut) mbar_arrive_expect_tx(&ctl->tail[s], bytes);
           else if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
           if (PROD == kForward) {
@@ -379,19 +381,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
           } else {
             pair_load_2d(b, &p.tb[box], k, b0, bar);
           }
+          held = max(held, s + 1);
+          if (++s == kStages) s = 0, parity ^= 1u;
         }
       }
-      // never leave with loads in flight: the products on the last stages
-      // (which waited for their loads) are done
-      for (int64_t j = it - kStages; j < it; ++j) {
-        if (j < 0) continue;
-        if (!mbar_wait(&ctl->empty[j % kStages], uint32_t(j / kStages) & 1u)) atomicOr(&g_err_linear, kErrDrain);
+      // never leave with loads in flight: the products on each stage's last
+      // slice (which waited for its loads) are done
+      if (s == held) s = 0, parity ^= 1u;
+      for (int j = 0; j < held; ++j) {
+        if (!mbar_wait(&ctl->empty[s], parity ^ 1u)) atomicOr(&g_err_linear, kErrDrain);
+        if (++s == held) s = 0, parity ^= 1u;
       }
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA --
-    int64_t it = 0;
+    int s = 0;
+    uint32_t parity = 0;
     int32_t i = 0;
+    const uint32_t a_addr = smem_u32(stages);
+    const uint64_t ad0 = kAmn ? tc::sw128_mnmajor_desc(a_addr, kBox) : tc::sw128_kmajor_desc(a_addr);
+    const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand, kBox) : tc::sw128_kmajor_desc(a_addr + kOperand);
     uint32_t cuts = 0;  // bit s: parity of the next cut slice of stage s
     bool ok = true;
     for (int32_t t = pair; t < tiles && ok; t += pairs) {
@@ -408,11 +417,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       }
       const uint32_t d = tmem + uint32_t(b * kTile);
       const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
-      for (int32_t kb = 0; kb < x.nk; ++kb, ++it) {
-        const int s = int(it % kStages);
-        uint8_t* stage = stages + s * kStageBytes;
-        const int32_t have = x.k_end - x.k0 - kb * kBK;
+      for (int32_t k = x.k0; k < x.k_end; k += kBK) {
+        const int32_t have = x.k_end - k;
         if (PROD == kGradW && have < kBK) {
+          uint8_t* stage = stages + s * kStageBytes;
           // zero the rows past this expert's: whole 128-byte rows of every box
           // (the swizzle moves 16-byte pieces inside a row only)
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
@@ -438,23 +446,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
             if (lane == 0) mbar_arrive(&ctl->full[s]);  // both parts are there
           }
         }
-        if (rank != 0) continue;
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], uint32_t(it / kStages) & 1u));
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-          break;
-        }
-        tc::fence_after();
-        if (lane == 0) {
-          const uint32_t a_addr = smem_u32(stage), b_addr = a_addr + kOperand;
-          const uint64_t ad = kAmn ? tc::sw128_mnmajor_desc(a_addr, kBox) : tc::sw128_kmajor_desc(a_addr);
-          const uint64_t bd = kBmn ? tc::sw128_mnmajor_desc(b_addr, kBox) : tc::sw128_kmajor_desc(b_addr);
+        if (rank == 0) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+            break;
+          }
+          tc::fence_after();
+          if (lane == 0) {
+            const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
 #pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            tc::pair_mma_bf16(d, ad + k * (kAmn ? 128 : 2), bd + k * (kBmn ? 128 : 2), idesc, uint32_t(kb | k));
-          tc::pair_commit(&ctl->empty[s]);
+            for (int j = 0; j < kBK / 16; ++j)
+              tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
+            tc::pair_commit(&ctl->empty[s]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (++s == kStages) s = 0, parity ^= 1u;
       }
       if (!ok) break;
       if (rank == 0 && lane == 0) tc::pair_commit(&ctl->tfull[b]);
