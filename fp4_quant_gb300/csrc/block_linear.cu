@@ -32,11 +32,14 @@
 //
 // Ten warps per CTA: one issues the loads, one (of CTA 0) the products into
 // one of two accumulators in tensor memory, eight read the other accumulator
-// and store it.  Every wait is bounded.
+// and store it (sixteen were no faster: 278 against 273 us at 4096 x 8192 x
+// 7168, the issuing warps wait longer for their turn).  Every wait is bounded.
 #include <atomic>
 #include <cstring>
 
 #include "block.h"
+#include "block_act.cuh"
+#include "block_linear.cuh"
 #include "block_util.cuh"
 #include "tc.cuh"
 #include "tma.cuh"
@@ -89,39 +92,17 @@ struct LinearP {
   const uint16_t* residual;
   const void* bias;
   int32_t b32;
+  int32_t splits;   // parts of the sum (dense y and dx of few tokens): fp32 parts to `part`
+  float* part;      // [splits, rows, ld_part]
+  int64_t ld_part;
 };
-
-// The normal distribution function, from Abramowitz and Stegun's formula
-// 7.1.26 for erf (absolute error below 1.5e-7): with v = |z| / sqrt 2 and t = 1
-// / (1 + 0.3275911 v), 1 - Phi(|z|) = t (a1 + t (a2 + ...)) exp(-v^2) / 2.
-__device__ __forceinline__ float normal_cdf(float z, float exp_half_sq) {
-  const float t = __fdividef(1.0f, fmaf(0.3275911f * 0.70710678f, fabsf(z), 1.0f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  q = 0.5f * q * t * exp_half_sq;
-  return z < 0.0f ? q : 1.0f - q;
-}
-
-// act(z), for values that are rounded to bf16 next.
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if (ACT == GLU_ACT_SILU) return __fdividef(z, 1.0f + __expf(-z));
-  if (ACT == GLU_ACT_GELU_TANH) {
-    const float u = 1.5957691216057308f * fmaf(0.044715f * z * z, z, z);  // 2 sqrt(2 / pi) (z + 0.044715 z^3)
-    return __fdividef(z, 1.0f + __expf(-u));                              // z sigmoid(u) = z (1 + tanh(u / 2)) / 2
-  }
-  if (ACT == GLU_ACT_RELU) return z > 0.0f ? z : (z != z ? z : 0.0f);
-  if (ACT == GLU_ACT_GELU_ERF) return z * normal_cdf(z, __expf(-0.5f * z * z));
-  return z;
-}
 
 struct Tile {
   int32_t e, a0;           // expert; first row of D
   int32_t b0, b_end;       // columns of D: tokens, or columns of a dw
   int32_t n;               // columns computed (b_end - b0 rounded up)
   int32_t k0, k_end, nk;   // summed range and its 64-wide blocks
+  int32_t split;           // the part of the sum that the range is
 };
 
 // `rows` tokens in equal tiles of at most 256.
@@ -133,7 +114,11 @@ __device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kT
 template <int PROD>
 __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_t t) {
   Tile x;
-  x.e = 0;
+  x.e = x.split = 0;
+  if (PROD != kGradW && p.splits > 1) {
+    x.split = t % p.splits;
+    t /= p.splits;
+  }
   int32_t rows0 = 0, rows1 = p.rows;
   if (p.offsets) {
     int32_t lo = 0, hi = p.E - 1;  // last expert whose first tile is not after t
@@ -166,6 +151,11 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
     x.n = min(each, (x.b_end - x.b0 + kStep - 1) / kStep * kStep);
     x.k0 = 0;
     x.k_end = p.depth;
+    if (p.splits > 1) {  // whole slices, as equal as they go
+      const int32_t slices = (p.depth + kBK - 1) / kBK;
+      x.k0 = slices * x.split / p.splits * kBK;
+      x.k_end = min(p.depth, slices * (x.split + 1) / p.splits * kBK);
+    }
   }
   x.nk = (x.k_end - x.k0 + kBK - 1) / kBK;
   return x;
@@ -175,7 +165,7 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
 template <int PROD>
 __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane) {
   if (!p.offsets) {
-    if (lane == 0) ctl->first[1] = p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(p.rows));
+    if (lane == 0) ctl->first[1] = p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(p.rows) * p.splits);
     return;
   }
   int32_t row = 0, tiles = 0;
@@ -307,7 +297,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   Ctl* ctl = reinterpret_cast<Ctl*>(stages + kStages * kStageBytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -407,85 +397,86 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       const Tile x = tile_at<PROD>(p, ctl, t);
       if (x.nk == 0) continue;  // an expert without rows: the epilogue stores zeros
       const int b = i & 1;
-      if (rank == 0) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
-          break;
-        }
-        tc::fence_after();
-      }
       const uint32_t d = tmem + uint32_t(b * kTile);
       const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
-      for (int32_t k = x.k0; k < x.k_end; k += kBK) {
-        const int32_t have = x.k_end - k;
-        if (PROD == kGradW && have < kBK) {
-          uint8_t* stage = stages + s * kStageBytes;
-          // zero the rows past this expert's: whole 128-byte rows of every box
-          // (the swizzle moves 16-byte pieces inside a row only)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
-          cuts ^= 1u << s;
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-            break;
-          }
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          const int32_t n = (kBK - have) * 8;  // 16-byte pieces per box
-          for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
-            *reinterpret_cast<uint4*>(stage + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
-          fence_proxy_async();
-          __syncwarp();
-          if (rank != 0) {
-            if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
-          } else {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], ((cuts >> s) & 1u) ^ 1u));
-            if (!ok) {
-              if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-              break;
-            }
-            if (lane == 0) mbar_arrive(&ctl->full[s]);  // both parts are there
-          }
-        }
-        if (rank == 0) {
+      // the products of the slice in stage s, from element k of the sum on
+      auto products = [&](int32_t k) {
+        const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
+#pragma unroll
+        for (int j = 0; j < kBK / 16; ++j)
+          tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
+        tc::pair_commit(&ctl->empty[s]);
+      };
+      const int32_t k_cut = PROD == kGradW ? x.k_end - (x.k_end - x.k0) % kBK : x.k_end;  // where whole slices end
+      if (rank == 0) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
+        if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+        tc::fence_after();
+        for (int32_t k = x.k0; k < k_cut && ok; k += kBK) {
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
           if (!ok) {
             if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
             break;
           }
           tc::fence_after();
-          if (lane == 0) {
-            const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
-#pragma unroll
-            for (int j = 0; j < kBK / 16; ++j)
-              tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
-            tc::pair_commit(&ctl->empty[s]);
-          }
-          __syncwarp();
+          if (tc::elect_one()) products(k);
+          if (++s == kStages) s = 0, parity ^= 1u;
         }
-        if (++s == kStages) s = 0, parity ^= 1u;
+        __syncwarp();
       }
-      if (!ok) break;
-      if (rank == 0 && lane == 0) tc::pair_commit(&ctl->tfull[b]);
+      if (PROD == kGradW && ok) {
+        const int32_t whole = (k_cut - x.k0) / kBK;
+        if (rank != 0) s = (s + whole) % kStages;
+        const int32_t have = x.k_end - k_cut;
+        if (have > 0) {
+          // zero the rows past this expert's: whole 128-byte rows of every box
+          // (the swizzle moves 16-byte pieces inside a row only)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          const int32_t n = (kBK - have) * 8;  // 16-byte pieces per box
+          for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
+            *reinterpret_cast<uint4*>(stages + s * kStageBytes + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
+          fence_proxy_async();
+          __syncwarp();
+          if (rank != 0) {
+            if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
+          } else if (ok) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], (cuts >> s) & 1u));
+            tc::fence_after();
+            if (tc::elect_one()) {
+              mbar_arrive(&ctl->full[s]);  // both parts are there: its phase is done too
+              if (ok) products(k_cut);
+            }
+            __syncwarp();
+          }
+          if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+          cuts ^= 1u << s;
+          if (++s == kStages) s = 0, parity ^= 1u;
+        }
+      }
+      if (ok && rank == 0 && tc::elect_one()) tc::pair_commit(&ctl->tfull[b]);
       ++i;
     }
-    if (lane == 0) {
+    __syncwarp();
+    if (tc::elect_one()) {  // the lane that issued the products
       if (rank == 0) tc::pair_commit(&ctl->done);
       if (!mbar_wait(&ctl->done, 0)) atomicOr(&g_err_linear, kErrDrain);
     }
     __syncwarp();
   } else {
     // ---------------------------------------------------------- epilogue --
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, group = (warp - 2) >> 2;
     int32_t i = 0;
     for (int32_t t = pair; t < tiles; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
       const int b = i & 1;
       if (x.nk > 0) {
-        const bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tfull[b], (uint32_t(i) >> 1) & 1u));
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-          break;
+        bool ok = true;
+        if (lane == 0) {
+          ok = mbar_wait(&ctl->tfull[b], (uint32_t(i) >> 1) & 1u);
+          if (!ok) atomicOr(&g_err_linear, kErrWaitFull);
         }
+        if (!__shfl_sync(0xFFFFFFFFu, ok, 0)) break;
         tc::fence_after();
         ++i;
       }
@@ -497,14 +488,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
         bias = p.b32 ? __ldg(static_cast<const float*>(p.bias) + at) : bf16_of_bits(__ldg(static_cast<const uint16_t*>(p.bias) + at));
       }
 #pragma unroll 1
-      for (int c = half * 32; c < x.n; c += 64) {
+      for (int c = group * 32; c < x.n; c += 8 * kEpiWarps) {
         uint32_t r[32];
         // y and dx: this lane has column row0 + lane of 32 tokens in r, and
         // after the transposition four columns of every fourth token
         const int32_t token = x.b0 + c + (lane & 3), col = row0 + (lane & ~3);
         const TokenView view = {p.width - col, x.b_end - token};
         uint32_t res[8][2];
-        if (PROD == kForward && p.residual)
+        if (PROD == kForward && p.residual && p.splits == 1)
           load_quads(p.residual + int64_t(token) * p.ld_residual + col, p.ld_residual, view, res);
         if (x.nk > 0) {
           tc::ld32(tbase + uint32_t(c), r);
@@ -513,7 +504,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 #pragma unroll
           for (int j = 0; j < 32; ++j) r[j] = 0;
         }
-        if (PROD != kGradW) {
+        if (PROD != kGradW && p.splits > 1) {
+          float* part = p.part + (int64_t(x.split) * p.rows + x.b0 + c) * p.ld_part + row0 + lane;
+          if (row0 + lane < p.width) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (x.b0 + c + j < x.b_end) part[j * p.ld_part] = __uint_as_float(r[j]);
+          }
+        } else if (PROD != kGradW) {
           uint32_t w[8][2];
           if (PROD == kForward) {
 #pragma unroll
@@ -561,7 +559,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
       if (x.nk > 0) {
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) peer_arrive(peer_addr(&ctl->tempty[b], 0));
+        if (lane == 0) peer_arrive_relaxed(peer_addr(&ctl->tempty[b], 0));  // its reads are done (wait_ld)
       }
     }
     // rows that no expert has
@@ -622,7 +620,7 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   // by expert the device counts the tiles: no more than one token tile per
   // expert above the dense count
   const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
-                                      : p.n_at * ((int64_t(p.rows) + kTile - 1) / kTile + (p.offsets ? p.E : 0));
+                                      : p.n_at * ((int64_t(p.rows) + kTile - 1) / kTile + (p.offsets ? p.E : 0)) * p.splits;
   int pairs = 0;
   e = pairs_at_once(reinterpret_cast<const void*>(kern), d, &pairs);
   if (e != cudaSuccess) return e;
@@ -630,156 +628,43 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   return launch_kernel(kern, 2 * pairs, kThreads, kSmem, s, p);
 }
 
-// ------------------------------------------------------- dz and its sums --
-
-constexpr int kDzRows = 128;  // rows of one expert per block
-
-struct DzP {
-  const uint16_t *dy, *z;
-  uint16_t* dz;  // NULL: not stored
-  float* part;   // [slots, N], or NULL
-  float* db;
-  const int32_t* offsets;
-  int64_t ld_dy, ld_z, ld_dz;
-  int32_t rows, N, E, slots;
-};
-
-template <int ACT>
-__device__ __forceinline__ float act_grad(float z) {
-  if (ACT == GLU_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + __expf(-z)), q = __fdividef(1.0f, 1.0f + __expf(z));
-    return s * fmaf(z, q, 1.0f);
+// Parts of the sum of a dense y or dx: with fewer tiles than half the pairs,
+// the number (up to 8) with the fewest slices on the busiest pair, where each
+// keeps eight slices at least.  At 64 x 7168 x 8192 two parts and their join
+// took 27 us against 44 us for one part.  A function of the shape alone (76 pairs).
+int split_of(int64_t rows, int64_t width, int64_t depth) {
+  const int64_t tiles = (rows + kTile - 1) / kTile * ((width + kTile - 1) / kTile), slices = (depth + kBK - 1) / kBK;
+  if (tiles > 38) return 1;
+  int best = 1;
+  int64_t least = slices;
+  for (int n = 2; n <= 8 && slices / n >= 8; ++n) {
+    const int64_t busiest = (tiles * n + 75) / 76 * ((slices + n - 1) / n);
+    if (busiest < least) least = busiest, best = n;
   }
-  if (ACT == GLU_ACT_GELU_TANH) {
-    const float z2 = z * z;
-    const float u = 1.5957691216057308f * fmaf(0.044715f * z2, z, z);
-    const float du = 1.5957691216057308f * fmaf(0.134145f, z2, 1.0f);
-    const float s = __fdividef(1.0f, 1.0f + __expf(-u)), q = __fdividef(1.0f, 1.0f + __expf(u));
-    return s * fmaf(z * q, du, 1.0f);
-  }
-  if (ACT == GLU_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-  if (ACT == GLU_ACT_GELU_ERF) {
-    const float e = __expf(-0.5f * z * z);
-    return fmaf(z * 0.3989422804014327f, e, normal_cdf(z, e));
-  }
-  return 1.0f;
-}
-
-__device__ __forceinline__ int32_t cut_at(const int32_t* offsets, int32_t e, int32_t rows) {
-  return e == 0 ? 0 : max(0, min(offsets[e], rows));
-}
-
-// Slots of the sums: expert e has those from floor(cut[e] / kDzRows) + e on,
-// enough for its rows in parts of kDzRows.  One block per slot and 256
-// columns: 32 threads of eight columns each by eight rows at a time, four
-// rows' loads in flight per thread; the eight sums of a column are joined in
-// a fixed order.  Bound by DRAM: dy and z read, dz written, 6 bytes per
-// element.
-constexpr int kDzCols = 256, kDzDeep = 4;
-
-template <int ACT>
-__global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
-  __shared__ float sh[8][kDzCols + 8];
-  const int32_t slot = blockIdx.x;
-  int32_t e = 0, r0 = 0, r1 = p.rows, part = slot;
-  if (p.offsets) {
-    int32_t lo = 0, hi = p.E - 1;
-    while (lo < hi) {
-      const int32_t mid = (lo + hi + 1) >> 1;
-      if (cut_at(p.offsets, mid, p.rows) / kDzRows + mid <= slot) lo = mid;
-      else hi = mid - 1;
-    }
-    e = lo;
-    r0 = cut_at(p.offsets, e, p.rows);
-    r1 = max(r0, cut_at(p.offsets, e + 1, p.rows));
-    part = slot - r0 / kDzRows - e;
-  }
-  const int32_t m0 = r0 + part * kDzRows, m1 = min(r1, m0 + kDzRows);
-  if (part < 0 || m0 >= m1) return;
-  const int32_t c = blockIdx.y * kDzCols + 8 * threadIdx.x, left = p.N - c;
-  F8 sum = zeros();
-  if (left > 0) {
-    for (int32_t m = m0 + threadIdx.y; m < m1; m += 8 * kDzDeep) {
-      uint4 a[kDzDeep], z[kDzDeep];
-#pragma unroll
-      for (int i = 0; i < kDzDeep; ++i) {
-        const int64_t row = m + 8 * i;
-        if (row >= m1) continue;
-        a[i] = raw8(p.dy + row * p.ld_dy + c, left);
-        if (ACT != GLU_ACT_IDENTITY) z[i] = raw8(p.z + row * p.ld_z + c, left);
-      }
-#pragma unroll
-      for (int i = 0; i < kDzDeep; ++i) {
-        const int64_t row = m + 8 * i;
-        if (row >= m1) continue;
-        F8 d = pairs(a[i]);
-        if (ACT != GLU_ACT_IDENTITY) {
-          const F8 v = pairs(z[i]);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) d.v[q] = mul_2(d.v[q], make_float2(act_grad<ACT>(v.v[q].x), act_grad<ACT>(v.v[q].y)));
-          // kept in L2: the products read it next
-          if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.ld_dz + c) = packed(d);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) sum.v[q] = add_2(sum.v[q], d.v[q]);
-      }
-    }
-  }
-  if (!p.part) return;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) *reinterpret_cast<float2*>(&sh[threadIdx.y][8 * threadIdx.x + 2 * q]) = sum.v[q];
-  __syncthreads();
-  const int32_t t = threadIdx.y * 32 + threadIdx.x, col = blockIdx.y * kDzCols + t;
-  if (col >= p.N) return;
-  float v = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v += sh[i][t];
-  p.part[int64_t(slot) * p.N + col] = v;
-}
-
-// db[e] from the slots of expert e.
-__global__ void __launch_bounds__(512) db_kernel(const DzP p) {
-  __shared__ float sh[16][33];
-  const int32_t e = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
-  int32_t r0 = 0, r1 = p.rows, first = 0;
-  if (p.offsets) {
-    r0 = cut_at(p.offsets, e, p.rows);
-    r1 = max(r0, cut_at(p.offsets, e + 1, p.rows));
-    first = r0 / kDzRows + e;
-  }
-  const int32_t n = (r1 - r0 + kDzRows - 1) / kDzRows;
-  float v = 0.0f;
-  if (c < p.N)
-    for (int32_t i = threadIdx.y; i < n; i += 16) v += p.part[int64_t(first + i) * p.N + c];
-  sh[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y != 0 || c >= p.N) return;
-  v = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v += sh[i][threadIdx.x];
-  p.db[int64_t(e) * p.N + c] = v;
+  return best;
 }
 
 int64_t padded8(int64_t n) { return (n + 7) / 8 * 8; }
 int64_t dz_slots(const glu_block_linear_bwd_args& a) { return (a.M + kDzRows - 1) / kDzRows + (a.E > 0 ? a.E : 0); }
 size_t dz_bytes(const glu_block_linear_bwd_args& a) {
-  return a.act != GLU_ACT_IDENTITY && (a.dx || a.dw) ? size_t(a.M) * padded8(a.N) * 2 : 0;
+  return a.act != GLU_ACT_IDENTITY && (a.dx || a.dw) ? size_t(a.M) * size_t(padded8(a.N)) * 2 : 0;
 }
 
 }  // namespace
 
-size_t linear_fwd_workspace(const glu_block_linear_fwd_args&) { return 0; }
-size_t linear_bwd_workspace(const glu_block_linear_bwd_args& a) {
-  return dz_bytes(a) + (a.db ? size_t(dz_slots(a)) * a.N * 4 : 0);
+static size_t part_bytes(int splits, int64_t rows, int64_t width) {
+  return splits > 1 ? size_t(splits) * size_t(rows) * size_t(padded8(width)) * 4 : 0;
 }
+static int fwd_splits(const glu_block_linear_fwd_args& a) {
+  return a.E > 0 || linear_few(a) ? 1 : split_of(a.M, a.N, a.K);
+}
+static int dx_splits(const glu_block_linear_bwd_args& a) { return a.E > 0 || !a.dx ? 1 : split_of(a.M, a.K, a.N); }
 
-static cudaError_t launch_dz(int act, const DzP& q, cudaStream_t s) {
-  auto kern = act == GLU_ACT_SILU        ? dz_kernel<GLU_ACT_SILU>
-              : act == GLU_ACT_GELU_TANH ? dz_kernel<GLU_ACT_GELU_TANH>
-              : act == GLU_ACT_RELU      ? dz_kernel<GLU_ACT_RELU>
-              : act == GLU_ACT_GELU_ERF  ? dz_kernel<GLU_ACT_GELU_ERF>
-                                         : dz_kernel<GLU_ACT_IDENTITY>;
-  return launch_kernel(kern, dim3(unsigned(q.slots), unsigned((q.N + kDzCols - 1) / kDzCols)), dim3(32, 8), 0, s, q);
+size_t linear_fwd_workspace(const glu_block_linear_fwd_args& a) { return part_bytes(fwd_splits(a), a.M, a.N); }
+size_t linear_bwd_workspace(const glu_block_linear_bwd_args& a) {
+  // dz, then the parts of db and those of dx, which follow each other on the stream
+  const size_t db = a.db ? size_t(dz_slots(a)) * a.N * 4 : 0, dx = part_bytes(dx_splits(a), a.M, a.K);
+  return dz_bytes(a) + (db > dx ? db : dx);
 }
 
 // Maps of the tokens' rows (64-wide slices), in boxes of 128, 64 and 32 rows.
@@ -790,6 +675,7 @@ static cudaError_t token_maps(LinearP& p, const void* t, int64_t cols, int64_t r
 }
 
 cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s, const DevInfo& d) {
+  if (linear_few(a)) return launch_linear_few(a, s);
   LinearP p;
   memset(&p, 0, sizeof p);
   const int64_t E = a.E > 0 ? a.E : 1;
@@ -801,6 +687,9 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   p.rows = int32_t(a.M);
   p.width = int32_t(a.N);
   p.depth = int32_t(a.K);
+  p.splits = fwd_splits(a);
+  p.part = static_cast<float*>(a.workspace);
+  p.ld_part = padded8(a.N);
   p.out = static_cast<uint16_t*>(a.y);
   p.ld_out = a.ld_y;
   p.z = static_cast<uint16_t*>(a.z);
@@ -809,6 +698,10 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   p.ld_residual = a.ld_residual;
   p.bias = a.bias;
   p.b32 = a.b_fmt == GLU_FMT_FP32;
+  if (p.splits > 1) {
+    e = launch_t<kForward, GLU_ACT_IDENTITY>(p, s, d);
+    return e == cudaSuccess ? launch_linear_join(a, p.part, p.splits, s) : e;
+  }
   switch (a.act) {
     case GLU_ACT_SILU: return launch_t<kForward, GLU_ACT_SILU>(p, s, d);
     case GLU_ACT_GELU_TANH: return launch_t<kForward, GLU_ACT_GELU_TANH>(p, s, d);
@@ -839,12 +732,8 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     q.N = int32_t(a.N);
     q.E = int32_t(E);
     q.slots = int32_t(dz_slots(a));
-    e = launch_dz(a.act, q, s);
+    e = launch_linear_dz(a.act, q, s);
     if (e != cudaSuccess) return e;
-    if (a.db) {
-      e = launch_kernel(db_kernel, dim3(unsigned((a.N + 31) / 32), unsigned(E)), dim3(32, 16), 0, s, q);
-      if (e != cudaSuccess) return e;
-    }
     if (q.dz) dz = q.dz, ld_dz = q.ld_dz;
   }
   LinearP p;
@@ -858,9 +747,22 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.K);
     p.depth = int32_t(a.N);
+    p.splits = dx_splits(a);
+    p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + dz_bytes(a));
+    p.ld_part = padded8(a.K);
     p.out = static_cast<uint16_t*>(a.dx);
     p.ld_out = a.ld_dx;
     e = launch_t<kGradX, GLU_ACT_IDENTITY>(p, s, d);
+    if (e == cudaSuccess && p.splits > 1) {
+      glu_block_linear_fwd_args j = {};  // the join of a forward without bias, activation and residual
+      j.act = GLU_ACT_IDENTITY;
+      j.b_fmt = GLU_FMT_BF16;
+      j.M = a.M;
+      j.N = a.K;
+      j.ld_y = a.ld_dx;
+      j.y = a.dx;
+      e = launch_linear_join(j, p.part, p.splits, s);
+    }
     if (e != cudaSuccess) return e;
   }
   if (a.dw) {
@@ -872,6 +774,7 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     p.out = static_cast<uint16_t*>(a.dw);
     p.ld_out = a.ld_dw;
     p.stride_out = a.stride_dw;
+    p.splits = 1;
     e = launch_t<kGradW, GLU_ACT_IDENTITY>(p, s, d);
   }
   return e;

@@ -73,6 +73,15 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
+// True in one lane of a converged warp, always the same one.  Code that only it
+// runs keeps what the whole warp computed in uniform registers, which is where
+// the MMA's operands have to be.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xFFFFFFFF; selp.u32 %0, 1, 0, p;}" : "=r"(r));
+  return r != 0;
+}
+
 // Arrive on `bar` once every tcgen05.mma issued so far by this thread has
 // completed.
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -148,6 +157,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
 }
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same where no memory of this thread's is handed over (a release would
+// first wait for its stores to arrive).
+__device__ __forceinline__ void peer_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Bounded wait that also orders what the other CTA did before it arrived.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
