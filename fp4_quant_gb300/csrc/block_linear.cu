@@ -331,26 +331,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 
   if (warp == 0) {
     // ---------------------------------------------------------- producer --
-    if (lane == 0) {
-      // one thread's latency per stage counts here and in the issuing warp:
-      // stage and parity are counted, addresses formed once
-      int s = 0, held = 0;  // held: stages ever filled, up to all
-      uint32_t parity = 0;
-      const uint32_t full0 = peer_addr(&ctl->full[0], 0);
-      bool ok = true;
-      for (int32_t t = pair; t < tiles && ok; t += pairs) {
-        const Tile x = tile_at<PROD>(p, ctl, t);
-        const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
-        // the smallest box with the half's columns (more than it needs are not
-        // multiplied)
-        const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
-        const uint32_t bytes = uint32_t(kOperand + (kHalf >> box) * kBK * 2);
-        for (int32_t k = x.k0; k < x.k_end; k += kBK) {
-          if (!mbar_wait(&ctl->empty[s], parity ^ 1u)) {
-            atomicOr(&g_err_linear, kErrWaitEmpty);
-            ok = false;
-            break;
-          }
+    // the warp runs as one, so that what it computes stays in uniform
+    // registers; one lane issues
+    int s = 0, held = 0;  // held: stages ever filled, up to all
+    uint32_t parity = 0;
+    const uint32_t full0 = peer_addr(&ctl->full[0], 0);
+    bool ok = true;
+    for (int32_t t = pair; t < tiles && ok; t += pairs) {
+      const Tile x = tile_at<PROD>(p, ctl, t);
+      const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
+      // the smallest box with the half's columns (more than it needs are not
+      // multiplied)
+      const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
+      const uint32_t bytes = uint32_t(kOperand + (kHalf >> box) * kBK * 2);
+      const CUtensorMap* tb = &p.tb[PROD == kGradW ? 0 : box];
+      for (int32_t k = x.k0; k < x.k_end; k += kBK) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+          break;
+        }
+        if (tc::elect_one()) {
           uint8_t* a = stages + s * kStageBytes;
           uint8_t* b = a + kOperand;
           // a slice that another expert's rows follow lands on this CTA's own
@@ -362,26 +363,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
           if (PROD == kForward) {
             pair_load_3d(a, &p.ta, k, a0, x.e, bar);
           } else if (PROD == kGradX) {
+#pragma unroll
             for (int i = 0; i < kHalf / 64; ++i) pair_load_3d(a + i * kBox, &p.ta, a0 + 64 * i, k, x.e, bar);
           } else {
+#pragma unroll
             for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(a + i * kBox, &p.ta, a0 + 64 * i, k, bar);
           }
           if (PROD == kGradW) {
-            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(b + i * kBox, &p.tb[0], b0 + 64 * i, k, bar);
+#pragma unroll
+            for (int i = 0; i < kHalf / 64; ++i) pair_load_2d(b + i * kBox, tb, b0 + 64 * i, k, bar);
           } else {
-            pair_load_2d(b, &p.tb[box], k, b0, bar);
+            pair_load_2d(b, tb, k, b0, bar);
           }
-          held = max(held, s + 1);
-          if (++s == kStages) s = 0, parity ^= 1u;
         }
+        held = max(held, s + 1);
+        if (++s == kStages) s = 0, parity ^= 1u;
       }
-      // never leave with loads in flight: the products on each stage's last
-      // slice (which waited for its loads) are done
-      if (s == held) s = 0, parity ^= 1u;
-      for (int j = 0; j < held; ++j) {
-        if (!mbar_wait(&ctl->empty[s], parity ^ 1u)) atomicOr(&g_err_linear, kErrDrain);
-        if (++s == held) s = 0, parity ^= 1u;
-      }
+    }
+    // never leave with loads in flight: the products on each stage's last slice
+    // (which waited for its loads) are done
+    if (s == held) s = 0, parity ^= 1u;
+    for (int j = 0; j < held; ++j) {
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u)) && lane == 0) atomicOr(&g_err_linear, kErrDrain);
+      if (++s == held) s = 0, parity ^= 1u;
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA --
