@@ -94,14 +94,14 @@ def _c():
 
 
 def _call(name, args, stream):
-    st = getattr(_c(), name)(ctypes.byref(args), stream)
+    st = getattr(_bound or _c(), name)(args, stream)
     if st != GLU_OK:
         raise GluQuantError(st, name)
 
 
 def _workspace(name, *args):
     n = _size(0)
-    st = getattr(_c(), name)(*args, ctypes.byref(n))
+    st = getattr(_bound or _c(), name)(*args, n)
     if st != GLU_OK:
         raise GluQuantError(st, name)
     return n.value
@@ -110,19 +110,18 @@ def _workspace(name, *args):
 def _device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    d = t.device
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {d}, but the current device is cuda:{torch.cuda.current_device()} "
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()} "
                          "(the kernels run on the current device)")
-    return d
+    return t.device
 
 
 def _matrix(t, name, shape, device, dtype=_BF16):
     """Checks a matrix and returns its row stride."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     st = t.stride()
@@ -136,8 +135,8 @@ def _packed(t, name, shape, device, dtypes):
     """Checks a contiguous operand."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with shape {shape}, got {tuple(t.shape)}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     return t.data_ptr()
@@ -148,7 +147,7 @@ def _new(shape, dtype, device):
     n = shape[-1]
     if n % 8 == 0:
         return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(shape[:-1] + (-(-n // 8) * 8,), dtype=dtype, device=device)[..., :n]
+    return torch.empty(tuple(shape[:-1]) + (-(-n // 8) * 8,), dtype=dtype, device=device)[..., :n]
 
 
 def _result(out, key, shape, dtype, device, packed=False):
@@ -205,7 +204,8 @@ def _gate(gate, D, device):
     if gate is None:
         return 0, 0
     if gate.dim() == 1:
-        gate = gate.unsqueeze(0)
+        _packed(gate, "gate", (D,), device, (_BF16,))
+        return 1, -(-D // 8) * 8
     return gate.shape[0], _matrix(gate, "gate", (gate.shape[0], D), device)
 
 
@@ -223,7 +223,7 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     device = _device(x, "x")
-    M, D = shape = tuple(x.shape)
+    M, D = shape = x.shape
     fmt = _stream_fmt(x, "x")
     wf = _weight_fmt(w_pre, w_post)
     ld_x = _matrix(x, "x", shape, device, x.dtype)
@@ -252,7 +252,7 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     if r.dim() != 2:
         raise ValueError("r must be a matrix")
     device = _device(r, "r")
-    M, D = shape = tuple(r.shape)
+    M, D = shape = r.shape
     fmt = _stream_fmt(r, "r")
     wf = _weight_fmt(w_pre, w_post)
     ld_r = _matrix(r, "r", shape, device, r.dtype)
@@ -288,14 +288,14 @@ def route(ids, n_experts, *, out=None, stream=None) -> dict:
     device = _device(ids, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, choices]")
-    T, K = shape = tuple(ids.shape)
+    T, K = shape = ids.shape
     p = _packed(ids, "ids", shape, device, (torch.int64, _I32))
     slot = _result(out, "slot", shape, _I32, device, True)
     src = _result(out, "src", (T * K,), _I32, device, True)
     offsets = _result(out, "offsets", (n_experts + 1,), _I32, device, True)
     n = _workspace("glu_block_route_workspace", T, K, n_experts)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
-    a = RouteArgs(8 if ids.dtype is torch.int64 else 4, n_experts, T, K, p, slot.data_ptr(), src.data_ptr(), offsets.data_ptr(), ws.data_ptr(), n)
+    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    a = RouteArgs(8 if ids.dtype is torch.int64 else 4, n_experts, T, K, p, slot.data_ptr(), src.data_ptr(), offsets.data_ptr(), _p(ws), n)
     _call("glu_block_route", a, _handle(stream, device, slot, src, offsets, ws))
     return {"slot": slot, "src": src, "offsets": offsets}
 
@@ -388,7 +388,7 @@ def linear(x, w, *, bias=None, act=ACT_IDENTITY, residual=None, offsets=None, ke
     z = _result(out, "z", (M, N), _BF16, device) if keep_z else None
     a = LinearFwdArgs(act, FMT_FP32 if bias is not None and bias.dtype is _F32 else FMT_BF16, E, 0, M, N, K, ld_x, ld_w, stride_w, ld_res,
                       _ld(y), _ld(z), x.data_ptr(), w.data_ptr(), b, _p(residual), off, y.data_ptr(), _p(z), None, 0)
-    n = _workspace("glu_block_linear_fwd_workspace", ctypes.byref(a))
+    n = _workspace("glu_block_linear_fwd_workspace", a)
     ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
     a.workspace, a.workspace_bytes = _p(ws), n
     _call("glu_block_linear_fwd", a, _handle(stream, device, y, z, ws))
@@ -408,13 +408,13 @@ def linear_bwd(dy, x, w, *, z=None, act=ACT_IDENTITY, offsets=None, need_dx=True
     ld_dy = _matrix(dy, "dy", (M, N), device)
     ld_z = _matrix(z, "z", (M, N), device) if z is not None else 0
     dx = _result(out, "dx", (M, K), _BF16, device) if need_dx else None
-    dw = _result(out, "dw", tuple(w.shape), _BF16, device) if need_dw else None
+    dw = _result(out, "dw", w.shape, _BF16, device) if need_dw else None
     db = _result(out, "db", (E, N) if E else (N,), _F32, device, True) if need_db else None
     ld_dw = _ld(dw)
     stride_dw = 0 if dw is None or not E else dw.stride(0) if E > 1 else N * ld_dw
     a = LinearBwdArgs(act, E, M, N, K, ld_dy, ld_z, ld_x, ld_w, stride_w, _ld(dx), ld_dw, stride_dw, dy.data_ptr(), _p(z), x.data_ptr(), w.data_ptr(),
                       off, _p(dx), _p(dw), _p(db), None, 0)
-    n = _workspace("glu_block_linear_bwd_workspace", ctypes.byref(a))
+    n = _workspace("glu_block_linear_bwd_workspace", a)
     ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
     a.workspace, a.workspace_bytes = _p(ws), n
     _call("glu_block_linear_bwd", a, _handle(stream, device, dx, dw, db, ws))

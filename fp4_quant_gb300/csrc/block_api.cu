@@ -100,8 +100,9 @@ int check_route(const glu_block_route_args* a) {
   if (a == nullptr || (a->id_bytes != 4 && a->id_bytes != 8)) return GLU_EINVAL;
   const int st = check_route_size(a->T, a->K, a->E);
   if (st != GLU_OK) return st;
-  if (!a->ids || !a->slot || !a->src || !a->offsets || !a->workspace) return GLU_EINVAL;
-  if (a->workspace_bytes < gq::route_workspace(a->T, a->K, a->E)) return GLU_EINVAL;
+  if (!a->ids || !a->slot || !a->src || !a->offsets) return GLU_EINVAL;
+  const size_t need = gq::route_workspace(a->T, a->K, a->E);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need)) return GLU_EINVAL;
   Check c;
   for (const void* p : {a->ids, static_cast<const void*>(a->slot), static_cast<const void*>(a->src),
                         static_cast<const void*>(a->offsets), static_cast<const void*>(a->workspace)})

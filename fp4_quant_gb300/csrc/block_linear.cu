@@ -55,7 +55,8 @@ constexpr int kStageBytes = 2 * kOperand;
 constexpr int kBox = 64 * kBK * 2;   // one M/N-major box: 64 elements by 64 k
 constexpr int kStep = 32;            // granularity of a tile's columns
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+// warps: loads, products, epilogue, and for dw one that cuts slices short
+constexpr int threads_of(bool dw) { return (2 + kEpiWarps + (dw ? 1 : 0)) * 32; }
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr uint32_t kIdescK = tc::idesc_bf16_f32(kTile, 0);  // the columns are added per tile
 
@@ -291,7 +292,7 @@ __device__ __forceinline__ void piece_transpose(uint32_t (&w)[16], int lane) {
 }
 
 template <int PROD, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_kernel(const __grid_constant__ LinearP p) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == kGradW), 1) linear_kernel(const __grid_constant__ LinearP p) {
   constexpr bool kAmn = PROD != kForward, kBmn = PROD == kGradW;
   constexpr uint32_t kIdesc = kIdescK | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
@@ -355,7 +356,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
           uint8_t* a = stages + s * kStageBytes;
           uint8_t* b = a + kOperand;
           // a slice that another expert's rows follow lands on this CTA's own
-          // barrier, to be cut short by warp 1
+          // barrier, to be cut short by its last warp
           const bool cut = PROD == kGradW && k + kBK > x.k_end;
           const uint32_t bar = cut ? smem_u32(&ctl->tail[s]) : full0 + 8u * uint32_t(s);
           if (cut) mbar_arrive_expect_tx(&ctl->tail[s], bytes);
@@ -395,76 +396,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
     const uint32_t a_addr = smem_u32(stages);
     const uint64_t ad0 = kAmn ? tc::sw128_mnmajor_desc(a_addr, kBox) : tc::sw128_kmajor_desc(a_addr);
     const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand, kBox) : tc::sw128_kmajor_desc(a_addr + kOperand);
-    uint32_t cuts = 0;  // bit s: parity of the next cut slice of stage s
     bool ok = true;
-    for (int32_t t = pair; t < tiles && ok; t += pairs) {
+    for (int32_t t = pair; t < tiles && ok && rank == 0; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
       if (x.nk == 0) continue;  // an expert without rows: the epilogue stores zeros
       const int b = i & 1;
       const uint32_t d = tmem + uint32_t(b * kTile);
       const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
-      // the products of the slice in stage s, from element k of the sum on
-      auto products = [&](int32_t k) {
-        const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
-#pragma unroll
-        for (int j = 0; j < kBK / 16; ++j)
-          tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
-        tc::pair_commit(&ctl->empty[s]);
-      };
-      const int32_t k_cut = PROD == kGradW ? x.k_end - (x.k_end - x.k0) % kBK : x.k_end;  // where whole slices end
-      if (rank == 0) {
-        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
-        if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
+      if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+      tc::fence_after();
+      for (int32_t k = x.k0; k < x.k_end && ok; k += kBK) {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+          break;
+        }
         tc::fence_after();
-        for (int32_t k = x.k0; k < k_cut && ok; k += kBK) {
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-            break;
-          }
-          tc::fence_after();
-          if (tc::elect_one()) products(k);
-          if (++s == kStages) s = 0, parity ^= 1u;
+        if (tc::elect_one()) {
+          const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
+#pragma unroll
+          for (int j = 0; j < kBK / 16; ++j)
+            if (PROD != kGradW || k + 16 * j < x.k_end)  // dw: 16 rows at a time, as far as there are some
+              tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
+          tc::pair_commit(&ctl->empty[s]);
         }
-        __syncwarp();
+        if (++s == kStages) s = 0, parity ^= 1u;
       }
-      if (PROD == kGradW && ok) {
-        const int32_t whole = (k_cut - x.k0) / kBK;
-        if (rank != 0) s = (s + whole) % kStages;
-        const int32_t have = x.k_end - k_cut;
-        if (have > 0) {
-          // zero the rows past this expert's: whole 128-byte rows of every box
-          // (the swizzle moves 16-byte pieces inside a row only)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
-          const uint4 zero = make_uint4(0, 0, 0, 0);
-          const int32_t n = (kBK - have) * 8;  // 16-byte pieces per box
-          for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
-            *reinterpret_cast<uint4*>(stages + s * kStageBytes + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
-          fence_proxy_async();
-          __syncwarp();
-          if (rank != 0) {
-            if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
-          } else if (ok) {
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], (cuts >> s) & 1u));
-            tc::fence_after();
-            if (tc::elect_one()) {
-              mbar_arrive(&ctl->full[s]);  // both parts are there: its phase is done too
-              if (ok) products(k_cut);
-            }
-            __syncwarp();
-          }
-          if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-          cuts ^= 1u << s;
-          if (++s == kStages) s = 0, parity ^= 1u;
-        }
-      }
-      if (ok && rank == 0 && tc::elect_one()) tc::pair_commit(&ctl->tfull[b]);
+      __syncwarp();
+      if (ok && tc::elect_one()) tc::pair_commit(&ctl->tfull[b]);
       ++i;
     }
     __syncwarp();
     if (tc::elect_one()) {  // the lane that issued the products
       if (rank == 0) tc::pair_commit(&ctl->done);
       if (!mbar_wait(&ctl->done, 0)) atomicOr(&g_err_linear, kErrDrain);
+    }
+    __syncwarp();
+  } else if (warp == 2 + kEpiWarps) {
+    // --------------------------------------------------- slices cut short --
+    // Of an expert's last slice the products take 16 rows at a time; the rows
+    // of the next expert among the last 16 are zeroed here, ahead of the
+    // issuing warp: whole 128-byte rows of every box (the swizzle moves 16-byte
+    // pieces inside a row only).  CTA 0's warp then counts the slice in for
+    // both CTAs.
+    int s = 0;
+    uint32_t cuts = 0;  // bit s: parity of the next cut slice of stage s
+    for (int32_t t = pair; t < tiles; t += pairs) {
+      const Tile x = tile_at<PROD>(p, ctl, t);
+      if (x.nk == 0) continue;
+      const int32_t have = (x.k_end - x.k0) % kBK;
+      s = (s + x.nk - 1) % kStages;
+      if (have > 0) {
+        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        const int32_t n = (-have & 15) * 8;  // 16-byte pieces per box
+        for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
+          *reinterpret_cast<uint4*>(stages + s * kStageBytes + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
+        fence_proxy_async();
+        __syncwarp();
+        if (rank != 0) {
+          if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
+        } else {
+          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], (cuts >> s) & 1u));
+          if (ok && lane == 0) mbar_arrive(&ctl->full[s]);
+        }
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+          break;
+        }
+        cuts ^= 1u << s;
+      }
+      s = (s + 1) % kStages;
     }
     __syncwarp();
   } else {
@@ -591,8 +594,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) linear_
 // Pairs that the current device runs at once: fewer than half its SMs where a
 // GPC's SMs do not all pair up, and a pair more than that would run as a
 // second wave.  Asked once per device (devices are never reconfigured).
-cudaError_t pairs_at_once(const void* kern, const DevInfo& d, int* pairs) {
-  static std::atomic<int> known[64];
+cudaError_t pairs_at_once(const void* kern, int threads, const DevInfo& d, int* pairs) {
+  static std::atomic<int> known[64];  // shared memory, one block per SM, limits every product alike
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -604,7 +607,7 @@ cudaError_t pairs_at_once(const void* kern, const DevInfo& d, int* pairs) {
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(d.sms / 2 * 2));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(unsigned(threads));
   cfg.dynamicSmemBytes = kSmem;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
@@ -626,10 +629,10 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
                                       : p.n_at * ((int64_t(p.rows) + kTile - 1) / kTile + (p.offsets ? p.E : 0)) * p.splits;
   int pairs = 0;
-  e = pairs_at_once(reinterpret_cast<const void*>(kern), d, &pairs);
+  e = pairs_at_once(reinterpret_cast<const void*>(kern), threads_of(PROD == kGradW), d, &pairs);
   if (e != cudaSuccess) return e;
   if (most < pairs) pairs = int(most);
-  return launch_kernel(kern, 2 * pairs, kThreads, kSmem, s, p);
+  return launch_kernel(kern, 2 * pairs, threads_of(PROD == kGradW), kSmem, s, p);
 }
 
 // Parts of the sum of a dense y or dx: with fewer tiles than half the pairs,

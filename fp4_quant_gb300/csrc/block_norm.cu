@@ -45,8 +45,6 @@ struct RingWait {
   }
 };
 
-__device__ __forceinline__ void row_barrier(int threads) { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); }
-
 // A chunk of eight columns (from column c) of a staged row.  RAGGED: where the
 // width D ends inside it, its first ones from row m itself (the copies take
 // whole chunks), the rest 0.
@@ -112,100 +110,67 @@ __device__ __forceinline__ float rstd_of(float sum, float per_d, float eps) {
   return __frcp_rn(__fsqrt_rn(fmaf(sum, per_d, eps)));
 }
 
-// Outputs of row m from V chunks per thread (chunk k of thread t starts at
-// column 8 (t + k * threads)): r holds x on entry, b the branch times f =
-// alpha gate (w_post + o), sq the thread's sum of the branch's squares.  Only
-// a product and a conversion per element wait for each sum.  `met` is called
-// once, behind a barrier that every thread reached with its chunks in
-// registers.
-template <typename XT, int V, bool RAGGED, typename W, typename Met>
-__device__ __forceinline__ void norm_row(const NormFwdP& p, int64_t m, int threads, BlockSum<1>& sums, uint32_t& buf,
-                                         F8 (&r)[V], F8 (&b)[V], float sq, float per_d, W w_pre, Met met) {
-  const int D = int(p.D), tid = threadIdx.x;
-  if (p.branch) {
-    float rs = 1.0f;
-    if (p.w_post) {
-      float s[1] = {sq};
-      block_sum(sums, buf, threads, s);
-      met();
-      rs = rstd_of(s[0], per_d, p.eps);
-      if (tid == 0) p.rstd_post[m] = rs;
-    }
-    XT* rr = static_cast<XT*>(p.r) + m * p.ld_r;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = 8 * (tid + k * threads);
-      if (c >= D) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[k].v[i] = fma_2(b[k].v[i], both(rs), r[k].v[i]);
-      store8<RAGGED>(rr + c, D - c, r[k]);
-    }
-  }
-  if (p.w_pre) {
-    float2 s2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = 8 * (tid + k * threads);
-      if (c >= D) continue;
-      const F8 w = w_pre(k, c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s2 = fma_2(r[k].v[i], r[k].v[i], s2);
-        r[k].v[i] = mul_2(r[k].v[i], w.v[i]);
-      }
-    }
-    float s[1] = {sum2(s2)};
-    block_sum(sums, buf, threads, s);
-    if (!p.w_post) met();
-    const float rs = rstd_of(s[0], per_d, p.eps);
-    if (tid == 0) p.rstd_pre[m] = rs;
-    uint16_t* yr = p.y + m * p.ld_y;
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int c = 8 * (tid + k * threads);
-      if (c >= D) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) r[k].v[i] = mul_2(r[k].v[i], both(rs));
-      store8<RAGGED>(yr + c, D - c, r[k]);
-    }
-  } else if (!p.w_post) {
-    row_barrier(threads);
-    met();
-  }
-}
-
 // Few rows: one block per row, one chunk per thread, straight from memory.
 template <typename XT>
 __global__ void __launch_bounds__(1024) norm_fwd_row_kernel(const NormFwdP p) {
   __shared__ BlockSum<1> sums;
   uint32_t buf = 0;
-  const int D = int(p.D), c = 8 * int(threadIdx.x);
+  const int D = int(p.D), c = 8 * int(threadIdx.x), threads = blockDim.x;
   const int64_t m = blockIdx.x;
-  F8 r[1] = {zeros()}, b[1] = {zeros()}, w = zeros();
-  float2 sq = make_float2(0.0f, 0.0f);
+  const float per_d = __frcp_rn(float(D));
+  F8 r = zeros(), b = zeros(), w = zeros();
+  float2 s2 = make_float2(0.0f, 0.0f);
   if (c < D) {
-    r[0] = direct8(static_cast<const XT*>(p.x) + m * p.ld_x, c, D - c);
+    r = direct8(static_cast<const XT*>(p.x) + m * p.ld_x, c, D - c);
     if (p.w_pre) w = weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c);
     if (p.branch) {
-      b[0] = direct8(p.branch + m * p.ld_branch, c, D - c);
+      b = direct8(p.branch + m * p.ld_branch, c, D - c);
       const F8 f = weight8(p.w_post, p.w32, p.w_offset, p.alpha, p.gate ? p.gate + (m / p.rows_per_gate) * p.ld_gate : nullptr, c, D - c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        sq = fma_2(b[0].v[i], b[0].v[i], sq);
-        b[0].v[i] = mul_2(b[0].v[i], f.v[i]);
+        s2 = fma_2(b.v[i], b.v[i], s2);
+        b.v[i] = mul_2(b.v[i], f.v[i]);
       }
     }
   }
-  norm_row<XT, 1, true>(p, m, blockDim.x, sums, buf, r, b, sum2(sq), __frcp_rn(float(D)), [&](int, int) { return w; }, [] {});
+  if (p.branch) {
+    float rs = 1.0f;
+    if (p.w_post) {
+      float s[1] = {sum2(s2)};
+      block_sum(sums, buf, threads, s);
+      rs = rstd_of(s[0], per_d, p.eps);
+      if (threadIdx.x == 0) p.rstd_post[m] = rs;
+    }
+    if (c < D) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.v[i] = fma_2(b.v[i], both(rs), r.v[i]);
+      store8<true>(static_cast<XT*>(p.r) + m * p.ld_r + c, D - c, r);
+    }
+  }
+  if (!p.w_pre) return;
+  s2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s2 = fma_2(r.v[i], r.v[i], s2);
+  float s[1] = {sum2(s2)};
+  block_sum(sums, buf, threads, s);
+  const float rs = rstd_of(s[0], per_d, p.eps);
+  if (threadIdx.x == 0) p.rstd_pre[m] = rs;
+  if (c >= D) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = mul_2(mul_2(r.v[i], w.v[i]), both(rs));
+  store8<true>(p.y + m * p.ld_y + c, D - c, r);
 }
 
-// Many rows: each block takes consecutive ones through a ring of staged rows.
-// Up to V = 2 chunks per thread (D <= 8192) the weights of a thread's columns
+// Many rows: each block takes consecutive ones through a ring of staged rows,
+// chunk k of thread t starting at column 8 (t + k * threads).  One exchange per
+// row: the sum of squares of r goes with that of the next row's branch, which
+// is in registers by then.  (With an exchange for each, 16384 x 7168 took 252
+// us with an fp32 stream and 190 us with a bf16 one.)  Up to V = 2 chunks per thread (D <= 8192) the weights of a thread's columns
 // stay in its registers, wider rows fetch them again.
 template <typename XT, int V, bool RAGGED>
 __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  RingCtl<1>* ctl = reinterpret_cast<RingCtl<1>*>(smem);
+  RingCtl<2>* ctl = reinterpret_cast<RingCtl<2>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
   const uint32_t whole = uint32_t(D / 8) * 16, xb = whole / 2 * sizeof(XT), at_g = xb + (p.branch ? whole : 0u);
@@ -236,12 +201,13 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
     }
   }
   RingWait wait;
-  int s = 0;
+  int s = 0;  // the stage of the next row to read
   uint32_t parity = 0, buf = 0;
   const float per_d = __frcp_rn(float(D));
   int64_t grp = 0, g_end = m0;  // the gate row, and the first row past its rows
   int64_t f_end = m0;           // first row that f does not hold for
-  for (int64_t m = m0; m < m1; ++m) {
+  F8 x[V], b[V];                // the row read last: the stream, and the branch times f (with the gate)
+  auto read_row = [&](int64_t m) {
     if (m >= g_end) {
       grp = m / p.rows_per_gate;
       g_end = (grp + 1) * p.rows_per_gate;
@@ -260,13 +226,12 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
     }
     const uint8_t* st = stages + s * p.stage_bytes;
     wait(&ctl->full[s], parity);
-    F8 r[V], b[V];
     float2 sq = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int k = 0; k < V; ++k) {
       const int c = 8 * (tid + k * threads);
       if (c >= D) continue;
-      r[k] = staged8<RAGGED>(st, static_cast<const XT*>(p.x), m, p.ld_x, c, D);
+      x[k] = staged8<RAGGED>(st, static_cast<const XT*>(p.x), m, p.ld_x, c, D);
       if (!p.branch) continue;
       b[k] = staged8<RAGGED>(st + xb, p.branch, m, p.ld_branch, c, D);
       const F8 fk = kHold ? f[kHold ? k : 0] : factors(c);
@@ -279,12 +244,59 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
         if (p.stream_gate) b[k].v[i] = mul_2(b[k].v[i], g.v[i]);
       }
     }
-    norm_row<XT, V, RAGGED>(p, m, threads, ctl->sums, buf, r, b, sum2(sq), per_d,
-                    [&](int k, int c) { return kHold ? w[kHold ? k : 0] : weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c); },
-                    [&] {
-                      if (tid == 0 && m + p.stages < m1) load(m + p.stages, s);
-                    });
+    return sum2(sq);
+  };
+  // every thread has read row m: its stage takes the row `stages` further on
+  auto free_row = [&](int64_t m) {
+    if (tid == 0 && m + p.stages < m1) load(m + p.stages, s);
     if (++s == p.stages) s = 0, parity ^= 1u;
+  };
+  XT* r_out = static_cast<XT*>(p.r) + m0 * p.ld_r;
+  uint16_t* y_out = p.y + m0 * p.ld_y;
+  float sum[2] = {0.0f, 0.0f};
+  for (int64_t m = m0 - 1; m < m1; ++m) {  // row m is written, row m + 1 read
+    const bool row = m >= m0;
+    F8 r[V];
+    float2 s2 = make_float2(0.0f, 0.0f);
+    if (row) {
+      const float rq = p.w_post ? rstd_of(sum[1], per_d, p.eps) : 1.0f;
+      if (p.w_post && tid == 0) p.rstd_post[m] = rq;
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        const int c = 8 * (tid + k * threads);
+        if (c >= D) continue;
+        r[k] = x[k];
+        if (p.branch) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) r[k].v[i] = fma_2(b[k].v[i], both(rq), r[k].v[i]);
+          store8<RAGGED>(r_out + c, D - c, r[k]);
+        }
+        if (!p.w_pre) continue;
+        const F8 wk = kHold ? w[kHold ? k : 0] : weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s2 = fma_2(r[k].v[i], r[k].v[i], s2);
+          r[k].v[i] = mul_2(r[k].v[i], wk.v[i]);
+        }
+      }
+      r_out += p.ld_r;
+    }
+    sum[0] = sum2(s2);
+    sum[1] = m + 1 < m1 ? read_row(m + 1) : 0.0f;
+    block_sum(ctl->sums, buf, threads, sum);
+    if (m + 1 < m1) free_row(m + 1);
+    if (!row || !p.w_pre) continue;
+    const float rs = rstd_of(sum[0], per_d, p.eps);
+    if (tid == 0) p.rstd_pre[m] = rs;
+#pragma unroll
+    for (int k = 0; k < V; ++k) {
+      const int c = 8 * (tid + k * threads);
+      if (c >= D) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r[k].v[i] = mul_2(r[k].v[i], both(rs));
+      store8<RAGGED>(y_out + c, D - c, r[k]);
+    }
+    y_out += p.ld_y;
   }
 }
 

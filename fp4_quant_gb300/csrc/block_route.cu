@@ -19,7 +19,7 @@ namespace {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int64_t kSortMin = 4096;  // assignments per block of the list, at least
+constexpr int64_t kSortMin = 1024;  // assignments per block of the list, at least
 constexpr int64_t kSortBlocks = 1024;
 
 struct RouteP {
@@ -70,24 +70,39 @@ __device__ __forceinline__ int32_t block_scan(int32_t v, int32_t* warp_total) {
   return v + (warp ? warp_total[warp - 1] : 0);
 }
 
-// Places of block b's assignments.  `count` (shared, [E, warps + 1]) holds
-// each warp's count of each expert, then its start.
+// Places of block b's assignments.  `count` (shared, [warps, E]) holds each
+// warp's count of each expert, then its start.  A list of one block is counted
+// here too.
 __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const RouteP p) {
   __shared__ int32_t base[kMaxExperts + 1];  // next place of each expert for this block
+  __shared__ int32_t all[kMaxExperts];
   __shared__ int32_t warp_total[32];
   extern __shared__ int32_t count[];  // [kSortWarps][E]
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // totals and this block's share before it: thread e for expert e
-  int32_t total = 0, before = 0;
-  if (int(threadIdx.x) < p.E)
-    for (int b = 0; b < p.blocks; ++b) {
-      const int32_t v = p.hist[int64_t(b) * p.E + threadIdx.x];
-      if (b < int(blockIdx.x)) before += v;
-      total += v;
+  // totals, and what the blocks before this one have of them (whole numbers:
+  // the order of the additions does not matter)
+  if (int(threadIdx.x) < p.E) all[threadIdx.x] = base[threadIdx.x] = 0;
+  __syncthreads();
+  if (p.blocks == 1) {
+    for (int64_t j = threadIdx.x; j < p.n; j += kSortThreads) {
+      const int e = id_at(p, j);
+      if (e >= 0) atomicAdd(&all[e], 1);
     }
+  } else {
+    const int64_t ahead = int64_t(blockIdx.x) * p.E;
+    for (int64_t i = threadIdx.x; i < int64_t(p.blocks) * p.E; i += kSortThreads) {
+      const int32_t v = p.hist[i];
+      if (v == 0) continue;
+      const int e = int(i % p.E);
+      atomicAdd(&all[e], v);
+      if (i < ahead) atomicAdd(&base[e], v);
+    }
+  }
+  __syncthreads();
+  const int32_t total = int(threadIdx.x) < p.E ? all[threadIdx.x] : 0;
   const int32_t end = block_scan(total, warp_total);
   if (int(threadIdx.x) < p.E) {
-    base[threadIdx.x] = end - total + before;
+    base[threadIdx.x] += end - total;
     if (blockIdx.x == 0) p.offsets[threadIdx.x + 1] = end;
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[0] = 0;
@@ -316,7 +331,7 @@ int row_grid(int64_t warps, const DevInfo& d) {
 
 size_t route_workspace(int64_t T, int64_t K, int32_t E) {
   const int64_t n = T * K, per = sort_per_block(n);
-  return size_t((n + per - 1) / per) * size_t(E) * 4;
+  return n <= per ? 0 : size_t((n + per - 1) / per) * size_t(E) * 4;
 }
 
 cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s) {
@@ -334,7 +349,7 @@ cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s) {
   const int smem = kSortWarps * a.E * 4;
   cudaError_t e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  e = launch_kernel(route_count_kernel, p.blocks, kSortThreads, 0, s, p);
+  if (p.blocks > 1) e = launch_kernel(route_count_kernel, p.blocks, kSortThreads, 0, s, p);
   if (e != cudaSuccess) return e;
   return launch_kernel(route_place_kernel, p.blocks, kSortThreads, smem, s, p);
 }

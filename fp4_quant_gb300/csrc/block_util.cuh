@@ -202,12 +202,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Sums over the block's `threads` threads (whole warps) of N = 1 or 3 values
+// Barrier of the block's `threads` threads (whole warps).  The warp converges
+// first: an aligned barrier that its lanes reached apart (the compiler may
+// place it behind either side of a branch) would count them twice.
+__device__ __forceinline__ void row_barrier(int threads) {
+  __syncwarp();
+  asm volatile("barrier.sync 1, %0;" ::"r"(threads) : "memory");
+}
+
+// Sums over the block's `threads` threads (whole warps) of N = 1, 2 or 3 values
 // each, the same bits in every thread.  `buf` alternates between calls (two
 // buffers), so one barrier per call is enough: a buffer is written again only
-// after the next call's barrier.  Three values share the exchanges inside a
-// warp: halves of it first swap values, so that each quarter then sums one
-// (6 exchanges instead of 15, and 10 instead of 15 across up to 16 warps).
+// after the next call's barrier.  Two or three values share the exchanges inside
+// a warp: halves of it first swap values, so that each half or quarter then
+// sums one (5 exchanges instead of 10, 6 instead of 15).
 template <int N>
 struct BlockSum {
   float part[2][N][32];
@@ -222,8 +230,30 @@ __device__ __forceinline__ void block_sum(BlockSum<1>& s, uint32_t& buf, int thr
   float* q = s.part[buf & 1u][0];
   ++buf;
   if (lane == 0) q[threadIdx.x >> 5] = v[0];
-  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  row_barrier(threads);
   v[0] = warp_sum(lane < warps ? q[lane] : 0.0f);
+}
+__device__ __forceinline__ void block_sum(BlockSum<2>& s, uint32_t& buf, int threads, float (&v)[2]) {
+  constexpr uint32_t kAll = 0xFFFFFFFFu;
+  const int warps = threads >> 5, lane = threadIdx.x & 31;  // at most 16 warps
+  const bool hi = lane & 16;
+  float x = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+  if (warps > 1) {
+    float(&q)[2][32] = s.part[buf & 1u];
+    ++buf;
+    if ((lane & 15) == 0) q[lane >> 4][threadIdx.x >> 5] = x;
+    row_barrier(threads);
+    const int w = lane & 15;
+    x = w < warps ? q[lane >> 4][w] : 0.0f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+  } else {
+    __syncwarp();
+  }
+  v[0] = __shfl_sync(kAll, x, 0);
+  v[1] = __shfl_sync(kAll, x, 16);
 }
 __device__ __forceinline__ void block_sum(BlockSum<3>& s, uint32_t& buf, int threads, float (&v)[3]) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -238,12 +268,13 @@ __device__ __forceinline__ void block_sum(BlockSum<3>& s, uint32_t& buf, int thr
   if (warps == 1) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) v[j] = __shfl_sync(kAll, x, 8 * j);
+    __syncwarp();
     return;
   }
   float(&q)[3][32] = s.part[buf & 1u];
   ++buf;
   if ((lane & 7) == 0 && lane < 24) q[lane >> 3][threadIdx.x >> 5] = x;
-  asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");
+  row_barrier(threads);
   const int w = lane & 15;
   a = w < warps ? q[lane >> 4][w] : 0.0f;
   b = w < warps ? q[2][w] : 0.0f;

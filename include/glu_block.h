@@ -121,7 +121,8 @@ GLU_API int glu_block_norm_bwd_workspace(int64_t M, int64_t D, int64_t gates, si
  *   slot [T, K]:     the place of (t, k), -1 where it was dropped
  *   src [T * K]:     the j at each place, -1 from offsets[E] on
  * (all int32).  1 <= T * K < 2^31, 1 <= E <= 1024.  The workspace (16-byte
- * aligned) has glu_block_route_workspace's bytes. */
+ * aligned; NULL where the query says 0) has glu_block_route_workspace's
+ * bytes. */
 typedef struct glu_block_route_args {
   int32_t id_bytes; /* 4 or 8 */
   int32_t E;

@@ -80,7 +80,7 @@ ROUTE = dict(id_bytes=8, E=8, T=16, K=2, ids=P, slot=P, src=P, offsets=P, worksp
 
 @pytest.mark.parametrize("kw,status", [
     (dict(id_bytes=2), G.GLU_EINVAL), (dict(T=0), G.GLU_EINVAL), (dict(E=0), G.GLU_EINVAL), (dict(ids=None), G.GLU_EINVAL),
-    (dict(workspace_bytes=0), G.GLU_EINVAL), (dict(E=1025), G.GLU_ESHAPE), (dict(T=1 << 31), G.GLU_ESHAPE), (dict(slot=P + 4), G.GLU_EALIGN)])
+    (dict(T=4096, workspace_bytes=0), G.GLU_EINVAL), (dict(E=1025), G.GLU_ESHAPE), (dict(T=1 << 31), G.GLU_ESHAPE), (dict(slot=P + 4), G.GLU_EALIGN)])
 def test_route_refusals(kw, status):
     assert _status("glu_block_route", B.RouteArgs, ROUTE, kw) == status
 
