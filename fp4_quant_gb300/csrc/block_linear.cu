@@ -26,9 +26,12 @@
 //
 // By expert the rows are cut at offsets[e]: a tile of y or dx has tokens of
 // one expert (those of the next one that its boxes also fetched are not
-// stored); a tile of dw sums over one expert's rows (those of the next one are
-// zeroed in shared memory before the product, so that what they hold, NaN
-// included, does not count).
+// stored); a tile of dw sums over one expert's rows, 16 at a time.  Its last
+// rows, fewer than 16, come through a buffer of their own, ahead of the others,
+// where the rows of the next expert are zeroed (so that what they hold, NaN
+// included, does not count) while the sum over the whole sixteens goes on.
+// (Zeroed in the ring's stages they held the products up: 242 us against 197
+// for 64 uneven experts of 32768 x 2048 x 2048.)
 //
 // Ten warps per CTA: one issues the loads, one (of CTA 0) the products into
 // one of two accumulators in tensor memory, eight read the other accumulator
@@ -53,9 +56,11 @@ constexpr int kBK = 64, kStages = 6;
 constexpr int kOperand = kHalf * kBK * 2;  // 16 KB
 constexpr int kStageBytes = 2 * kOperand;
 constexpr int kBox = 64 * kBK * 2;   // one M/N-major box: 64 elements by 64 k
+constexpr int kTailBox = 64 * 16 * 2;                      // the same by 16 k
+constexpr int kTailBytes = 2 * (kHalf / 64) * kTailBox;    // A's and B's boxes of a CTA
 constexpr int kStep = 32;            // granularity of a tile's columns
 constexpr int kEpiWarps = 8;
-// warps: loads, products, epilogue, and for dw one that cuts slices short
+// warps: loads, products, epilogue, and for dw one for the last rows
 constexpr int threads_of(bool dw) { return (2 + kEpiWarps + (dw ? 1 : 0)) * 32; }
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr uint32_t kIdescK = tc::idesc_bf16_f32(kTile, 0);  // the columns are added per tile
@@ -67,20 +72,24 @@ struct Ctl {
   uint64_t empty[kStages];  // each CTA's own: the products on its stage are done
   uint64_t tfull[2];        // each CTA's own: the accumulator is complete
   uint64_t tempty[2];       // CTA 0's: both CTAs' warps have read it
-  uint64_t tail[kStages];   // each CTA's own: a slice to be cut short has landed
-  uint64_t other[kStages];  // CTA 0's: CTA 1 has cut its part of it
+  // dw, two buffers of last rows: landed (each CTA's own), cut short in both
+  // CTAs (CTA 0's), multiplied (each CTA's own)
+  uint64_t tail_full[2], tail_ready[2], tail_free[2];
   uint64_t done;            // each CTA's own: all products are done
   uint32_t tmem;
   int32_t cut[kMaxExperts + 1];    // first row of each expert, in range and not falling
-  int32_t first[kMaxExperts + 1];  // tiles before each expert's
+  int32_t order[kMaxExperts];      // experts by falling row count
+  int32_t first[kMaxExperts + 1];  // tiles before each expert's, in that order
 };
-constexpr int kSmem = 1024 + kStages * kStageBytes + int(sizeof(Ctl));
+constexpr int kSmem = 1024 + kStages * kStageBytes + 2 * kTailBytes + int(sizeof(Ctl));
 static_assert(kSmem <= 232448, "shared memory per CTA exceeds 227 KB");
 
 __device__ uint32_t g_err_linear;
 
 struct LinearP {
-  CUtensorMap ta, tb[3];     // tb[i]: boxes of 128 >> i rows, for tiles with fewer columns
+  // tb[i]: boxes of 128 >> i rows, for tiles with fewer columns; dw: tb[0], and
+  // ta16, tb[1] by 16 rows
+  CUtensorMap ta, tb[3], ta16;
   const int32_t* offsets;    // NULL: dense
   int32_t E;                 // experts (dense: 1)
   int32_t rows;              // of x and dy
@@ -88,6 +97,7 @@ struct LinearP {
   int32_t cols;              // columns of D of a dw (K)
   int32_t depth;             // summed over (kForward: K, kGradX: N)
   int32_t n_at;              // tiles of 256 rows of D
+  int32_t most;              // most tokens of a tile (a multiple of 32, up to 256)
   int64_t ld_out, stride_out, ld_residual, ld_z;
   uint16_t *out, *z;
   const uint16_t* residual;
@@ -102,12 +112,13 @@ struct Tile {
   int32_t e, a0;           // expert; first row of D
   int32_t b0, b_end;       // columns of D: tokens, or columns of a dw
   int32_t n;               // columns computed (b_end - b0 rounded up)
-  int32_t k0, k_end, nk;   // summed range and its 64-wide blocks
+  int32_t k0, k_end;       // summed range
+  int32_t k_main;          // where the ring's part of it ends (dw: whole sixteens)
   int32_t split;           // the part of the sum that the range is
 };
 
-// `rows` tokens in equal tiles of at most 256.
-__device__ __forceinline__ int32_t token_tiles(int32_t rows) { return (rows + kTile - 1) / kTile; }
+// `rows` tokens in equal tiles of at most `most`.
+__device__ __forceinline__ int32_t token_tiles(int32_t rows, int32_t most) { return (rows + most - 1) / most; }
 
 // Tile t of the walk: bands of eight row tiles of D, the columns inside, so
 // that the pairs at work share a band's rows of A and a few columns of B in
@@ -122,18 +133,18 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
   }
   int32_t rows0 = 0, rows1 = p.rows;
   if (p.offsets) {
-    int32_t lo = 0, hi = p.E - 1;  // last expert whose first tile is not after t
+    int32_t lo = 0, hi = p.E - 1;  // last one in order whose first tile is not after t
     while (lo < hi) {
       const int32_t mid = (lo + hi + 1) >> 1;
       if (ctl->first[mid] <= t) lo = mid;
       else hi = mid - 1;
     }
-    x.e = lo;
     t -= ctl->first[lo];
-    rows0 = ctl->cut[lo];
-    rows1 = ctl->cut[lo + 1];
+    x.e = ctl->order[lo];
+    rows0 = ctl->cut[x.e];
+    rows1 = ctl->cut[x.e + 1];
   }
-  const int32_t n_bt = PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(rows1 - rows0);
+  const int32_t n_bt = PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(rows1 - rows0, p.most);
   constexpr int32_t kBand = 8;
   const int32_t band = t / (kBand * n_bt), rem = t - band * kBand * n_bt;
   const int32_t high = min(kBand, p.n_at - band * kBand);
@@ -158,47 +169,69 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
       x.k_end = min(p.depth, slices * (x.split + 1) / p.splits * kBK);
     }
   }
-  x.nk = (x.k_end - x.k0 + kBK - 1) / kBK;
+  x.k_main = PROD == kGradW ? x.k_end - (x.k_end - x.k0) % 16 : x.k_end;
   return x;
 }
 
-// The experts' row ranges and tile counts, by warp 0.
+// The experts' row ranges, their order and tile counts, by the whole block.
+// The tiles go round the pairs by falling size (largest expert first), so that
+// the pairs' sums differ by no more than one tile; beyond 256 experts, where
+// ranking them would take longer than that is worth, in their own order.
 template <int PROD>
-__device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int lane) {
+__device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int warp, int lane) {
+  const int32_t col_tiles = (p.cols + kTile - 1) / kTile;
   if (!p.offsets) {
-    if (lane == 0) ctl->first[1] = p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(p.rows) * p.splits);
+    if (threadIdx.x == 0) ctl->first[1] = p.n_at * (PROD == kGradW ? col_tiles : token_tiles(p.rows, p.most) * p.splits);
     return;
   }
-  int32_t row = 0, tiles = 0;
-  for (int32_t e0 = 0; e0 < p.E; e0 += 32) {
-    const int32_t e = e0 + lane;
-    // ends in range, and a running maximum so that none falls
-    int32_t end = e < p.E ? max(0, min(p.offsets[e + 1], p.rows)) : 0;
+  if (warp == 0) {
+    int32_t row = 0;
+    for (int32_t e0 = 0; e0 < p.E; e0 += 32) {
+      const int32_t e = e0 + lane;
+      // ends in range, and a running maximum so that none falls
+      int32_t end = e < p.E ? max(0, min(p.offsets[e + 1], p.rows)) : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, end, o);
-      if (lane >= o) end = max(end, u);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, end, o);
+        if (lane >= o) end = max(end, u);
+      }
+      end = max(end, row);
+      if (e < p.E) {
+        ctl->cut[e + 1] = end;
+        ctl->order[e] = e;
+      }
+      row = __shfl_sync(0xFFFFFFFFu, end, 31);
     }
-    end = max(end, row);
-    int32_t start = __shfl_up_sync(0xFFFFFFFFu, end, 1);
-    if (lane == 0) start = row;
-    int32_t n = e >= p.E ? 0 : p.n_at * (PROD == kGradW ? (p.cols + kTile - 1) / kTile : token_tiles(end - start));
-    const int32_t own = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int32_t u = __shfl_up_sync(0xFFFFFFFFu, n, o);
-      if (lane >= o) n += u;
-    }
-    if (e < p.E) {
-      ctl->cut[e] = start;
-      ctl->first[e] = tiles + n - own;
-    }
-    row = __shfl_sync(0xFFFFFFFFu, end, 31);
-    tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
+    if (lane == 0) ctl->cut[0] = 0;
   }
-  if (lane == 0) {
-    ctl->cut[p.E] = row;
-    ctl->first[p.E] = tiles;
+  __syncthreads();
+  if (p.E <= 256) {
+    for (int32_t e = threadIdx.x; e < p.E; e += blockDim.x) {
+      const int32_t own = ctl->cut[e + 1] - ctl->cut[e];
+      int32_t rank = 0;
+      for (int32_t f = 0; f < p.E; ++f) {
+        const int32_t n = ctl->cut[f + 1] - ctl->cut[f];
+        rank += n > own || (n == own && f < e);
+      }
+      ctl->order[rank] = e;
+    }
+    __syncthreads();
+  }
+  if (warp == 0) {
+    int32_t tiles = 0;
+    for (int32_t i0 = 0; i0 < p.E; i0 += 32) {
+      const int32_t i = i0 + lane, e = i < p.E ? ctl->order[i] : 0;
+      const int32_t own = i >= p.E ? 0 : p.n_at * (PROD == kGradW ? col_tiles : token_tiles(ctl->cut[e + 1] - ctl->cut[e], p.most));
+      int32_t n = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int32_t u = __shfl_up_sync(0xFFFFFFFFu, n, o);
+        if (lane >= o) n += u;
+      }
+      if (i < p.E) ctl->first[i] = tiles + n - own;
+      tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+    if (lane == 0) ctl->first[p.E] = tiles;
   }
 }
 
@@ -297,7 +330,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
   constexpr uint32_t kIdesc = kIdescK | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  Ctl* ctl = reinterpret_cast<Ctl*>(stages + kStages * kStageBytes);
+  uint8_t* tails = stages + kStages * kStageBytes;
+  Ctl* ctl = reinterpret_cast<Ctl*>(tails + 2 * kTailBytes);
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -307,18 +341,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
     prefetch_tensormap(&p.tb[0]);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
-      mbar_init(&ctl->other[s], 1);
       mbar_init(&ctl->empty[s], 1);
-      mbar_init(&ctl->tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->tfull[b], 1);
       mbar_init(&ctl->tempty[b], 2 * kEpiWarps);
+      mbar_init(&ctl->tail_full[b], 1);
+      mbar_init(&ctl->tail_ready[b], 2);
+      mbar_init(&ctl->tail_free[b], 1);
     }
     mbar_init(&ctl->done, 1);
     fence_barrier_init();
   }
-  if (warp == 0) plan_tiles<PROD>(p, ctl, lane);
+  plan_tiles<PROD>(p, ctl, warp, lane);
   if (warp == 1) {
     __syncwarp();
     tc::pair_alloc(&ctl->tmem, kTmemCols);
@@ -336,6 +371,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
     // registers; one lane issues
     int s = 0, held = 0;  // held: stages ever filled, up to all
     uint32_t parity = 0;
+    uint32_t tail = 0;  // buffers of last rows filled
     const uint32_t full0 = peer_addr(&ctl->full[0], 0);
     bool ok = true;
     for (int32_t t = pair; t < tiles && ok; t += pairs) {
@@ -346,7 +382,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
       const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
       const uint32_t bytes = uint32_t(kOperand + (kHalf >> box) * kBK * 2);
       const CUtensorMap* tb = &p.tb[PROD == kGradW ? 0 : box];
-      for (int32_t k = x.k0; k < x.k_end; k += kBK) {
+      if (PROD == kGradW && x.k_main < x.k_end) {
+        const int u = int(tail & 1u);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail_free[u], ((tail >> 1) & 1u) ^ 1u));
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
+          break;
+        }
+        if (tc::elect_one()) {
+          uint8_t* a = tails + u * kTailBytes;
+          const uint32_t bar = smem_u32(&ctl->tail_full[u]);
+          mbar_arrive_expect_tx(&ctl->tail_full[u], kTailBytes);
+#pragma unroll
+          for (int i = 0; i < kHalf / 64; ++i) {
+            pair_load_2d(a + i * kTailBox, &p.ta16, a0 + 64 * i, x.k_main, bar);
+            pair_load_2d(a + (kHalf / 64 + i) * kTailBox, &p.tb[1], b0 + 64 * i, x.k_main, bar);
+          }
+        }
+        ++tail;
+      }
+      for (int32_t k = x.k0; k < x.k_main; k += kBK) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u));
         if (!ok) {
           if (lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
@@ -355,12 +410,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
         if (tc::elect_one()) {
           uint8_t* a = stages + s * kStageBytes;
           uint8_t* b = a + kOperand;
-          // a slice that another expert's rows follow lands on this CTA's own
-          // barrier, to be cut short by its last warp
-          const bool cut = PROD == kGradW && k + kBK > x.k_end;
-          const uint32_t bar = cut ? smem_u32(&ctl->tail[s]) : full0 + 8u * uint32_t(s);
-          if (cut) mbar_arrive_expect_tx(&ctl->tail[s], bytes);
-          else if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
+          const uint32_t bar = full0 + 8u * uint32_t(s);
+          if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
           if (PROD == kForward) {
             pair_load_3d(a, &p.ta, k, a0, x.e, bar);
           } else if (PROD == kGradX) {
@@ -388,6 +439,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
       if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u)) && lane == 0) atomicOr(&g_err_linear, kErrDrain);
       if (++s == held) s = 0, parity ^= 1u;
     }
+    for (uint32_t j = tail > 2 ? tail - 2 : 0; j < tail; ++j)
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail_free[j & 1u], (j >> 1) & 1u)) && lane == 0) atomicOr(&g_err_linear, kErrDrain);
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA --
     int s = 0;
@@ -396,17 +449,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
     const uint32_t a_addr = smem_u32(stages);
     const uint64_t ad0 = kAmn ? tc::sw128_mnmajor_desc(a_addr, kBox) : tc::sw128_kmajor_desc(a_addr);
     const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand, kBox) : tc::sw128_kmajor_desc(a_addr + kOperand);
+    uint32_t tail = 0;  // buffers of last rows multiplied
     bool ok = true;
     for (int32_t t = pair; t < tiles && ok && rank == 0; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
-      if (x.nk == 0) continue;  // an expert without rows: the epilogue stores zeros
+      if (x.k0 == x.k_end) continue;  // an expert without rows: the epilogue stores zeros
       const int b = i & 1;
       const uint32_t d = tmem + uint32_t(b * kTile);
       const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tempty[b], ((uint32_t(i) >> 1) & 1u) ^ 1u));
       if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitEmpty);
       tc::fence_after();
-      for (int32_t k = x.k0; k < x.k_end && ok; k += kBK) {
+      for (int32_t k = x.k0; k < x.k_main && ok; k += kBK) {
         ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
         if (!ok) {
           if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
@@ -417,11 +471,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
           const uint64_t ad = ad0 + uint32_t(s * (kStageBytes >> 4)), bd = bd0 + uint32_t(s * (kStageBytes >> 4));
 #pragma unroll
           for (int j = 0; j < kBK / 16; ++j)
-            if (PROD != kGradW || k + 16 * j < x.k_end)  // dw: 16 rows at a time, as far as there are some
+            if (PROD != kGradW || k + 16 * j < x.k_main)  // dw: 16 rows at a time, as far as there are some
               tc::pair_mma_bf16(d, ad + j * (kAmn ? 128 : 2), bd + j * (kBmn ? 128 : 2), idesc, uint32_t((k - x.k0) | j));
           tc::pair_commit(&ctl->empty[s]);
         }
         if (++s == kStages) s = 0, parity ^= 1u;
+      }
+      if (PROD == kGradW && ok && x.k_main < x.k_end) {
+        const int u = int(tail & 1u);
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->tail_ready[u], (tail >> 1) & 1u));
+        if (!ok && lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+        ++tail;
+        tc::fence_after();
+        if (ok && tc::elect_one()) {
+          const uint32_t at = smem_u32(tails) + uint32_t(u * kTailBytes);
+          tc::pair_mma_bf16(d, tc::sw128_mnmajor_desc(at, kTailBox), tc::sw128_mnmajor_desc(at + (kHalf / 64) * kTailBox, kTailBox), idesc,
+                            uint32_t(x.k_main - x.k0));
+          tc::pair_commit(&ctl->tail_free[u]);
+        }
       }
       __syncwarp();
       if (ok && tc::elect_one()) tc::pair_commit(&ctl->tfull[b]);
@@ -434,40 +501,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
     }
     __syncwarp();
   } else if (warp == 2 + kEpiWarps) {
-    // --------------------------------------------------- slices cut short --
-    // Of an expert's last slice the products take 16 rows at a time; the rows
-    // of the next expert among the last 16 are zeroed here, ahead of the
-    // issuing warp: whole 128-byte rows of every box (the swizzle moves 16-byte
-    // pieces inside a row only).  CTA 0's warp then counts the slice in for
-    // both CTAs.
-    int s = 0;
-    uint32_t cuts = 0;  // bit s: parity of the next cut slice of stage s
+    // ------------------------------------------------------- dw: last rows --
+    // zeroes the next expert's rows of the 16: whole 128-byte rows of every box
+    // (the swizzle moves 16-byte pieces inside a row only)
+    uint32_t tail = 0;
     for (int32_t t = pair; t < tiles; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
-      if (x.nk == 0) continue;
-      const int32_t have = (x.k_end - x.k0) % kBK;
-      s = (s + x.nk - 1) % kStages;
-      if (have > 0) {
-        bool ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail[s], (cuts >> s) & 1u));
-        const uint4 zero = make_uint4(0, 0, 0, 0);
-        const int32_t n = (-have & 15) * 8;  // 16-byte pieces per box
-        for (int32_t q = lane; q < n * (kStageBytes / kBox); q += 32)
-          *reinterpret_cast<uint4*>(stages + s * kStageBytes + (q / n) * kBox + have * 128 + (q % n) * 16) = zero;
-        fence_proxy_async();
-        __syncwarp();
-        if (rank != 0) {
-          if (lane == 0) peer_arrive(peer_addr(&ctl->other[s], 0));
-        } else {
-          ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->other[s], (cuts >> s) & 1u));
-          if (ok && lane == 0) mbar_arrive(&ctl->full[s]);
-        }
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
-          break;
-        }
-        cuts ^= 1u << s;
+      const int32_t have = x.k_end - x.k_main;
+      if (have == 0) continue;
+      const int u = int(tail & 1u);
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tail_full[u], (tail >> 1) & 1u))) {
+        if (lane == 0) atomicOr(&g_err_linear, kErrWaitFull);
+        break;
       }
-      s = (s + 1) % kStages;
+      ++tail;
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      const int32_t n = (16 - have) * 8;  // 16-byte pieces per box
+      for (int32_t q = lane; q < n * (kTailBytes / kTailBox); q += 32)
+        *reinterpret_cast<uint4*>(tails + u * kTailBytes + (q / n) * kTailBox + have * 128 + (q % n) * 16) = zero;
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) peer_arrive(peer_addr(&ctl->tail_ready[u], 0));
     }
     __syncwarp();
   } else {
@@ -477,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
     for (int32_t t = pair; t < tiles; t += pairs) {
       const Tile x = tile_at<PROD>(p, ctl, t);
       const int b = i & 1;
-      if (x.nk > 0) {
+      if (x.k0 < x.k_end) {
         bool ok = true;
         if (lane == 0) {
           ok = mbar_wait(&ctl->tfull[b], (uint32_t(i) >> 1) & 1u);
@@ -504,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
         uint32_t res[8][2];
         if (PROD == kForward && p.residual && p.splits == 1)
           load_quads(p.residual + int64_t(token) * p.ld_residual + col, p.ld_residual, view, res);
-        if (x.nk > 0) {
+        if (x.k0 < x.k_end) {
           tc::ld32(tbase + uint32_t(c), r);
           tc::wait_ld();
         } else {
@@ -563,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
               put8(out + j * p.ld_out, left, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
         }
       }
-      if (x.nk > 0) {
+      if (x.k0 < x.k_end) {
         tc::fence_before();
         __syncwarp();
         if (lane == 0) peer_arrive_relaxed(peer_addr(&ctl->tempty[b], 0));  // its reads are done (wait_ld)
@@ -627,7 +681,7 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   // by expert the device counts the tiles: no more than one token tile per
   // expert above the dense count
   const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
-                                      : p.n_at * ((int64_t(p.rows) + kTile - 1) / kTile + (p.offsets ? p.E : 0)) * p.splits;
+                                      : p.n_at * ((int64_t(p.rows) + p.most - 1) / p.most + (p.offsets ? p.E : 0)) * p.splits;
   int pairs = 0;
   e = pairs_at_once(reinterpret_cast<const void*>(kern), threads_of(PROD == kGradW), d, &pairs);
   if (e != cudaSuccess) return e;
@@ -635,19 +689,27 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   return launch_kernel(kern, 2 * pairs, threads_of(PROD == kGradW), kSmem, s, p);
 }
 
-// Parts of the sum of a dense y or dx: with fewer tiles than half the pairs,
-// the number (up to 8) with the fewest slices on the busiest pair, where each
-// keeps eight slices at least.  At 64 x 7168 x 8192 two parts and their join
-// took 27 us against 44 us for one part.  A function of the shape alone (76 pairs).
-int split_of(int64_t rows, int64_t width, int64_t depth) {
-  const int64_t tiles = (rows + kTile - 1) / kTile * ((width + kTile - 1) / kTile), slices = (depth + kBK - 1) / kBK;
-  if (tiles > 38) return 1;
-  int best = 1;
-  int64_t least = slices;
-  for (int n = 2; n <= 8 && slices / n >= 8; ++n) {
-    const int64_t busiest = (tiles * n + 75) / 76 * ((slices + n - 1) / n);
-    if (busiest < least) least = busiest, best = n;
-  }
+// How the tokens of a dense y or dx are cut into tiles (at most `most` each)
+// and the sum into parts, a function of the shape alone (76 pairs): the plan
+// with the least estimated time.  A slice takes what its bytes take into the
+// SM (16 KB of weights and 64 per token at about 115 KB per us, measured at
+// 1024 x 7168 x 8192 with 128-wide tiles, 83 us, and 256-wide ones, 78 us), the
+// busiest pair's tiles follow each other, and the join of split sums reads and
+// writes the fp32 parts.
+struct TokenPlan {
+  int most, splits;
+};
+TokenPlan token_plan(int64_t rows, int64_t width, int64_t depth) {
+  const int64_t at = (width + kTile - 1) / kTile, slices = (depth + kBK - 1) / kBK;
+  TokenPlan best = {kTile, 1};
+  double least = 1e30;
+  for (int n = 1; n <= 8 && slices / n >= 8; ++n)
+    for (int most = kTile; most >= 64; most -= kStep) {
+      const int64_t bt = (rows + most - 1) / most, each = ((rows + bt - 1) / bt + kStep - 1) / kStep * kStep;
+      double us = double((at * bt * n + 75) / 76) * (double((slices + n - 1) / n) * (16.384 + 0.064 * double(each)) / 115.0 + 0.5);
+      if (n > 1) us += 3.0 + double(n) * double(rows) * double(width) * 8e-6 / 4.0;
+      if (us < least * 0.98) least = us, best = {most, n};
+    }
   return best;
 }
 
@@ -662,15 +724,17 @@ size_t dz_bytes(const glu_block_linear_bwd_args& a) {
 static size_t part_bytes(int splits, int64_t rows, int64_t width) {
   return splits > 1 ? size_t(splits) * size_t(rows) * size_t(padded8(width)) * 4 : 0;
 }
-static int fwd_splits(const glu_block_linear_fwd_args& a) {
-  return a.E > 0 || linear_few(a) ? 1 : split_of(a.M, a.N, a.K);
+static TokenPlan fwd_plan(const glu_block_linear_fwd_args& a) {
+  return a.E > 0 || linear_few(a) ? TokenPlan{kTile, 1} : token_plan(a.M, a.N, a.K);
 }
-static int dx_splits(const glu_block_linear_bwd_args& a) { return a.E > 0 || !a.dx ? 1 : split_of(a.M, a.K, a.N); }
+static TokenPlan dx_plan(const glu_block_linear_bwd_args& a) {
+  return a.E > 0 || !a.dx ? TokenPlan{kTile, 1} : token_plan(a.M, a.K, a.N);
+}
 
-size_t linear_fwd_workspace(const glu_block_linear_fwd_args& a) { return part_bytes(fwd_splits(a), a.M, a.N); }
+size_t linear_fwd_workspace(const glu_block_linear_fwd_args& a) { return part_bytes(fwd_plan(a).splits, a.M, a.N); }
 size_t linear_bwd_workspace(const glu_block_linear_bwd_args& a) {
   // dz, then the parts of db and those of dx, which follow each other on the stream
-  const size_t db = a.db ? size_t(dz_slots(a)) * a.N * 4 : 0, dx = part_bytes(dx_splits(a), a.M, a.K);
+  const size_t db = a.db ? size_t(dz_slots(a)) * a.N * 4 : 0, dx = part_bytes(dx_plan(a).splits, a.M, a.K);
   return dz_bytes(a) + (db > dx ? db : dx);
 }
 
@@ -694,7 +758,9 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   p.rows = int32_t(a.M);
   p.width = int32_t(a.N);
   p.depth = int32_t(a.K);
-  p.splits = fwd_splits(a);
+  const TokenPlan plan = fwd_plan(a);
+  p.splits = plan.splits;
+  p.most = plan.most;
   p.part = static_cast<float*>(a.workspace);
   p.ld_part = padded8(a.N);
   p.out = static_cast<uint16_t*>(a.y);
@@ -754,7 +820,9 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.K);
     p.depth = int32_t(a.N);
-    p.splits = dx_splits(a);
+    const TokenPlan plan = dx_plan(a);
+    p.splits = plan.splits;
+    p.most = plan.most;
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + dz_bytes(a));
     p.ld_part = padded8(a.K);
     p.out = static_cast<uint16_t*>(a.dx);
@@ -774,7 +842,9 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
   }
   if (a.dw) {
     e = make_tile_map(&p.ta, dz, 2, a.N, a.M, ld_dz * 2, 64, kBK, 128);
+    if (e == cudaSuccess) e = make_tile_map(&p.ta16, dz, 2, a.N, a.M, ld_dz * 2, 64, 16, 128);
     if (e == cudaSuccess) e = make_tile_map(&p.tb[0], a.x, 2, a.K, a.M, a.ld_x * 2, 64, kBK, 128);
+    if (e == cudaSuccess) e = make_tile_map(&p.tb[1], a.x, 2, a.K, a.M, a.ld_x * 2, 64, 16, 128);
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.N);
     p.cols = int32_t(a.K);
@@ -782,6 +852,7 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
     p.ld_out = a.ld_dw;
     p.stride_out = a.stride_dw;
     p.splits = 1;
+    p.most = kTile;
     e = launch_t<kGradW, GLU_ACT_IDENTITY>(p, s, d);
   }
   return e;
