@@ -10,17 +10,17 @@ namespace {
 // ------------------------------------------------------------ few tokens --
 //
 // y = act(x W^T + b) + residual for up to 16 tokens: bound by reading W once (2
-// N K bytes), so W goes from memory straight into registers, 16 bytes per
-// lane, and no shared memory or tensor memory is passed on the way.  A block
-// has 16 rows of W; its warps share the sum over K, each with a part of its
-// own, and join in a fixed order.  The products are mma.sync (16 rows x 8
-// tokens x 16): their rate does not matter here, and their operand layout is
-// met without moving data.  A lane holds eight consecutive k of rows g and g +
-// 8 (g = lane / 4), from k0 + 8 (lane % 4) on; the sum's order is free, so
-// words 0, 1 of it serve as the instruction's k = 2 t .. and 2 t + 8 .. for one
-// instruction, words 2, 3 for the next, with x taken the same way.
+// N K bytes).  A block has 16 rows of W; its warps share the sum over K, each
+// with a part of its own, and join in a fixed order.  The products are mma.sync
+// (16 rows x 8 tokens x 16): their rate does not matter here, and their operand
+// layout is met without moving data between lanes.  A lane holds eight
+// consecutive k of rows g and g + 8 (g = lane / 4), from k0 + 8 (lane % 4) on;
+// the sum's order is free, so words 0, 1 of it serve as the instruction's k =
+// 2 t .. and 2 t + 8 .. for one instruction, words 2, 3 for the next, with x
+// taken the same way.  Every lane copies what it will use itself, 16 bytes at a
+// time, into slots of shared memory that only it reads (cp.async), so a warp
+// keeps several steps of 32 k in flight without registers or barriers.
 constexpr int kFewWarps = 8;
-constexpr int kFewDeep = 4;  // 32-wide steps whose loads are in flight per warp
 
 struct FewP {
   const uint16_t *x, *w, *residual;
@@ -36,46 +36,67 @@ __device__ __forceinline__ void mma_16x8x16(float (&c)[4], uint32_t a0, uint32_t
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 few_load(const uint16_t* row, int32_t k, int32_t k_end) {
-  return k < k_end ? raw8(row + k, k_end - k) : make_uint4(0, 0, 0, 0);
+// The first n (as far as 1..8) elements from k of a row to a slot, the rest 0.
+__device__ __forceinline__ void few_copy(uint4* slot, const uint16_t* row, int32_t k, int32_t n) {
+  const uint32_t bytes = n >= 8 ? 16u : n > 0 ? 2u * uint32_t(n) : 0u;
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(slot))),
+               "l"(bytes ? row + k : row), "r"(bytes)
+               : "memory");
 }
 
-// TT: groups of eight tokens.
-template <int ACT, int TT>
+// TT: groups of eight tokens; DEEP: slots, one more than the steps in flight.
+template <int TT, int DEEP>
+constexpr int few_smem() {
+  const int ring = kFewWarps * DEEP * (2 + TT) * 32 * 16, sums = kFewWarps * 16 * (8 * TT + 1) * 4;
+  return ring > sums ? ring : sums;
+}
+
+template <int ACT, int TT, int DEEP>
 __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const FewP p) {
-  __shared__ float sums[kFewWarps][16][8 * TT + 1];
+  extern __shared__ __align__(16) uint4 ring[];  // [warps][DEEP][2 + TT][32], then the sums
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t8 = 8 * (lane & 3);
   const int32_t n0 = blockIdx.x * 16;
   // rows past N are read as the last one and not stored
   const uint16_t* w0 = p.w + int64_t(min(n0 + g, p.N - 1)) * p.ld_w;
   const uint16_t* w1 = p.w + int64_t(min(n0 + g + 8, p.N - 1)) * p.ld_w;
-  const uint16_t* xr[TT];
-#pragma unroll
-  for (int i = 0; i < TT; ++i) xr[i] = p.x + int64_t(min(8 * i + g, p.M - 1)) * p.ld_x;
   float c[TT][4] = {};
   // this warp's part of K, in steps of 32
   const int32_t steps = (p.K + 31) / 32, s0 = steps * warp / kFewWarps, s1 = steps * (warp + 1) / kFewWarps;
-  const int32_t k_end = min(p.K, s1 * 32);
-  for (int32_t s = s0; s < s1; s += kFewDeep) {
-    uint4 a[kFewDeep], b[kFewDeep];
-#pragma unroll
-    for (int i = 0; i < kFewDeep; ++i) {
-      const int32_t k = (s + i) * 32 + t8;
-      a[i] = few_load(w0, k, k_end);
-      b[i] = few_load(w1, k, k_end);
-    }
-#pragma unroll
-    for (int i = 0; i < kFewDeep; ++i) {
-      const int32_t k = (s + i) * 32 + t8;
+  uint4* mine = ring + warp * DEEP * (2 + TT) * 32 + lane;
+  auto copy = [&](int32_t s, int slot) {
+    if (s < s1) {
+      const int32_t k = s * 32 + t8, left = p.K - k;
+      uint4* q = mine + slot * (2 + TT) * 32;
+      few_copy(q, w0, k, left);
+      few_copy(q + 32, w1, k, left);
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (8 * j + g < p.M && k < k_end) v = k + 8 <= k_end ? __ldg(reinterpret_cast<const uint4*>(xr[j] + k)) : raw8(xr[j] + k, k_end - k);
-        mma_16x8x16(c[j], a[i].x, b[i].x, a[i].y, b[i].y, v.x, v.y);
-        mma_16x8x16(c[j], a[i].z, b[i].z, a[i].w, b[i].w, v.z, v.w);
+        const int32_t m = 8 * j + g;
+        few_copy(q + (2 + j) * 32, p.x + int64_t(min(m, p.M - 1)) * p.ld_x, k, m < p.M ? left : 0);
       }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < DEEP - 1; ++i) copy(s0 + i, i);
+  int slot = 0;
+  for (int32_t s = s0; s < s1; ++s) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEEP - 2) : "memory");
+    const uint4* q = mine + slot * (2 + TT) * 32;
+    const uint4 a = q[0], b = q[32];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) {
+      const uint4 v = q[(2 + j) * 32];
+      mma_16x8x16(c[j], a.x, b.x, a.y, b.y, v.x, v.y);
+      mma_16x8x16(c[j], a.z, b.z, a.w, b.w, v.z, v.w);
+    }
+    // the slot read in the step before this one takes the next copy
+    copy(s + DEEP - 1, slot == 0 ? DEEP - 1 : slot - 1);
+    if (++slot == DEEP) slot = 0;
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();
+  float(*sums)[16][8 * TT + 1] = reinterpret_cast<float(*)[16][8 * TT + 1]>(ring);
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     const int tok = 8 * j + 2 * (lane & 3);
@@ -100,11 +121,27 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const FewP p) {
   }
 }
 
-template <int ACT>
+template <int ACT, int TT, int DEEP>
+cudaError_t launch_few_d(const FewP& p, cudaStream_t s) {
+  constexpr int smem = few_smem<TT, DEEP>();
+  auto kern = few_kernel<ACT, TT, DEEP>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, unsigned((p.N + 15) / 16), kFewWarps * 32, smem, s, p);
+}
+
+// Slots by how many blocks share an SM: what is in flight per SM stays about
+// the same, and all blocks are there at once up to four per SM.
+template <int ACT, int TT>
 cudaError_t launch_few_t(const FewP& p, cudaStream_t s) {
-  const dim3 grid(unsigned((p.N + 15) / 16));
-  if (p.M <= 8) return launch_kernel(few_kernel<ACT, 1>, grid, kFewWarps * 32, 0, s, p);
-  return launch_kernel(few_kernel<ACT, 2>, grid, kFewWarps * 32, 0, s, p);
+  const int blocks = (p.N + 15) / 16;
+  if (blocks <= 152) return launch_few_d<ACT, TT, 12 / TT>(p, s);
+  if (blocks <= 304) return launch_few_d<ACT, TT, 8 / TT>(p, s);
+  return launch_few_d<ACT, TT, 4>(p, s);
+}
+template <int ACT>
+cudaError_t launch_few_a(const FewP& p, cudaStream_t s) {
+  return p.M <= 8 ? launch_few_t<ACT, 1>(p, s) : launch_few_t<ACT, 2>(p, s);
 }
 
 // ------------------------------------------------- the join of split sums --
@@ -253,9 +290,9 @@ __global__ void __launch_bounds__(512) db_kernel(const DzP p) {
 
 }  // namespace
 
-// Up to 16 tokens: at 7168 x 8192 this takes 20.3 us for one token, 21.6 for
-// eight and 29.6 for 16, with 32 (at 72 us) every block's own read of x would
-// cost more than W; the pairs' tiles take 30 us from 1 to 64.
+// Up to 16 tokens: at 7168 x 8192 with W from DRAM this takes 19.9 us for one
+// token (5.9 TB/s), 20.3 for eight and 23.2 for 16, where every block's own
+// read of x begins to count; the pairs' tiles take 27 us from 1 to 64.
 bool linear_few(const glu_block_linear_fwd_args& a) { return a.E == 0 && a.M <= 16; }
 
 cudaError_t launch_linear_few(const glu_block_linear_fwd_args& a, cudaStream_t s) {
@@ -276,11 +313,11 @@ cudaError_t launch_linear_few(const glu_block_linear_fwd_args& a, cudaStream_t s
   p.K = int32_t(a.K);
   p.b32 = a.b_fmt == GLU_FMT_FP32;
   switch (a.act) {
-    case GLU_ACT_SILU: return launch_few_t<GLU_ACT_SILU>(p, s);
-    case GLU_ACT_GELU_TANH: return launch_few_t<GLU_ACT_GELU_TANH>(p, s);
-    case GLU_ACT_RELU: return launch_few_t<GLU_ACT_RELU>(p, s);
-    case GLU_ACT_GELU_ERF: return launch_few_t<GLU_ACT_GELU_ERF>(p, s);
-    default: return launch_few_t<GLU_ACT_IDENTITY>(p, s);
+    case GLU_ACT_SILU: return launch_few_a<GLU_ACT_SILU>(p, s);
+    case GLU_ACT_GELU_TANH: return launch_few_a<GLU_ACT_GELU_TANH>(p, s);
+    case GLU_ACT_RELU: return launch_few_a<GLU_ACT_RELU>(p, s);
+    case GLU_ACT_GELU_ERF: return launch_few_a<GLU_ACT_GELU_ERF>(p, s);
+    default: return launch_few_a<GLU_ACT_IDENTITY>(p, s);
   }
 }
 
