@@ -79,6 +79,7 @@ _SIGNATURES = {
     "glu_block_device_errors": [ctypes.POINTER(ctypes.c_uint32), ctypes.c_int], "glu_block_abi_version": [],
 }
 _bound = None
+_funcs = {}  # name -> function, filled with the first call
 
 
 def _c():
@@ -89,19 +90,40 @@ def _c():
         for name, argtypes in _SIGNATURES.items():
             f = getattr(lib, name)
             f.argtypes, f.restype = argtypes, ctypes.c_int
+            _funcs[name] = f
         _bound = lib
     return _bound
 
 
+def _func(name):
+    f = _funcs.get(name)
+    if f is None:
+        _c()
+        f = _funcs[name]
+    return f
+
+
+def _empty_strided(shape, strides, dtype):
+    return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+
+
+# The allocation that torch's own generated code makes (on the current device):
+# the same as torch.empty_strided at half its cost per call.
+try:
+    _alloc = torch._C._dynamo.guards._empty_strided_cuda
+except AttributeError:
+    _alloc = _empty_strided
+
+
 def _call(name, args, stream):
-    st = getattr(_bound or _c(), name)(args, stream)
+    st = _func(name)(args, stream)
     if st != GLU_OK:
         raise GluQuantError(st, name)
 
 
 def _workspace(name, *args):
     n = _size(0)
-    st = getattr(_bound or _c(), name)(*args, n)
+    st = _func(name)(*args, n)
     if st != GLU_OK:
         raise GluQuantError(st, name)
     return n.value
@@ -142,24 +164,34 @@ def _packed(t, name, shape, device, dtypes):
     return t.data_ptr()
 
 
-def _new(shape, dtype, device):
-    """A matrix (or a stack of them) whose rows start on 16 bytes."""
+def _new(shape, dtype):
+    """A matrix (or a stack of them) whose rows start on 16 bytes, on the
+    current device."""
     n = shape[-1]
-    if n % 8 == 0:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return torch.empty(tuple(shape[:-1]) + (-(-n // 8) * 8,), dtype=dtype, device=device)[..., :n]
+    ld = n if n % 8 == 0 else -(-n // 8) * 8
+    return _alloc(shape, (ld, 1) if len(shape) == 2 else (shape[1] * ld, ld, 1), dtype)
 
 
-def _result(out, key, shape, dtype, device, packed=False):
-    """The tensor for an output: the caller's, checked, or a new one."""
+def _result(out, key, shape, dtype, device):
+    """The matrix for an output: the caller's, checked, or a new one."""
     t = None if out is None else out.get(key)
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device) if packed else _new(shape, dtype, device)
-    if packed:
-        _packed(t, key, shape, device, (dtype,))
-    else:
-        _matrix(t, key, shape, device, dtype)
+        return _new(shape, dtype)
+    _matrix(t, key, shape, device, dtype)
     return t
+
+
+def _result_packed(out, key, shape, dtype, device):
+    """The same for a contiguous output."""
+    t = None if out is None else out.get(key)
+    if t is None:
+        return _alloc(shape, (1,) if len(shape) == 1 else (shape[1], 1), dtype)
+    _packed(t, key, shape, device, (dtype,))
+    return t
+
+
+def _scratch(n):
+    return _alloc((n,), (1,), torch.uint8) if n else None
 
 
 def _ld(t):
@@ -223,7 +255,8 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     device = _device(x, "x")
-    M, D = shape = x.shape
+    M, D = x.shape
+    shape = (M, D)
     fmt = _stream_fmt(x, "x")
     wf = _weight_fmt(w_pre, w_post)
     ld_x = _matrix(x, "x", shape, device, x.dtype)
@@ -233,8 +266,8 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     wq = _packed(w_post, "w_post", (D,), device, (_BF16, _F32)) if w_post is not None else None
     r = _result(out, "r", shape, x.dtype, device) if branch is not None else None
     y = _result(out, "y", shape, _BF16, device) if wp is not None else None
-    rp = _result(out, "rstd_pre", (M,), _F32, device, True) if wp is not None else None
-    rq = _result(out, "rstd_post", (M,), _F32, device, True) if wq is not None else None
+    rp = _result_packed(out, "rstd_pre", (M,), _F32, device) if wp is not None else None
+    rq = _result_packed(out, "rstd_post", (M,), _F32, device) if wq is not None else None
     a = NormFwdArgs(fmt, wf, alpha, w_offset, eps, 0, M, D, gates, ld_x, ld_b, ld_g, _ld(r), _ld(y), x.data_ptr(), _p(branch), _p(gate),
                     wp, wq, _p(r), _p(y), _p(rp), _p(rq))
     _call("glu_block_norm_fwd", a, _handle(stream, device, r, y, rp, rq))
@@ -252,7 +285,8 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     if r.dim() != 2:
         raise ValueError("r must be a matrix")
     device = _device(r, "r")
-    M, D = shape = r.shape
+    M, D = r.shape
+    shape = (M, D)
     fmt = _stream_fmt(r, "r")
     wf = _weight_fmt(w_pre, w_post)
     ld_r = _matrix(r, "r", shape, device, r.dtype)
@@ -268,11 +302,11 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     rq = _packed(rstd_post, "rstd_post", (M,), device, (_F32,)) if rstd_post is not None else None
     dx = _result(out, "dx", shape, r.dtype, device)
     db = _result(out, "dbranch", shape, _BF16, device) if branch is not None else None
-    dwp = _result(out, "dw_pre", (D,), _F32, device, True) if wp is not None else None
-    dwq = _result(out, "dw_post", (D,), _F32, device, True) if wq is not None else None
-    dg = _result(out, "dgate", (gates, D), _F32, device, True) if gates else None
+    dwp = _result_packed(out, "dw_pre", (D,), _F32, device) if wp is not None else None
+    dwq = _result_packed(out, "dw_post", (D,), _F32, device) if wq is not None else None
+    dg = _result_packed(out, "dgate", (gates, D), _F32, device) if gates else None
     n = _workspace("glu_block_norm_bwd_workspace", M, D, gates)
-    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    ws = _scratch(n)
     a = NormBwdArgs(fmt, wf, alpha, w_offset, M, D, gates, ld_r, ld_b, ld_g, ld_dy, ld_dr, _ld(dx), _ld(db), r.data_ptr(), _p(branch), _p(gate),
                     wp, wq, rp, rq, _p(dy), _p(dr), dx.data_ptr(), _p(db), _p(dwp), _p(dwq), _p(dg), ws.data_ptr(), n)
     _call("glu_block_norm_bwd", a, _handle(stream, device, dx, db, dwp, dwq, dg, ws))
@@ -288,13 +322,14 @@ def route(ids, n_experts, *, out=None, stream=None) -> dict:
     device = _device(ids, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, choices]")
-    T, K = shape = ids.shape
+    T, K = ids.shape
+    shape = (T, K)
     p = _packed(ids, "ids", shape, device, (torch.int64, _I32))
-    slot = _result(out, "slot", shape, _I32, device, True)
-    src = _result(out, "src", (T * K,), _I32, device, True)
-    offsets = _result(out, "offsets", (n_experts + 1,), _I32, device, True)
+    slot = _result_packed(out, "slot", shape, _I32, device)
+    src = _result_packed(out, "src", (T * K,), _I32, device)
+    offsets = _result_packed(out, "offsets", (n_experts + 1,), _I32, device)
     n = _workspace("glu_block_route_workspace", T, K, n_experts)
-    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    ws = _scratch(n)
     a = RouteArgs(8 if ids.dtype is torch.int64 else 4, n_experts, T, K, p, slot.data_ptr(), src.data_ptr(), offsets.data_ptr(), _p(ws), n)
     _call("glu_block_route", a, _handle(stream, device, slot, src, offsets, ws))
     return {"slot": slot, "src": src, "offsets": offsets}
@@ -352,7 +387,7 @@ def combine_bwd(dout, ys, route, weights, *, out=None, stream=None) -> dict:
     ld_rows = _matrix(ys, "ys", (T * K, D), device)
     w = _packed(weights, "weights", (T, K), device, (_F32,))
     dys = _result(out, "dys", (T * K, D), _BF16, device)
-    dw = _result(out, "dw", (T, K), _F32, device, True)
+    dw = _result_packed(out, "dw", (T, K), _F32, device)
     a = RowsArgs(T, K, D, ld, ld_rows, _ld(dys), 0, slot, src, w, dout.data_ptr(), ys.data_ptr(), None, None, dys.data_ptr(), dw.data_ptr())
     _call("glu_block_combine_bwd", a, _handle(stream, device, dys, dw))
     return {"dys": dys, "dw": dw}
@@ -388,9 +423,12 @@ def linear(x, w, *, bias=None, act=ACT_IDENTITY, residual=None, offsets=None, ke
     z = _result(out, "z", (M, N), _BF16, device) if keep_z else None
     a = LinearFwdArgs(act, FMT_FP32 if bias is not None and bias.dtype is _F32 else FMT_BF16, E, 0, M, N, K, ld_x, ld_w, stride_w, ld_res,
                       _ld(y), _ld(z), x.data_ptr(), w.data_ptr(), b, _p(residual), off, y.data_ptr(), _p(z), None, 0)
-    n = _workspace("glu_block_linear_fwd_workspace", a)
-    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
-    a.workspace, a.workspace_bytes = _p(ws), n
+    ws = None
+    if E == 0 and M > 16:  # by expert and for few rows it takes none
+        n = _workspace("glu_block_linear_fwd_workspace", a)
+        if n:
+            ws = _scratch(n)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), n
     _call("glu_block_linear_fwd", a, _handle(stream, device, y, z, ws))
     return {"y": y, "z": z}
 
@@ -408,14 +446,14 @@ def linear_bwd(dy, x, w, *, z=None, act=ACT_IDENTITY, offsets=None, need_dx=True
     ld_dy = _matrix(dy, "dy", (M, N), device)
     ld_z = _matrix(z, "z", (M, N), device) if z is not None else 0
     dx = _result(out, "dx", (M, K), _BF16, device) if need_dx else None
-    dw = _result(out, "dw", w.shape, _BF16, device) if need_dw else None
-    db = _result(out, "db", (E, N) if E else (N,), _F32, device, True) if need_db else None
+    dw = _result(out, "dw", tuple(w.shape), _BF16, device) if need_dw else None
+    db = _result_packed(out, "db", (E, N) if E else (N,), _F32, device) if need_db else None
     ld_dw = _ld(dw)
     stride_dw = 0 if dw is None or not E else dw.stride(0) if E > 1 else N * ld_dw
     a = LinearBwdArgs(act, E, M, N, K, ld_dy, ld_z, ld_x, ld_w, stride_w, _ld(dx), ld_dw, stride_dw, dy.data_ptr(), _p(z), x.data_ptr(), w.data_ptr(),
                       off, _p(dx), _p(dw), _p(db), None, 0)
     n = _workspace("glu_block_linear_bwd_workspace", a)
-    ws = torch.empty(n, dtype=torch.uint8, device=device) if n else None
+    ws = _scratch(n)
     a.workspace, a.workspace_bytes = _p(ws), n
     _call("glu_block_linear_bwd", a, _handle(stream, device, dx, dw, db, ws))
     return {"dx": dx, "dw": dw, "db": db}

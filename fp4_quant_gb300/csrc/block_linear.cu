@@ -338,7 +338,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
 
   if (threadIdx.x == 32) {
     prefetch_tensormap(&p.ta);
-    prefetch_tensormap(&p.tb[0]);
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
@@ -675,7 +674,8 @@ cudaError_t pairs_at_once(const void* kern, int threads, const DevInfo& d, int* 
 template <int PROD, int ACT>
 cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   auto kern = linear_kernel<PROD, ACT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), kSmem);
   if (e != cudaSuccess) return e;
   p.n_at = (p.width + kTile - 1) / kTile;
   // by expert the device counts the tiles: no more than one token tile per
@@ -739,9 +739,15 @@ size_t linear_bwd_workspace(const glu_block_linear_bwd_args& a) {
 }
 
 // Maps of the tokens' rows (64-wide slices), in boxes of 128, 64 and 32 rows.
-static cudaError_t token_maps(LinearP& p, const void* t, int64_t cols, int64_t rows, int64_t ld) {
+// Dense tiles are alike but for the last, which has no more columns: theirs and
+// the narrower ones; by expert any.
+static cudaError_t token_maps(LinearP& p, const void* t, int64_t cols, int64_t rows, int64_t ld, int most) {
+  const int64_t tiles = (rows + most - 1) / most, half = ((rows + tiles - 1) / tiles + kStep - 1) / kStep * kStep / 2;
   cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = make_tile_map(&p.tb[i], t, 2, cols, rows, ld * 2, kBK, kHalf >> i, 128);
+  for (int i = p.offsets || half > 64 ? 0 : half > 32 ? 1 : 2; i < 3 && e == cudaSuccess; ++i) {
+    e = make_tile_map(&p.tb[i], t, 2, cols, rows, ld * 2, kBK, kHalf >> i, 128);
+    if (!p.offsets && rows % (2 * half) == 0) break;  // no narrower last tile
+  }
   return e;
 }
 
@@ -751,14 +757,14 @@ cudaError_t launch_linear_fwd(const glu_block_linear_fwd_args& a, cudaStream_t s
   memset(&p, 0, sizeof p);
   const int64_t E = a.E > 0 ? a.E : 1;
   cudaError_t e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kHalf);
-  if (e == cudaSuccess) e = token_maps(p, a.x, a.K, a.M, a.ld_x);
-  if (e != cudaSuccess) return e;
+  const TokenPlan plan = fwd_plan(a);
   p.offsets = a.E > 0 ? a.offsets : nullptr;
+  if (e == cudaSuccess) e = token_maps(p, a.x, a.K, a.M, a.ld_x, plan.most);
+  if (e != cudaSuccess) return e;
   p.E = int32_t(E);
   p.rows = int32_t(a.M);
   p.width = int32_t(a.N);
   p.depth = int32_t(a.K);
-  const TokenPlan plan = fwd_plan(a);
   p.splits = plan.splits;
   p.most = plan.most;
   p.part = static_cast<float*>(a.workspace);
@@ -816,11 +822,11 @@ cudaError_t launch_linear_bwd(const glu_block_linear_bwd_args& a, cudaStream_t s
   p.rows = int32_t(a.M);
   if (a.dx) {
     e = make_stack_map(&p.ta, a.w, a.K, a.N, a.ld_w * 2, E, (a.E > 0 ? a.stride_w : a.N * a.ld_w) * 2, kBK);
-    if (e == cudaSuccess) e = token_maps(p, dz, a.N, a.M, ld_dz);
+    const TokenPlan plan = dx_plan(a);
+    if (e == cudaSuccess) e = token_maps(p, dz, a.N, a.M, ld_dz, plan.most);
     if (e != cudaSuccess) return e;
     p.width = int32_t(a.K);
     p.depth = int32_t(a.N);
-    const TokenPlan plan = dx_plan(a);
     p.splits = plan.splits;
     p.most = plan.most;
     p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + dz_bytes(a));

@@ -125,7 +125,8 @@ template <int ACT, int TT, int DEEP>
 cudaError_t launch_few_d(const FewP& p, cudaStream_t s) {
   constexpr int smem = few_smem<TT, DEEP>();
   auto kern = few_kernel<ACT, TT, DEEP>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, unsigned((p.N + 15) / 16), kFewWarps * 32, smem, s, p);
 }

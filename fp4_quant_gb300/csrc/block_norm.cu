@@ -323,7 +323,8 @@ cudaError_t launch_fwd_rows(NormFwdP p, cudaStream_t s, const DevInfo& d) {
   const int smem = kCtlBytes + p.stages * p.stage_bytes;
   if (smem > kSmemMost) return cudaErrorInvalidValue;
   auto kern = p.D % 8 != 0 ? norm_fwd_kernel<XT, V, true> : norm_fwd_kernel<XT, V, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit[2];
+  const cudaError_t e = limit[p.D % 8 != 0].raise(reinterpret_cast<const void*>(kern), kSmemMost);
   if (e != cudaSuccess) return e;
   const int64_t most = int64_t(d.sms) * blocks;
   return launch_kernel(kern, int(p.M < most ? p.M : most), threads, smem, s, p);
@@ -665,7 +666,8 @@ cudaError_t launch_bwd_v(NormBwdP p, const NormBwdPlan& q, cudaStream_t s) {
   const int smem = kCtlBytes + p.stages * p.stage_bytes;
   if (smem > kSmemMost) return cudaErrorInvalidValue;
   auto kern = p.D % 8 != 0 ? norm_bwd_kernel<XT, V, MANY, true> : norm_bwd_kernel<XT, V, MANY, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit[2];
+  const cudaError_t e = limit[p.D % 8 != 0].raise(reinterpret_cast<const void*>(kern), kSmemMost);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, q.grid, q.threads, smem, s, p);
 }

@@ -347,7 +347,8 @@ cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s) {
   p.id_bytes = a.id_bytes;
   p.blocks = int32_t((p.n + p.per_block - 1) / p.per_block);
   const int smem = kSortWarps * a.E * 4;
-  cudaError_t e = cudaFuncSetAttribute(route_place_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(route_place_kernel), kSortWarps * kMaxExperts * 4);
   if (e != cudaSuccess) return e;
   if (p.blocks > 1) e = launch_kernel(route_count_kernel, p.blocks, kSortThreads, 0, s, p);
   if (e != cudaSuccess) return e;

@@ -3,12 +3,32 @@
 // reductions of a warp and a block in a fixed order.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
 #include "glu_quant.h"
 
 namespace gq {
+
+// Raises a kernel's limit of dynamic shared memory, once per device: one object
+// per kernel, static where it is launched (the call costs as much as a launch).
+class SmemLimit {
+ public:
+  cudaError_t raise(const void* kern, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < kDevices && set_[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < kDevices) set_[dev].store(bytes, std::memory_order_relaxed);
+    return e;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<int> set_[kDevices] = {};
+};
 
 // Launches a kernel of one parameter block; the launch's own error only.
 template <typename P>
