@@ -361,6 +361,18 @@ struct NormBwdP {
   int w32, stages, stage_bytes;
 };
 
+// A chunk of sums, [.., D] contiguous: rows start on 16 bytes unless RAGGED.
+template <bool RAGGED>
+__device__ __forceinline__ void store_sums(float* row, int c, int D, const F8& v) {
+  if (!RAGGED) {
+    store8<false>(row + c, 8, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < D) row[c + i] = (i & 1) ? v.v[i / 2].y : v.v[i / 2].x;
+  }
+}
+
 // A thread has the same columns of every row of its block, so the sums over
 // rows stay in its registers.  With w = w_pre + o, h = alpha gate (w_post + o)
 // (or alpha gate), t = dr + rstd_pre dy w and b = branch:
@@ -453,9 +465,16 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
     const int64_t m0 = base + piece * p.rows_per_gate / p.pieces;
     XT* dx = static_cast<XT*>(p.dx) + m0 * p.ld_dx;
     uint16_t* db = p.dbranch + m0 * p.ld_dbranch;
+    float rs32 = 0.0f, rp32 = 1.0f;  // lane l: the rstd of the l-th of 32 rows, loaded together
     for (int64_t m = m0; m < m1; ++m, dx += p.ld_dx, db += p.ld_dbranch) {
       const uint8_t* st = stages + s * p.stage_bytes;
-      const float rs = pre ? p.rstd_pre[m] : 0.0f, rp = post ? p.rstd_post[m] : 1.0f;
+      const int row32 = int(m - m0) & 31;
+      if (row32 == 0) {
+        const int64_t ml = m + (tid & 31);
+        if (pre && ml < m1) rs32 = p.rstd_pre[ml];
+        if (post && ml < m1) rp32 = p.rstd_post[ml];
+      }
+      const float rs = __shfl_sync(0xFFFFFFFFu, rs32, row32), rp = __shfl_sync(0xFFFFFFFFu, rp32, row32);
       auto h_of = [&](int k, int c) {
         F8 f = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
         if (MANY) {
@@ -530,18 +549,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
         for (int k = 0; k < V; ++k) {
           const int c = 8 * (tid + k * threads);
           if (c >= D) continue;
-          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D), hk = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
-          float out[8];
+          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+          F8 out = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             a_post[MANY ? k : 0].v[i] = fma_2(mul_2(g.v[i], both(p.alpha)), a_x[k].v[i], a_post[MANY ? k : 0].v[i]);
-            const float2 q = mul_2(hk.v[i], a_x[k].v[i]);
-            out[2 * i] = q.x;
-            out[2 * i + 1] = q.y;
+            out.v[i] = mul_2(out.v[i], a_x[k].v[i]);
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            if (c + i < D) p.dgate[grp * D + c + i] = out[i];
+          store_sums<RAGGED>(p.dgate + grp * D, c, D, out);
           a_x[k] = zeros();
         }
       }
@@ -557,10 +572,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int c = 8 * (tid + k * threads);
-        const float v[8] = {a_x[k].v[0].x, a_x[k].v[0].y, a_x[k].v[1].x, a_x[k].v[1].y, a_x[k].v[2].x, a_x[k].v[2].y, a_x[k].v[3].x, a_x[k].v[3].y};
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          if (c + i < D) p.part_x[it * D + c + i] = v[i];
+        if (c < D) store_sums<RAGGED>(p.part_x + it * D, c, D, a_x[k]);
         a_x[k] = zeros();
       }
     }
@@ -568,18 +580,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
 #pragma unroll
   for (int k = 0; k < V; ++k) {
     const int c = 8 * (tid + k * threads);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (c + i >= D) continue;
-      if (pre) p.part_pre[int64_t(blockIdx.x) * D + c + i] = (i & 1) ? a_pre[k].v[i / 2].y : a_pre[k].v[i / 2].x;
-      if (MANY && post)
-        p.part_post[int64_t(blockIdx.x) * D + c + i] = (i & 1) ? a_post[MANY ? k : 0].v[i / 2].y : a_post[MANY ? k : 0].v[i / 2].x;
-    }
+    if (c >= D) continue;
+    if (pre) store_sums<RAGGED>(p.part_pre + int64_t(blockIdx.x) * D, c, D, a_pre[k]);
+    if (MANY && post) store_sums<RAGGED>(p.part_post + int64_t(blockIdx.x) * D, c, D, a_post[MANY ? k : 0]);
   }
 }
 
-// The sums over blocks and items, in a fixed order: 32 columns per block, 16
-// threads per column.  blockIdx.y: dw_pre, dw_post, then the gate rows.
+// The sums over blocks and items, in a fixed order: 32 columns per block, 32
+// threads per column, eight loads of each in flight.  blockIdx.y: dw_pre, dw_post, then the gate rows.
 struct JoinP {
   const float *part_pre, *part_post, *part_x;
   const uint16_t* gate;
@@ -589,8 +597,8 @@ struct JoinP {
   int blocks, w32;
   float alpha, w_offset;
 };
-__global__ void __launch_bounds__(512) join_kernel(const JoinP p) {
-  __shared__ float sh[16][33];
+__global__ void __launch_bounds__(1024) join_kernel(const JoinP p) {
+  __shared__ float sh[32][33];
   int64_t y = blockIdx.y;
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x;
   int what = 2;  // 0: dw_pre, 1: dw_post, 2: gate row y
@@ -599,15 +607,18 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinP p) {
   float v = 0.0f;
   if (c < p.D) {
     if (what == 2) {
-      for (int64_t i = threadIdx.y; i < p.pieces; i += 16) v += p.part_x[(y * p.pieces + i) * p.D + c];
+#pragma unroll 8
+      for (int64_t i = threadIdx.y; i < p.pieces; i += 32) v += p.part_x[(y * p.pieces + i) * p.D + c];
     } else if (what == 1 && p.part_x) {
-      for (int64_t i = threadIdx.y; i < p.items; i += 16) {
+#pragma unroll 8
+      for (int64_t i = threadIdx.y; i < p.items; i += 32) {
         const float x = p.part_x[i * p.D + c];
         v = p.gate ? fmaf(bf16_of_bits(p.gate[i / p.pieces * p.ld_gate + c]), x, v) : v + x;
       }
     } else {
       const float* q = what == 0 ? p.part_pre : p.part_post;
-      for (int64_t i = threadIdx.y; i < p.blocks; i += 16) v += q[i * p.D + c];
+#pragma unroll 8
+      for (int64_t i = threadIdx.y; i < p.blocks; i += 32) v += q[i * p.D + c];
     }
   }
   sh[threadIdx.y][threadIdx.x] = v;
@@ -615,7 +626,7 @@ __global__ void __launch_bounds__(512) join_kernel(const JoinP p) {
   if (threadIdx.y != 0 || c >= p.D) return;
   v = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) v += sh[i][threadIdx.x];
+  for (int i = 0; i < 32; ++i) v += sh[i][threadIdx.x];
   if (what == 0) {
     p.dw_pre[c] = v;
   } else if (what == 1) {
@@ -770,7 +781,7 @@ cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s) {
   j.w_offset = a.w_offset;
   const int64_t rows = (a.dw_pre ? 1 : 0) + (a.dw_post ? 1 : 0) + (j.dgate ? a.gates : 0);
   if (rows == 0) return cudaSuccess;
-  return launch_kernel(join_kernel, dim3(unsigned((a.D + 31) / 32), unsigned(rows)), dim3(32, 16), 0, s, j);
+  return launch_kernel(join_kernel, dim3(unsigned((a.D + 31) / 32), unsigned(rows)), dim3(32, 32), 0, s, j);
 }
 
 cudaError_t read_err_norm(uint32_t* v, bool clear) {
