@@ -294,8 +294,6 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     ld_dy = _matrix(dy, "dy", shape, device) if dy is not None else 0
     ld_dr = _matrix(dr, "dr", shape, device, r.dtype) if dr is not None else 0
     gates, ld_g = _gate(gate, D, device)
-    if gates and M % gates != 0:
-        raise ValueError(f"{gates} gate rows do not divide {M} rows")
     wp = _packed(w_pre, "w_pre", (D,), device, (_BF16, _F32)) if w_pre is not None else None
     wq = _packed(w_post, "w_post", (D,), device, (_BF16, _F32)) if w_post is not None else None
     rp = _packed(rstd_pre, "rstd_pre", (M,), device, (_F32,)) if rstd_pre is not None else None

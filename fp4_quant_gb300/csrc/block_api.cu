@@ -132,11 +132,13 @@ int check_rows(const glu_block_rows_args* a, RowsOp op) {
   return c.status;
 }
 
-// Sizes of a linear layer: 32-bit TMA coordinates, and tiles counted in 31 bits.
+// Sizes of a linear layer: 32-bit TMA coordinates, grids over N and K, and tiles
+// counted in 31 bits.
 int check_linear_size(int64_t M, int64_t N, int64_t K, int32_t E) {
   if (M <= 0 || N <= 0 || K <= 0 || E < 0) return GLU_EINVAL;
   constexpr int64_t kMost = INT32_MAX - 1024;
-  if (M > kMost || N > kMost || K > kMost || E > gq::kMaxExperts) return GLU_ESHAPE;
+  constexpr int64_t kWidest = int64_t(1) << 23;
+  if (M > kMost || N > kWidest || K > kWidest || E > gq::kMaxExperts) return GLU_ESHAPE;
   const int64_t m = M / 128 + 1 + E, n = N / 128 + 1, k = K / 128 + 1, most = int64_t(1) << 30;
   return m * n > most || m * k > most || n * k * (E > 0 ? E : 1) > most ? GLU_ESHAPE : GLU_OK;
 }

@@ -176,7 +176,7 @@ GLU_API int glu_block_combine_bwd(const glu_block_rows_args* args, void* stream)
  * By expert: E > 0, W [E, N, K] (stride_w elements between experts), bias
  * [E, N], and offsets [E + 1] (device int32, from 0, not falling): rows
  * offsets[e] .. offsets[e + 1] - 1 of x take W[e]; rows from offsets[E] on
- * give y = z = 0.  Dense: E = 0, offsets NULL.  E <= 1024.
+ * give y = z = 0.  Dense: E = 0, offsets NULL.  E <= 1024, N and K <= 2^23.
  * The workspace (16-byte aligned; NULL where the query says 0 bytes) joins
  * the parts of long sums that are split when there are few rows. */
 typedef struct glu_block_linear_fwd_args {

@@ -567,3 +567,31 @@ def test_refused_tensors():
 def test_no_wait_gave_up():
     torch.cuda.synchronize()
     assert G.block_device_errors() == (G.GLU_OK, 0)
+
+
+# ---- further shapes: rows through the ring, split sums, many experts -------------
+
+@pytest.mark.parametrize("M,D,stream,wt,branch,post,gates,alpha,o", [
+    (1000, 1032, BF, BF, True, True, 4, 1.0, 0.0), (611, 2056, F32, F32, True, True, 1, 0.5, 1.0), (640, 4096, BF, F32, True, False, 0, 1.0, 0.0),
+    (2000, 515, F32, BF, False, False, 0, 1.0, 0.0), (310, 20000, F32, BF, True, True, 310, 1.0, 1.0), (500, 8192, BF, BF, True, True, 125, 1.0, 0.0)])
+def test_norm_rows_through_the_ring(M, D, stream, wt, branch, post, gates, alpha, o):
+    test_norm_forward(M, D, stream, wt, branch, post, gates, alpha, o)
+    if D <= 16384:
+        test_norm_backward(M, D, stream, wt, branch, post, gates, alpha, o, True)
+
+
+@pytest.mark.parametrize("M,N,K,act,bias,residual,keep", [
+    (9, 520, 4096, "silu", BF, True, True), (16, 16400, 264, "gelu_erf", F32, True, False), (17, 600, 2048, "gelu_tanh", F32, True, True),
+    (40, 1001, 4103, "relu", BF, True, True), (200, 2048, 1536, "none", None, True, False), (600, 3001, 1032, "silu", F32, False, True)])
+def test_linear_of_few_rows(M, N, K, act, bias, residual, keep):
+    test_linear_forward(M, N, K, act, bias, residual, keep)
+    test_linear_backward(M, N, K, act)
+
+
+def test_linear_with_the_most_experts():
+    test_linear_by_expert([3, 0, 17, 1] * 256, 2, 136, 72, "silu")
+
+
+def test_rows_of_many_choices():
+    """More than eight choices per token, and more than one block of the sort."""
+    test_rows_there_and_back(700, 11, 24, 0.1, 264)
