@@ -336,6 +336,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
+  after_previous();
   if (threadIdx.x == 32) {
     prefetch_tensormap(&p.ta);
     for (int s = 0; s < kStages; ++s) {
@@ -686,7 +687,7 @@ cudaError_t launch_t(LinearP& p, cudaStream_t s, const DevInfo& d) {
   e = pairs_at_once(reinterpret_cast<const void*>(kern), threads_of(PROD == kGradW), d, &pairs);
   if (e != cudaSuccess) return e;
   if (most < pairs) pairs = int(most);
-  return launch_kernel(kern, 2 * pairs, threads_of(PROD == kGradW), kSmem, s, p);
+  return launch_kernel(kern, 2 * pairs, threads_of(PROD == kGradW), kSmem, s, p, true);
 }
 
 // How the tokens of a dense y or dx are cut into tiles (at most `most` each)

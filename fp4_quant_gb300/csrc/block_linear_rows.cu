@@ -60,6 +60,7 @@ __global__ void __launch_bounds__(kFewWarps * 32) few_kernel(const FewP p) {
   const uint16_t* w0 = p.w + int64_t(min(n0 + g, p.N - 1)) * p.ld_w;
   const uint16_t* w1 = p.w + int64_t(min(n0 + g + 8, p.N - 1)) * p.ld_w;
   float c[TT][4] = {};
+  after_previous();
   // this warp's part of K, in steps of 32
   const int32_t steps = (p.K + 31) / 32, s0 = steps * warp / kFewWarps, s1 = steps * (warp + 1) / kFewWarps;
   uint4* mine = ring + warp * DEEP * (2 + TT) * 32 + lane;
@@ -128,7 +129,7 @@ cudaError_t launch_few_d(const FewP& p, cudaStream_t s) {
   static SmemLimit limit;
   const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, unsigned((p.N + 15) / 16), kFewWarps * 32, smem, s, p);
+  return launch_kernel(kern, unsigned((p.N + 15) / 16), kFewWarps * 32, smem, s, p, true);
 }
 
 // Slots by how many blocks share an SM: what is in flight per SM stays about
@@ -160,6 +161,7 @@ struct JoinP {
 template <int ACT>
 __global__ void __launch_bounds__(256) linear_join_kernel(const JoinP p) {
   const int64_t chunks = (p.N + 7) / 8, q = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  after_previous();
   if (q >= p.M * chunks) return;
   const int64_t m = q / chunks;
   const int32_t c = int32_t(q % chunks) * 8, left = int32_t(p.N) - c;
@@ -211,6 +213,7 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
   __shared__ float sh[8][kDzCols + 8];
   const int32_t slot = blockIdx.x;
   int32_t e = 0, r0 = 0, r1 = p.rows, part = slot;
+  after_previous();
   if (p.offsets) {
     int32_t lo = 0, hi = p.E - 1;
     while (lo < hi) {
@@ -271,6 +274,7 @@ __global__ void __launch_bounds__(512) db_kernel(const DzP p) {
   __shared__ float sh[16][33];
   const int32_t e = blockIdx.y, c = blockIdx.x * 32 + threadIdx.x;
   int32_t r0 = 0, r1 = p.rows, first = 0;
+  after_previous();
   if (p.offsets) {
     r0 = cut_at(p.offsets, e, p.rows);
     r1 = max(r0, cut_at(p.offsets, e + 1, p.rows));
@@ -342,7 +346,7 @@ cudaError_t launch_linear_join(const glu_block_linear_fwd_args& a, const float* 
               : a.act == GLU_ACT_RELU      ? linear_join_kernel<GLU_ACT_RELU>
               : a.act == GLU_ACT_GELU_ERF  ? linear_join_kernel<GLU_ACT_GELU_ERF>
                                            : linear_join_kernel<GLU_ACT_IDENTITY>;
-  return launch_kernel(kern, dim3(unsigned((a.M * ((a.N + 7) / 8) + 255) / 256)), 256, 0, s, p);
+  return launch_kernel(kern, dim3(unsigned((a.M * ((a.N + 7) / 8) + 255) / 256)), 256, 0, s, p, true);
 }
 
 cudaError_t launch_linear_dz(int act, const DzP& q, cudaStream_t s) {
@@ -351,9 +355,9 @@ cudaError_t launch_linear_dz(int act, const DzP& q, cudaStream_t s) {
               : act == GLU_ACT_RELU      ? dz_kernel<GLU_ACT_RELU>
               : act == GLU_ACT_GELU_ERF  ? dz_kernel<GLU_ACT_GELU_ERF>
                                          : dz_kernel<GLU_ACT_IDENTITY>;
-  const cudaError_t e = launch_kernel(kern, dim3(unsigned(q.slots), unsigned((q.N + kDzCols - 1) / kDzCols)), dim3(32, 8), 0, s, q);
+  const cudaError_t e = launch_kernel(kern, dim3(unsigned(q.slots), unsigned((q.N + kDzCols - 1) / kDzCols)), dim3(32, 8), 0, s, q, true);
   if (e != cudaSuccess || q.db == nullptr) return e;
-  return launch_kernel(db_kernel, dim3(unsigned((q.N + 31) / 32), unsigned(q.E)), dim3(32, 16), 0, s, q);
+  return launch_kernel(db_kernel, dim3(unsigned((q.N + 31) / 32), unsigned(q.E)), dim3(32, 16), 0, s, q, true);
 }
 
 }  // namespace gq

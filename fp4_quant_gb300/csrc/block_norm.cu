@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_row_kernel(const NormFwdP p) {
   const int D = int(p.D), c = 8 * int(threadIdx.x), threads = blockDim.x;
   const int64_t m = blockIdx.x;
   const float per_d = __frcp_rn(float(D));
+  after_previous();
   F8 r = zeros(), b = zeros(), w = zeros();
   float2 s2 = make_float2(0.0f, 0.0f);
   if (c < D) {
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_row_kernel(const NormFwdP p) {
 template <typename XT, int V, bool RAGGED>
 __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  after_previous();
   RingCtl<2>* ctl = reinterpret_cast<RingCtl<2>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
@@ -327,13 +329,13 @@ cudaError_t launch_fwd_rows(NormFwdP p, cudaStream_t s, const DevInfo& d) {
   const cudaError_t e = limit[p.D % 8 != 0].raise(reinterpret_cast<const void*>(kern), kSmemMost);
   if (e != cudaSuccess) return e;
   const int64_t most = int64_t(d.sms) * blocks;
-  return launch_kernel(kern, int(p.M < most ? p.M : most), threads, smem, s, p);
+  return launch_kernel(kern, int(p.M < most ? p.M : most), threads, smem, s, p, true);
 }
 
 template <typename XT>
 cudaError_t launch_fwd_t(const NormFwdP& p, cudaStream_t s, const DevInfo& d) {
   const int64_t chunks = (p.D + 7) / 8;
-  if (p.M <= 2 * d.sms && chunks <= 1024) return launch_kernel(norm_fwd_row_kernel<XT>, int(p.M), row_threads(chunks, 1), 0, s, p);
+  if (p.M <= 2 * d.sms && chunks <= 1024) return launch_kernel(norm_fwd_row_kernel<XT>, int(p.M), row_threads(chunks, 1), 0, s, p, true);
   switch (row_chunks(chunks)) {
     case 1: return launch_fwd_rows<XT, 1>(p, s, d);
     case 2: return launch_fwd_rows<XT, 2>(p, s, d);
@@ -392,6 +394,7 @@ __device__ __forceinline__ void store_sums(float* row, int c, int D, const F8& v
 template <typename XT, int V, bool MANY, bool RAGGED>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  after_previous();
   RingCtl<3>* ctl = reinterpret_cast<RingCtl<3>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
@@ -602,6 +605,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const JoinP p) {
   int64_t y = blockIdx.y;
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x;
   int what = 2;  // 0: dw_pre, 1: dw_post, 2: gate row y
+  after_previous();
   if (p.dw_pre) what = y-- == 0 ? 0 : 2;
   if (what == 2 && p.dw_post) what = y-- == 0 ? 1 : 2;
   float v = 0.0f;
@@ -680,7 +684,7 @@ cudaError_t launch_bwd_v(NormBwdP p, const NormBwdPlan& q, cudaStream_t s) {
   static SmemLimit limit[2];
   const cudaError_t e = limit[p.D % 8 != 0].raise(reinterpret_cast<const void*>(kern), kSmemMost);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, q.grid, q.threads, smem, s, p);
+  return launch_kernel(kern, q.grid, q.threads, smem, s, p, true);
 }
 
 template <typename XT, bool MANY>
@@ -781,7 +785,7 @@ cudaError_t launch_norm_bwd(const glu_block_norm_bwd_args& a, cudaStream_t s) {
   j.w_offset = a.w_offset;
   const int64_t rows = (a.dw_pre ? 1 : 0) + (a.dw_post ? 1 : 0) + (j.dgate ? a.gates : 0);
   if (rows == 0) return cudaSuccess;
-  return launch_kernel(join_kernel, dim3(unsigned((a.D + 31) / 32), unsigned(rows)), dim3(32, 32), 0, s, j);
+  return launch_kernel(join_kernel, dim3(unsigned((a.D + 31) / 32), unsigned(rows)), dim3(32, 32), 0, s, j, true);
 }
 
 cudaError_t read_err_norm(uint32_t* v, bool clear) {

@@ -36,6 +36,7 @@ __device__ __forceinline__ int id_at(const RouteP& p, int64_t j) {
 
 __global__ void __launch_bounds__(kSortThreads) route_count_kernel(const RouteP p) {
   __shared__ int32_t h[kMaxExperts];
+  after_previous();
   for (int e = threadIdx.x; e < p.E; e += kSortThreads) h[e] = 0;
   __syncthreads();
   const int64_t j0 = int64_t(blockIdx.x) * p.per_block, j1 = min(p.n, j0 + p.per_block);
@@ -82,6 +83,7 @@ __global__ void __launch_bounds__(kSortThreads) route_place_kernel(const RouteP 
   // totals, and what the blocks before this one have of them (whole numbers:
   // the order of the additions does not matter)
   if (int(threadIdx.x) < p.E) all[threadIdx.x] = base[threadIdx.x] = 0;
+  after_previous();
   __syncthreads();
   if (p.blocks == 1) {
     for (int64_t j = threadIdx.x; j < p.n; j += kSortThreads) {
@@ -200,6 +202,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) dispatch_kernel(const RowsP p)
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
   const int64_t parts = (p.D + 256 * C - 1) / (256 * C);
+  after_previous();
   for (int64_t u = wid; u < p.T * parts; u += warps) {
     const int64_t t = u / parts;
     const int c0 = int(u % parts) * 256 * C + 8 * lane, D = int(p.D);
@@ -228,6 +231,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) combine_kernel(const RowsP p) 
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
   const int64_t parts = (p.D + 255) / 256;
+  after_previous();
   for (int64_t u = wid; u < p.T * parts; u += warps) {
     const int64_t t = u / parts;
     const int c = int(u % parts) * 256 + 8 * lane, left = int(p.D) - c;
@@ -262,6 +266,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) combine_kernel(const RowsP p) 
 __global__ void __launch_bounds__(kRowWarps * 32) combine_bwd_kernel(const RowsP p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = int64_t(blockIdx.x) * kRowWarps + (threadIdx.x >> 5), warps = int64_t(gridDim.x) * kRowWarps;
+  after_previous();
   for (int64_t t = wid; t < p.T; t += warps)
     for (int64_t k0 = 0; k0 < p.K; k0 += 8) {
       const Places at = places_of(p, t, k0, lane);
@@ -350,9 +355,9 @@ cudaError_t launch_route(const glu_block_route_args& a, cudaStream_t s) {
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(route_place_kernel), kSortWarps * kMaxExperts * 4);
   if (e != cudaSuccess) return e;
-  if (p.blocks > 1) e = launch_kernel(route_count_kernel, p.blocks, kSortThreads, 0, s, p);
+  if (p.blocks > 1) e = launch_kernel(route_count_kernel, p.blocks, kSortThreads, 0, s, p, true);
   if (e != cudaSuccess) return e;
-  return launch_kernel(route_place_kernel, p.blocks, kSortThreads, smem, s, p);
+  return launch_kernel(route_place_kernel, p.blocks, kSortThreads, smem, s, p, true);
 }
 
 cudaError_t launch_dispatch(const glu_block_rows_args& a, cudaStream_t s, const DevInfo& d) {
@@ -360,18 +365,18 @@ cudaError_t launch_dispatch(const glu_block_rows_args& a, cudaStream_t s, const 
   // 1024 columns per warp (four loads in flight) where there are enough
   // tokens to fill the SMs that way
   if (p.T * ((p.D + 1023) / 1024) >= int64_t(d.sms) * 32)
-    return launch_kernel(dispatch_kernel<4>, row_grid(p.T * ((p.D + 1023) / 1024), d), kRowWarps * 32, 0, s, p);
-  return launch_kernel(dispatch_kernel<1>, row_grid(p.T * ((p.D + 255) / 256), d), kRowWarps * 32, 0, s, p);
+    return launch_kernel(dispatch_kernel<4>, row_grid(p.T * ((p.D + 1023) / 1024), d), kRowWarps * 32, 0, s, p, true);
+  return launch_kernel(dispatch_kernel<1>, row_grid(p.T * ((p.D + 255) / 256), d), kRowWarps * 32, 0, s, p, true);
 }
 
 cudaError_t launch_combine(const glu_block_rows_args& a, cudaStream_t s, const DevInfo& d) {
   const RowsP p = rows_of(a);
-  return launch_kernel(combine_kernel, row_grid(p.T * ((p.D + 255) / 256), d), kRowWarps * 32, 0, s, p);
+  return launch_kernel(combine_kernel, row_grid(p.T * ((p.D + 255) / 256), d), kRowWarps * 32, 0, s, p, true);
 }
 
 cudaError_t launch_combine_bwd(const glu_block_rows_args& a, cudaStream_t s, const DevInfo& d) {
   const RowsP p = rows_of(a);
-  return launch_kernel(combine_bwd_kernel, row_grid(p.T > p.R / 32 ? p.T : p.R / 32, d), kRowWarps * 32, 0, s, p);
+  return launch_kernel(combine_bwd_kernel, row_grid(p.T > p.R / 32 ? p.T : p.R / 32, d), kRowWarps * 32, 0, s, p, true);
 }
 
 }  // namespace gq

@@ -31,14 +31,28 @@ class SmemLimit {
 };
 
 // Launches a kernel of one parameter block; the launch's own error only.
+// `early`: its blocks may come while the kernel before it on the stream drains;
+// it then begins with after_previous(), before it touches memory.
 template <typename P>
-inline cudaError_t launch_kernel(void (*kern)(const P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p) {
+inline cudaError_t launch_kernel(void (*kern)(const P), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const P& p,
+                                 bool early = false) {
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+// Waits until the kernels before this one on the stream are done and what they
+// wrote is there; lets the next one's blocks come.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
