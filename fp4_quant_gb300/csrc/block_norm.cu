@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_row_kernel(const NormFwdP p) {
   const int64_t m = blockIdx.x;
   const float per_d = __frcp_rn(float(D));
   after_previous();
+  next_may_come();
   F8 r = zeros(), b = zeros(), w = zeros();
   float2 s2 = make_float2(0.0f, 0.0f);
   if (c < D) {
@@ -172,6 +173,7 @@ template <typename XT, int V, bool RAGGED>
 __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   after_previous();
+  next_may_come();
   RingCtl<2>* ctl = reinterpret_cast<RingCtl<2>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
@@ -395,6 +397,7 @@ template <typename XT, int V, bool MANY, bool RAGGED>
 __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   after_previous();
+  next_may_come();
   RingCtl<3>* ctl = reinterpret_cast<RingCtl<3>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
@@ -606,6 +609,7 @@ __global__ void __launch_bounds__(1024) join_kernel(const JoinP p) {
   const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x;
   int what = 2;  // 0: dw_pre, 1: dw_post, 2: gate row y
   after_previous();
+  next_may_come();
   if (p.dw_pre) what = y-- == 0 ? 0 : 2;
   if (what == 2 && p.dw_post) what = y-- == 0 ? 1 : 2;
   float v = 0.0f;

@@ -49,11 +49,13 @@ inline cudaError_t launch_kernel(void (*kern)(const P), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 // Waits until the kernels before this one on the stream are done and what they
-// wrote is there; lets the next one's blocks come.
-__device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// wrote is there.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// The next kernel's blocks may come before this one's leave (they wait for its
+// end).  Only the norms let them: elsewhere blocks that wait took the place of
+// ones that work (the sort of 16384 x 8 assignments and their rows 128 against
+// 113 us, one token's linear layer 22.2 against 19.7 us).
+__device__ __forceinline__ void next_may_come() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   uint32_t r;
