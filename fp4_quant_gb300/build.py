@@ -27,7 +27,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden"]
 UNITS = ["api.cu", "tmap.cu", "fwd_mx.cu", "fwd_mx_b16.cu", "fwd_mx_x.cu", "fwd_mx_erf.cu", "bwd_mx.cu", "bwd_both.cu", "gemm_glu.cu", "plain.cu",
-         "block_api.cu", "block_norm.cu", "block_route.cu", "block_linear.cu", "block_linear_rows.cu"]
+         "block_api.cu", "block_norm.cu", "block_route.cu", "block_linear.cu", "block_linear_rows.cu", "block_tmap.cu"]
 
 
 def _nvcc() -> str:

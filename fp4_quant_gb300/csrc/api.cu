@@ -15,6 +15,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "block.h"
 #include "kernels.h"
 
 namespace {

@@ -32,6 +32,15 @@ struct RingCtl {
 };
 static_assert(sizeof(RingCtl<3>) <= kCtlBytes, "ring control block");
 
+// Copy of `bytes` contiguous bytes (a multiple of 16, both addresses 16-byte
+// aligned) into shared memory, completed on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 // Waits that gave up leave a mark and are not repeated: what follows runs on
 // with whatever the stage holds, within its bounds, to its end.
 struct RingWait {

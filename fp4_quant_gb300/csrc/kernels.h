@@ -14,10 +14,6 @@ struct DevInfo {
   int sms;  // streaming multiprocessors of the current device
 };
 
-// The current device's facts; GLU_OK, or GLU_EDEVICE unless it is a GB300
-// (api.cu).
-int device_info(DevInfo* info);
-
 cudaError_t launch_fwd_mx(const glu_quant_fwd_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_bwd_mx(const glu_quant_bwd_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_bwd_both(const glu_quant_bwd_args& a, cudaStream_t s, const DevInfo& d);  // both directions
@@ -36,9 +32,6 @@ cudaError_t launch_scale_pad(uint8_t* s, int64_t rows, int64_t cols, cudaStream_
 cudaError_t make_tile_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t cols,
                           int64_t rows, int64_t row_stride_bytes, int box_cols, int box_rows,
                           int swizzle_bytes = 0);
-// 3-D descriptor of a stack of bf16 matrices (tmap.cu).
-cudaError_t make_stack_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t row_stride_bytes,
-                           int64_t count, int64_t stride_bytes, int box_rows);
 
 // Error bits recorded by a kernel family (bounded waits that gave up).
 cudaError_t read_err_fwd_mx(uint32_t* v, bool clear);  // (includes the bf16-step kernels' bits)

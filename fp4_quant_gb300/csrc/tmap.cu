@@ -57,21 +57,4 @@ cudaError_t make_tile_map(CUtensorMap* map, const void* base, int elem_bytes, in
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// `count` row-major bf16 matrices of rows x cols, `stride_bytes` apart, loaded
-// in boxes of 64 columns (128 bytes, the 128-byte swizzle) by box_rows rows of
-// one matrix; what lies outside a matrix is filled with zeros.
-cudaError_t make_stack_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t row_stride_bytes,
-                           int64_t count, int64_t stride_bytes, int box_rows) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
-  if (enc == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[3] = {cuuint64_t(cols), cuuint64_t(rows), cuuint64_t(count)};
-  const cuuint64_t strides[2] = {cuuint64_t(row_stride_bytes), cuuint64_t(stride_bytes)};
-  const cuuint32_t box[3] = {64, cuuint32_t(box_rows), 1};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace gq
