@@ -251,10 +251,14 @@ __device__ __forceinline__ void row_barrier(int threads) {
 // buffers), so one barrier per call is enough: a buffer is written again only
 // after the next call's barrier.  Two or three values share the exchanges inside
 // a warp: halves of it first swap values, so that each half or quarter then
-// sums one (5 exchanges instead of 10, 6 instead of 15).
+// sums one (5 exchanges instead of 10, 6 instead of 15).  Up to 32 warps for one
+// value, up to 16 for more: those lie side by side, 16 floats each, so that a
+// lane reads the float of its own number.  (As rows [N][32], read at [lane / 16]
+// [lane % 16], CUDA 13.0's optimiser read every third float where such a call
+// stood ahead of a loop with another.)
 template <int N>
 struct BlockSum {
-  float part[2][N][32];
+  float part[2][N == 1 ? 32 : 16 * N];
 };
 __device__ __forceinline__ void block_sum(BlockSum<1>& s, uint32_t& buf, int threads, float (&v)[1]) {
   const int warps = threads >> 5, lane = threadIdx.x & 31;
@@ -263,7 +267,7 @@ __device__ __forceinline__ void block_sum(BlockSum<1>& s, uint32_t& buf, int thr
     __syncwarp();
     return;
   }
-  float* q = s.part[buf & 1u][0];
+  float* q = s.part[buf & 1u];
   ++buf;
   if (lane == 0) q[threadIdx.x >> 5] = v[0];
   row_barrier(threads);
@@ -271,18 +275,17 @@ __device__ __forceinline__ void block_sum(BlockSum<1>& s, uint32_t& buf, int thr
 }
 __device__ __forceinline__ void block_sum(BlockSum<2>& s, uint32_t& buf, int threads, float (&v)[2]) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  const int warps = threads >> 5, lane = threadIdx.x & 31;  // at most 16 warps
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
   const bool hi = lane & 16;
   float x = (hi ? v[1] : v[0]) + __shfl_xor_sync(kAll, hi ? v[0] : v[1], 16);
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
+  for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);  // lanes 0-15: v[0], 16-31: v[1]
   if (warps > 1) {
-    float(&q)[2][32] = s.part[buf & 1u];
+    float* q = s.part[buf & 1u];
     ++buf;
-    if ((lane & 15) == 0) q[lane >> 4][threadIdx.x >> 5] = x;
+    if ((lane & 15) == 0) q[lane + (threadIdx.x >> 5)] = x;
     row_barrier(threads);
-    const int w = lane & 15;
-    x = w < warps ? q[lane >> 4][w] : 0.0f;
+    x = (lane & 15) < warps ? q[lane] : 0.0f;
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) x += __shfl_xor_sync(kAll, x, o);
   } else {
@@ -293,7 +296,7 @@ __device__ __forceinline__ void block_sum(BlockSum<2>& s, uint32_t& buf, int thr
 }
 __device__ __forceinline__ void block_sum(BlockSum<3>& s, uint32_t& buf, int threads, float (&v)[3]) {
   constexpr uint32_t kAll = 0xFFFFFFFFu;
-  const int warps = threads >> 5, lane = threadIdx.x & 31;  // at most 16 warps
+  const int warps = threads >> 5, lane = threadIdx.x & 31;
   const bool hi = lane & 16, up = lane & 8;
   float a = hi ? v[2] : v[0], b = hi ? 0.0f : v[1];
   a += __shfl_xor_sync(kAll, hi ? v[0] : v[2], 16);
@@ -307,13 +310,13 @@ __device__ __forceinline__ void block_sum(BlockSum<3>& s, uint32_t& buf, int thr
     __syncwarp();
     return;
   }
-  float(&q)[3][32] = s.part[buf & 1u];
+  float* q = s.part[buf & 1u];
   ++buf;
-  if ((lane & 7) == 0 && lane < 24) q[lane >> 3][threadIdx.x >> 5] = x;
+  if ((lane & 7) == 0 && lane < 24) q[2 * lane + (threadIdx.x >> 5)] = x;
   row_barrier(threads);
-  const int w = lane & 15;
-  a = w < warps ? q[lane >> 4][w] : 0.0f;
-  b = w < warps ? q[2][w] : 0.0f;
+  const bool has = (lane & 15) < warps;
+  a = has ? q[lane] : 0.0f;
+  b = has ? q[32 + (lane & 15)] : 0.0f;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) {
     a += __shfl_xor_sync(kAll, a, o);
