@@ -8,7 +8,8 @@ are CUDA tensors on the current device with unit column stride, a row stride
 that is a multiple of 8 elements and a 16-byte aligned base; widths are free
 (a result whose width is not a multiple of 8 is a view of a wider buffer).
 Calls go to the current stream, or to ``stream`` (a ``torch.cuda.Stream`` or a
-raw handle).
+raw handle), to which what they allocate then belongs; ordering it with the
+streams of the operands is the caller's, as for any torch call.
 """
 from __future__ import annotations
 
@@ -204,16 +205,19 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
-def _handle(stream, device, *made):
-    """The raw stream.  What was allocated here (on the current stream) and is
-    used on another one is recorded there, so that it is not reused early."""
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index)
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, device=device)
-    for t in made:
-        if t is not None:
-            t.record_stream(s)
-    return s.cuda_stream
+def _on(stream, call, *args, **kwargs):
+    """The call with `stream` as torch's current one, so that what it allocates
+    belongs to that stream (memory that was freed on another may still be in use
+    there)."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return call(*args, **kwargs)
+
+
+def _handle(device):
+    """The current stream's handle."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _stream_fmt(x, name):
@@ -252,6 +256,8 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     Returns {"r", "y", "rstd_pre", "rstd_post"}, None where not produced: r has
     x's dtype, y is bf16, the rstd [M] fp32 are what ``block_norm_bwd`` wants.
     """
+    if stream is not None:
+        return _on(stream, block_norm, x, branch, w_pre=w_pre, w_post=w_post, gate=gate, alpha=alpha, w_offset=w_offset, eps=eps, out=out)
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     device = _device(x, "x")
@@ -270,7 +276,7 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     rq = _result_packed(out, "rstd_post", (M,), _F32, device) if wq is not None else None
     a = NormFwdArgs(fmt, wf, alpha, w_offset, eps, 0, M, D, gates, ld_x, ld_b, ld_g, _ld(r), _ld(y), x.data_ptr(), _p(branch), _p(gate),
                     wp, wq, _p(r), _p(y), _p(rp), _p(rq))
-    _call("glu_block_norm_fwd", a, _handle(stream, device, r, y, rp, rq))
+    _call("glu_block_norm_fwd", a, _handle(device))
     return {"r": r, "y": y, "rstd_pre": rp, "rstd_post": rq}
 
 
@@ -282,6 +288,9 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     {"dx", "dw_pre", "dbranch", "dw_post", "dgate"}, None where not produced: dx
     has r's dtype, dbranch is bf16, the gradients of the vectors and of the gate
     ([G, D]) are fp32."""
+    if stream is not None:
+        return _on(stream, block_norm_bwd, r, dy, dr, rstd_pre=rstd_pre, w_pre=w_pre, branch=branch, rstd_post=rstd_post, w_post=w_post,
+                   gate=gate, alpha=alpha, w_offset=w_offset, out=out)
     if r.dim() != 2:
         raise ValueError("r must be a matrix")
     device = _device(r, "r")
@@ -307,7 +316,7 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     ws = _scratch(n)
     a = NormBwdArgs(fmt, wf, alpha, w_offset, M, D, gates, ld_r, ld_b, ld_g, ld_dy, ld_dr, _ld(dx), _ld(db), r.data_ptr(), _p(branch), _p(gate),
                     wp, wq, rp, rq, _p(dy), _p(dr), dx.data_ptr(), _p(db), _p(dwp), _p(dwq), _p(dg), ws.data_ptr(), n)
-    _call("glu_block_norm_bwd", a, _handle(stream, device, dx, db, dwp, dwq, dg, ws))
+    _call("glu_block_norm_bwd", a, _handle(device))
     return {"dx": dx, "dw_pre": dwp, "dbranch": db, "dw_post": dwq, "dgate": dg}
 
 
@@ -317,6 +326,8 @@ def route(ids, n_experts, *, out=None, stream=None) -> dict:
     "slot" [T, K] (the place of each assignment, -1 dropped), "src" [T * K] (the
     assignment t * K + k at each place, -1 past the last) and "offsets"
     [n_experts + 1]."""
+    if stream is not None:
+        return _on(stream, route, ids, n_experts, out=out)
     device = _device(ids, "ids")
     if ids.dim() != 2:
         raise ValueError("ids must be [tokens, choices]")
@@ -329,7 +340,7 @@ def route(ids, n_experts, *, out=None, stream=None) -> dict:
     n = _workspace("glu_block_route_workspace", T, K, n_experts)
     ws = _scratch(n)
     a = RouteArgs(8 if ids.dtype is torch.int64 else 4, n_experts, T, K, p, slot.data_ptr(), src.data_ptr(), offsets.data_ptr(), _p(ws), n)
-    _call("glu_block_route", a, _handle(stream, device, slot, src, offsets, ws))
+    _call("glu_block_route", a, _handle(device))
     return {"slot": slot, "src": src, "offsets": offsets}
 
 
@@ -344,19 +355,23 @@ def _slots(route, device):
 def dispatch(x, route, *, out=None, stream=None):
     """The rows of ``x`` [T, D] in the order of the route, [T * K, D]; rows past
     the last expert's are 0."""
+    if stream is not None:
+        return _on(stream, dispatch, x, route, out=out)
     device = _device(x, "x")
     T, K, slot, src = _slots(route, device)
     D = x.shape[-1]
     ld = _matrix(x, "x", (T, D), device)
     xs = _result(None if out is None else {"out": out}, "out", (T * K, D), _BF16, device)
     a = RowsArgs(T, K, D, ld, 0, _ld(xs), 0, slot, src, None, x.data_ptr(), None, None, None, xs.data_ptr(), None)
-    _call("glu_block_dispatch", a, _handle(stream, device, xs))
+    _call("glu_block_dispatch", a, _handle(device))
     return xs
 
 
 def combine(ys, route, weights=None, *, residual=None, out=None, stream=None):
     """``out[t] = residual[t] + sum_k weights[t, k] * ys[slot[t, k]]`` [T, D]
     (``weights`` fp32 [T, K], None: 1; dropped assignments add nothing)."""
+    if stream is not None:
+        return _on(stream, combine, ys, route, weights, residual=residual, out=out)
     device = _device(ys, "ys")
     T, K, slot, _ = _slots(route, device)
     D = ys.shape[-1]
@@ -365,7 +380,7 @@ def combine(ys, route, weights=None, *, residual=None, out=None, stream=None):
     w = _packed(weights, "weights", (T, K), device, (_F32,)) if weights is not None else None
     o = _result(None if out is None else {"out": out}, "out", (T, D), _BF16, device)
     a = RowsArgs(T, K, D, _ld(o), ld, 0, ld_res, slot, None, w, None, ys.data_ptr(), _p(residual), o.data_ptr(), None, None)
-    _call("glu_block_combine", a, _handle(stream, device, o))
+    _call("glu_block_combine", a, _handle(device))
     return o
 
 
@@ -378,6 +393,8 @@ def combine_bwd(dout, ys, route, weights, *, out=None, stream=None) -> dict:
     """Gradients of ``combine``: {"dys" [T * K, D] = the weighted rows of
     ``dout`` (0 past the last expert's), "dw" [T, K] fp32 = <ys[slot], dout>};
     the gradient of the residual is ``dout``."""
+    if stream is not None:
+        return _on(stream, combine_bwd, dout, ys, route, weights, out=out)
     device = _device(dout, "dout")
     T, K, slot, src = _slots(route, device)
     D = dout.shape[-1]
@@ -387,7 +404,7 @@ def combine_bwd(dout, ys, route, weights, *, out=None, stream=None) -> dict:
     dys = _result(out, "dys", (T * K, D), _BF16, device)
     dw = _result_packed(out, "dw", (T, K), _F32, device)
     a = RowsArgs(T, K, D, ld, ld_rows, _ld(dys), 0, slot, src, w, dout.data_ptr(), ys.data_ptr(), None, None, dys.data_ptr(), dw.data_ptr())
-    _call("glu_block_combine_bwd", a, _handle(stream, device, dys, dw))
+    _call("glu_block_combine_bwd", a, _handle(device))
     return {"dys": dys, "dw": dw}
 
 
@@ -409,6 +426,8 @@ def linear(x, w, *, bias=None, act=ACT_IDENTITY, residual=None, offsets=None, ke
     both bf16.  With ``w`` [E, N, K] and a route's ``offsets`` the rows of expert
     e take ``w[e]`` and ``bias[e]``; rows past the last expert's give 0.  ``bias``
     is bf16 or fp32.  Returns {"y", "z"} (z bf16, None unless ``keep_z``)."""
+    if stream is not None:
+        return _on(stream, linear, x, w, bias=bias, act=act, residual=residual, offsets=offsets, keep_z=keep_z, out=out)
     device = _device(x, "x")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
@@ -427,7 +446,7 @@ def linear(x, w, *, bias=None, act=ACT_IDENTITY, residual=None, offsets=None, ke
         if n:
             ws = _scratch(n)
             a.workspace, a.workspace_bytes = ws.data_ptr(), n
-    _call("glu_block_linear_fwd", a, _handle(stream, device, y, z, ws))
+    _call("glu_block_linear_fwd", a, _handle(device))
     return {"y": y, "z": z}
 
 
@@ -435,6 +454,9 @@ def linear_bwd(dy, x, w, *, z=None, act=ACT_IDENTITY, offsets=None, need_dx=True
     """Gradients of ``linear``: {"dx" bf16 [M, K], "dw" bf16 like ``w``, "db"
     fp32 [N] or [E, N]}, None where not asked for; the gradient of the residual
     is ``dy``.  ``z`` is the forward's where it had an activation."""
+    if stream is not None:
+        return _on(stream, linear_bwd, dy, x, w, z=z, act=act, offsets=offsets, need_dx=need_dx, need_dw=need_dw, need_db=need_db,
+                   out=out)
     device = _device(dy, "dy")
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
@@ -453,7 +475,7 @@ def linear_bwd(dy, x, w, *, z=None, act=ACT_IDENTITY, offsets=None, need_dx=True
     n = _workspace("glu_block_linear_bwd_workspace", a)
     ws = _scratch(n)
     a.workspace, a.workspace_bytes = _p(ws), n
-    _call("glu_block_linear_bwd", a, _handle(stream, device, dx, dw, db, ws))
+    _call("glu_block_linear_bwd", a, _handle(device))
     return {"dx": dx, "dw": dw, "db": db}
 
 

@@ -595,3 +595,21 @@ def test_linear_with_the_most_experts():
 def test_rows_of_many_choices():
     """More than eight choices per token, and more than one block of the sort."""
     test_rows_there_and_back(700, 11, 24, 0.1, 264)
+
+
+def test_results_belong_to_the_given_stream():
+    """Memory that a call allocates comes from the pool of the stream it runs
+    on: what the current stream still uses cannot be handed out to it."""
+    side = torch.cuda.Stream()
+    x = torch.ones(64, 512, dtype=BF, device=DEV)
+    w = torch.ones(512, dtype=BF, device=DEV)
+    torch.cuda.synchronize()
+    big = torch.empty(64, 512, dtype=BF, device=DEV)
+    at = big.data_ptr()
+    torch.cuda._sleep(2_000_000)  # the current stream is busy (about a millisecond) and then writes to big
+    big.fill_(-3.0)
+    del big  # free for the current stream's next allocation only
+    y = G.block_norm(x, w_pre=w, stream=side)["y"]
+    assert y.data_ptr() != at
+    torch.cuda.synchronize()
+    assert bool((y == 1).all())
