@@ -615,9 +615,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of(PROD == k
           const int32_t row = row0 + (lane & ~3), left = x.b_end - x.b0 - c - 8 * (lane & 3);
           uint16_t* out = p.out + x.e * p.stride_out + int64_t(row) * p.ld_out + x.b0 + c + 8 * (lane & 3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (row + j < p.width && left > 0)
-              put8(out + j * p.ld_out, left, make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]));
+          for (int j = 0; j < 4; ++j) {
+            if (row + j >= p.width || left <= 0) continue;
+            // stores that stay in L2 (streamed ones: 200 against 195 us for 64 uneven experts)
+            const uint4 v = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if (left >= 8) *reinterpret_cast<uint4*>(out + j * p.ld_out) = v;
+            else put8(out + j * p.ld_out, left, v);
+          }
         }
       }
       if (x.k0 < x.k_end) {
