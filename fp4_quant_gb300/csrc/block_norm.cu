@@ -56,23 +56,32 @@ struct RingWait {
   }
 };
 
-// A chunk of eight columns (from column c) of a staged row.  RAGGED: where the
-// width D ends inside it, its first ones from row m itself (the copies take
-// whole chunks), the rest 0.
-template <bool RAGGED>
-__device__ __forceinline__ F8 staged8(const uint8_t* stage, const uint16_t* base, int64_t m, int64_t ld, int c, int D) {
-  if (!RAGGED || c + 8 <= D) return pairs(*reinterpret_cast<const uint4*>(stage + 2 * c));
-  return pairs(raw8(base + m * ld + c, D - c));
+// The chunk in which a row's width ends (n of its columns are in it), into
+// shared memory with zeros behind the width; nothing behind it is read.  Bulk
+// copies take whole chunks, so this one comes apart, and every chunk is read
+// alike.  (A case of its own for it at each read, with the stores below by
+// single elements, took 440 us for 14566 x 4607 backward in bf16 and 208
+// forward; 4608 columns take 193 and 148.)
+template <typename T>
+__device__ __forceinline__ void load_tail(void* dst, const T* src, int n) {
+  const uint32_t d = smem_u32(dst), bytes = uint32_t(n * sizeof(T));
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes < 16 ? bytes : 16) : "memory");
+  if (sizeof(T) == 4)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(d + 16), "l"(bytes > 16 ? src + 4 : src),
+                 "r"(bytes > 16 ? bytes - 16 : 0)
+                 : "memory");
 }
-template <bool RAGGED>
-__device__ __forceinline__ F8 staged8(const uint8_t* stage, const float* base, int64_t m, int64_t ld, int c, int D) {
-  if (!RAGGED || c + 8 <= D) {
-    const float4 a = *reinterpret_cast<const float4*>(stage + 4 * c), b = *reinterpret_cast<const float4*>(stage + 4 * c + 16);
-    return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
-  }
-  float v[8];
-  load8(base + m * ld + c, D - c, v);
-  return pairs(v);
+// Counts one arrival when the copies of this thread so far have landed.
+__device__ __forceinline__ void tails_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// A chunk of eight columns (from column c) of a staged row.
+template <typename T>
+__device__ __forceinline__ F8 staged8(const uint8_t* stage, int c) {
+  if (sizeof(T) == 2) return pairs(*reinterpret_cast<const uint4*>(stage + 2 * c));
+  const float4 a = *reinterpret_cast<const float4*>(stage + 4 * c), b = *reinterpret_cast<const float4*>(stage + 4 * c + 16);
+  return {{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
 }
 template <typename T>
 __device__ __forceinline__ F8 direct8(const T* row, int c, int n) {
@@ -99,6 +108,14 @@ __device__ __forceinline__ F8 weight8(const void* w, bool f32, float o, float sc
     for (int i = 0; i < 8; ++i) v[i] *= g[i];
   }
   return pairs(v);
+}
+
+// Stores a thread's chunk k of V.  RAGGED: the width may end inside the last of
+// them (a row has more chunks than V - 1 per thread).
+template <bool RAGGED, int V, typename T>
+__device__ __forceinline__ void store_last(int k, T* p, int n, const F8& f) {
+  if (RAGGED && k == V - 1) store8<true>(p, n, f);
+  else store8<false>(p, n, f);
 }
 
 struct NormFwdP {
@@ -188,23 +205,40 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
   RingCtl<2>* ctl = reinterpret_cast<RingCtl<2>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
-  const uint32_t whole = uint32_t(D / 8) * 16, xb = whole / 2 * sizeof(XT), at_g = xb + (p.branch ? whole : 0u);
+  const uint32_t wide = uint32_t((D + 7) / 8) * 16, xb = wide / 2 * sizeof(XT), at_g = xb + (p.branch ? wide : 0u);  // a stage
+  const int c_tail = D / 8 * 8;  // RAGGED: where the last chunk begins
   const int64_t m0 = p.M * blockIdx.x / gridDim.x, m1 = p.M * (blockIdx.x + 1) / gridDim.x;
-  // loads row m into stage s (one thread)
+  // loads row m into stage s (thread 0; RAGGED: its tails by a thread of the
+  // next warp, 14566 x 4607 in fp32 184 -> 174 us)
+  const int tail_tid = threads > 32 ? 32 : 0;
   auto load = [&](int64_t m, int s) {
     uint8_t* st = stages + s * p.stage_bytes;
-    mbar_arrive_expect_tx(&ctl->full[s], uint32_t(p.stage_bytes));
-    if (whole == 0) return;
-    bulk_load(st, static_cast<const XT*>(p.x) + m * p.ld_x, xb, &ctl->full[s]);
-    if (p.branch) bulk_load(st + xb, p.branch + m * p.ld_branch, whole, &ctl->full[s]);
-    if (p.stream_gate) bulk_load(st + at_g, p.gate + m / p.rows_per_gate * p.ld_gate, whole, &ctl->full[s]);
+    uint64_t* bar = &ctl->full[s];
+    if (!RAGGED || tid == 0) {
+      const uint32_t bytes = RAGGED ? uint32_t(c_tail) * 2 : wide, x_bytes = bytes / 2 * sizeof(XT);
+      mbar_arrive_expect_tx(bar, RAGGED ? x_bytes + (p.branch ? bytes : 0u) + (p.stream_gate ? bytes : 0u) : uint32_t(p.stage_bytes));
+      if (!RAGGED || bytes) {
+        bulk_load(st, static_cast<const XT*>(p.x) + m * p.ld_x, x_bytes, bar);
+        if (p.branch) bulk_load(st + xb, p.branch + m * p.ld_branch, bytes, bar);
+        if (p.stream_gate) bulk_load(st + at_g, p.gate + m / p.rows_per_gate * p.ld_gate, bytes, bar);
+      }
+    }
+    if (RAGGED && tid == tail_tid) {
+      load_tail(st + c_tail * sizeof(XT), static_cast<const XT*>(p.x) + m * p.ld_x + c_tail, D - c_tail);
+      if (p.branch) load_tail(st + xb + 2 * c_tail, p.branch + m * p.ld_branch + c_tail, D - c_tail);
+      if (p.stream_gate) load_tail(st + at_g + 2 * c_tail, p.gate + m / p.rows_per_gate * p.ld_gate + c_tail, D - c_tail);
+      tails_arrive(bar);
+    }
   };
+  const bool loads = tid == 0 || (RAGGED && tid == tail_tid);
   if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], 1);
+    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], RAGGED ? 2 : 1);
     fence_barrier_init();
+  }
+  if (RAGGED) __syncthreads();
+  if (loads)
     for (int s = 0; s < p.stages; ++s)
       if (m0 + s < m1) load(m0 + s, s);
-  }
   __syncthreads();
   constexpr bool kHold = V <= 2;
   F8 w[kHold ? V : 1], f[kHold ? V : 1];
@@ -246,12 +280,12 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
     for (int k = 0; k < V; ++k) {
       const int c = 8 * (tid + k * threads);
       if (c >= D) continue;
-      x[k] = staged8<RAGGED>(st, static_cast<const XT*>(p.x), m, p.ld_x, c, D);
+      x[k] = staged8<XT>(st, c);
       if (!p.branch) continue;
-      b[k] = staged8<RAGGED>(st + xb, p.branch, m, p.ld_branch, c, D);
+      b[k] = staged8<uint16_t>(st + xb, c);
       const F8 fk = kHold ? f[kHold ? k : 0] : factors(c);
       F8 g = zeros();
-      if (p.stream_gate) g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+      if (p.stream_gate) g = staged8<uint16_t>(st + at_g, c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         sq = fma_2(b[k].v[i], b[k].v[i], sq);
@@ -263,7 +297,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
   };
   // every thread has read row m: its stage takes the row `stages` further on
   auto free_row = [&](int64_t m) {
-    if (tid == 0 && m + p.stages < m1) load(m + p.stages, s);
+    if (loads && m + p.stages < m1) load(m + p.stages, s);
     if (++s == p.stages) s = 0, parity ^= 1u;
   };
   XT* r_out = static_cast<XT*>(p.r) + m0 * p.ld_r;
@@ -284,7 +318,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
         if (p.branch) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) r[k].v[i] = fma_2(b[k].v[i], both(rq), r[k].v[i]);
-          store8<RAGGED>(r_out + c, D - c, r[k]);
+          store_last<RAGGED, V>(k, r_out + c, D - c, r[k]);
         }
         if (!p.w_pre) continue;
         const F8 wk = kHold ? w[kHold ? k : 0] : weight8(p.w_pre, p.w32, p.w_offset, 1.0f, nullptr, c, D - c);
@@ -309,7 +343,7 @@ __global__ void __launch_bounds__(512, 1) norm_fwd_kernel(const NormFwdP p) {
       if (c >= D) continue;
 #pragma unroll
       for (int i = 0; i < 4; ++i) r[k].v[i] = mul_2(r[k].v[i], both(rs));
-      store8<RAGGED>(y_out + c, D - c, r[k]);
+      store_last<RAGGED, V>(k, y_out + c, D - c, r[k]);
     }
     y_out += p.ld_y;
   }
@@ -332,8 +366,9 @@ cudaError_t launch_fwd_rows(NormFwdP p, cudaStream_t s, const DevInfo& d) {
   const int threads = row_threads((p.D + 7) / 8, V), blocks = ring_blocks(threads);
   // a gate row shared by few rows comes with each (where one stage has room
   // for it), else its factors are fetched when it changes
-  p.stream_gate = p.gate != nullptr && p.rows_per_gate < 16 && p.D * int64_t(sizeof(XT) + 4) + kCtlBytes <= kSmemMost;
-  p.stage_bytes = int(p.D / 8 * 8 * (sizeof(XT) + (p.branch ? 2 : 0) + (p.stream_gate ? 2 : 0)));
+  const int64_t wide = (p.D + 7) / 8 * 8;
+  p.stream_gate = p.gate != nullptr && p.rows_per_gate < 16 && wide * int64_t(sizeof(XT) + 4) + kCtlBytes <= kSmemMost;
+  p.stage_bytes = int(wide * (sizeof(XT) + (p.branch ? 2 : 0) + (p.stream_gate ? 2 : 0)));
   p.stages = ring_stages(p.stage_bytes, blocks);
   const int smem = kCtlBytes + p.stages * p.stage_bytes;
   if (smem > kSmemMost) return cudaErrorInvalidValue;
@@ -412,11 +447,13 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
   RingCtl<3>* ctl = reinterpret_cast<RingCtl<3>*>(smem);
   uint8_t* stages = smem + kCtlBytes;
   const int threads = blockDim.x, D = int(p.D), tid = threadIdx.x;
-  const uint32_t whole = uint32_t(D / 8) * 16, xb = whole / 2 * sizeof(XT);
+  const uint32_t wide = uint32_t((D + 7) / 8) * 16, xb = wide / 2 * sizeof(XT);
+  const int c_tail = D / 8 * 8;  // RAGGED: where the last chunk begins
   const bool pre = p.w_pre != nullptr, post = p.w_post != nullptr, br = p.branch != nullptr, has_dr = p.dr != nullptr;
   // a stage: r, dy (pre), dr (given), branch (given), gate (MANY)
-  const uint32_t at_dy = pre ? xb : 0u, at_dr = at_dy + (pre ? whole : 0u), at_b = at_dr + (has_dr ? xb : 0u), at_g = at_b + whole;
-  // loads the next row of this block's items into stage s, if there is one (one thread)
+  const uint32_t at_dy = pre ? xb : 0u, at_dr = at_dy + (pre ? wide : 0u), at_b = at_dr + (has_dr ? xb : 0u), at_g = at_b + wide;
+  // loads the next row of this block's items into stage s, if there is one (one
+  // thread, the tails too: a second one for those changed the times by -3 to 3 %)
   auto load_next = [&](int s) {
     while (ctl->row >= ctl->end) {
       if (ctl->item >= p.items) return;
@@ -428,18 +465,27 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
     const int64_t m = ctl->row++;
     uint8_t* st = stages + s * p.stage_bytes;
     uint64_t* bar = &ctl->full[s];
-    mbar_arrive_expect_tx(bar, uint32_t(p.stage_bytes));
-    if (whole == 0) return;
-    if (pre) {
-      bulk_load(st, static_cast<const XT*>(p.r) + m * p.ld_r, xb, bar);
-      bulk_load(st + at_dy, p.dy + m * p.ld_dy, whole, bar);
+    const XT *r = static_cast<const XT*>(p.r) + m * p.ld_r, *dr = static_cast<const XT*>(p.dr) + m * p.ld_dr;
+    const uint16_t *dy = p.dy + m * p.ld_dy, *b = p.branch + m * p.ld_branch, *g = MANY ? p.gate + m / p.rows_per_gate * p.ld_gate : nullptr;
+    const uint32_t bytes = RAGGED ? uint32_t(c_tail) * 2 : wide, x_bytes = bytes / 2 * sizeof(XT);
+    mbar_arrive_expect_tx(bar, (pre ? x_bytes + bytes : 0u) + (has_dr ? x_bytes : 0u) + (br ? bytes : 0u) + (MANY ? bytes : 0u));
+    if (!RAGGED || bytes) {
+      if (pre) bulk_load(st, r, x_bytes, bar), bulk_load(st + at_dy, dy, bytes, bar);
+      if (has_dr) bulk_load(st + at_dr, dr, x_bytes, bar);
+      if (br) bulk_load(st + at_b, b, bytes, bar);
+      if (MANY) bulk_load(st + at_g, g, bytes, bar);
     }
-    if (has_dr) bulk_load(st + at_dr, static_cast<const XT*>(p.dr) + m * p.ld_dr, xb, bar);
-    if (br) bulk_load(st + at_b, p.branch + m * p.ld_branch, whole, bar);
-    if (MANY) bulk_load(st + at_g, p.gate + m / p.rows_per_gate * p.ld_gate, whole, bar);
+    if (RAGGED) {
+      const int n = D - c_tail;
+      if (pre) load_tail(st + x_bytes, r + c_tail, n), load_tail(st + at_dy + bytes, dy + c_tail, n);
+      if (has_dr) load_tail(st + at_dr + x_bytes, dr + c_tail, n);
+      if (br) load_tail(st + at_b + bytes, b + c_tail, n);
+      if (MANY) load_tail(st + at_g + bytes, g + c_tail, n);
+      tails_arrive(bar);
+    }
   };
   if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], 1);
+    for (int s = 0; s < p.stages; ++s) mbar_init(&ctl->full[s], RAGGED ? 2 : 1);
     fence_barrier_init();
     ctl->item = blockIdx.x;
     ctl->row = ctl->end = 0;
@@ -495,7 +541,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
       auto h_of = [&](int k, int c) {
         F8 f = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
         if (MANY) {
-          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+          const F8 g = staged8<uint16_t>(st + at_g, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) f.v[i] = mul_2(f.v[i], g.v[i]);
         }
@@ -508,11 +554,11 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
       for (int k = 0; k < V; ++k) {
         const int c = 8 * (tid + k * threads);
         if (c >= D) continue;
-        t[k] = has_dr ? staged8<RAGGED>(st + at_dr, static_cast<const XT*>(p.dr), m, p.ld_dr, c, D) : zeros();
+        t[k] = has_dr ? staged8<XT>(st + at_dr, c) : zeros();
         F8 r = zeros();
         if (pre) {
-          r = staged8<RAGGED>(st, static_cast<const XT*>(p.r), m, p.ld_r, c, D);
-          F8 v = staged8<RAGGED>(st + at_dy, p.dy, m, p.ld_dy, c, D);
+          r = staged8<XT>(st, c);
+          F8 v = staged8<uint16_t>(st + at_dy, c);
           const F8 wk = kHold ? w[kHold ? k : 0] : fetch_w(c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -524,7 +570,7 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
           }
         }
         if (post) {
-          const F8 b = staged8<RAGGED>(st + at_b, p.branch, m, p.ld_branch, c, D), hk = h_of(k, c);
+          const F8 b = staged8<uint16_t>(st + at_b, c), hk = h_of(k, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float2 q = mul_2(b.v[i], hk.v[i]);
@@ -545,13 +591,13 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
         const int c = 8 * (tid + k * threads);
         if (c >= D) continue;
         if (pre) {
-          const F8 r = staged8<RAGGED>(st, static_cast<const XT*>(p.r), m, p.ld_r, c, D);
+          const F8 r = staged8<XT>(st, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) t[k].v[i] = fma_2(r.v[i], both(k1), t[k].v[i]);
         }
-        store8<RAGGED>(dx + c, D - c, t[k]);
+        store_last<RAGGED, V>(k, dx + c, D - c, t[k]);
         if (!br) continue;
-        F8 b = staged8<RAGGED>(st + at_b, p.branch, m, p.ld_branch, c, D);
+        F8 b = staged8<uint16_t>(st + at_b, c);
         const F8 hk = h_of(k, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -559,14 +605,14 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
           a_x[k].v[i] = fma_2(e, b.v[i], a_x[k].v[i]);
           b.v[i] = post ? fma_2(b.v[i], both(k2), mul_2(e, hk.v[i])) : mul_2(e, hk.v[i]);
         }
-        store8<RAGGED>(db + c, D - c, b);
+        store_last<RAGGED, V>(k, db + c, D - c, b);
       }
       if (MANY && m + 1 == m1) {
 #pragma unroll
         for (int k = 0; k < V; ++k) {
           const int c = 8 * (tid + k * threads);
           if (c >= D) continue;
-          const F8 g = staged8<RAGGED>(st + at_g, p.gate, grp, p.ld_gate, c, D);
+          const F8 g = staged8<uint16_t>(st + at_g, c);
           F8 out = kHold ? h[kHold ? k : 0] : fetch_h(grp, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -604,7 +650,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
 }
 
 // The sums over blocks and items, in a fixed order: 32 columns per block, 32
-// threads per column, eight loads of each in flight.  blockIdx.y: dw_pre, dw_post, then the gate rows.
+// threads per column, eight loads of each in flight.  (part_x has few items,
+// at most four per block: divided in 64 bits their numbers took 11 us of 2000 x
+// 1024's 33.)  blockIdx.y: dw_pre, dw_post, then the gate rows.
 struct JoinP {
   const float *part_pre, *part_post, *part_x;
   const uint16_t* gate;
@@ -630,9 +678,9 @@ __global__ void __launch_bounds__(1024) join_kernel(const JoinP p) {
       for (int64_t i = threadIdx.y; i < p.pieces; i += 32) v += p.part_x[(y * p.pieces + i) * p.D + c];
     } else if (what == 1 && p.part_x) {
 #pragma unroll 8
-      for (int64_t i = threadIdx.y; i < p.items; i += 32) {
+      for (uint32_t i = threadIdx.y; i < uint32_t(p.items); i += 32) {
         const float x = p.part_x[i * p.D + c];
-        v = p.gate ? fmaf(bf16_of_bits(p.gate[i / p.pieces * p.ld_gate + c]), x, v) : v + x;
+        v = p.gate ? fmaf(bf16_of_bits(p.gate[i / uint32_t(p.pieces) * p.ld_gate + c]), x, v) : v + x;
       }
     } else {
       const float* q = what == 0 ? p.part_pre : p.part_post;
@@ -691,7 +739,7 @@ NormBwdPlan norm_bwd_plan(int64_t M, int64_t D, int64_t gates) {
 template <typename XT, int V, bool MANY>
 cudaError_t launch_bwd_v(NormBwdP p, const NormBwdPlan& q, cudaStream_t s) {
   p.stage_bytes =
-      int(p.D / 8 * 8 * ((p.w_pre ? sizeof(XT) + 2 : 0) + (p.dr ? sizeof(XT) : 0) + (p.branch ? 2 : 0) + (MANY ? 2 : 0)));
+      int((p.D + 7) / 8 * 8 * ((p.w_pre ? sizeof(XT) + 2 : 0) + (p.dr ? sizeof(XT) : 0) + (p.branch ? 2 : 0) + (MANY ? 2 : 0)));
   p.stages = ring_stages(p.stage_bytes, q.per_sm);
   const int smem = kCtlBytes + p.stages * p.stage_bytes;
   if (smem > kSmemMost) return cudaErrorInvalidValue;

@@ -90,23 +90,24 @@ __device__ __forceinline__ void stg_once(void* p, const uint4& v) {
                : "memory");
 }
 
+// A chunk's first n < 8 elements are moved as up to four, two and one (chunks
+// start on 16 bytes).
+//
 // The first n (1..8) bf16 of a chunk as they are; the rest is 0.
 __device__ __forceinline__ uint4 raw8(const uint16_t* p, int n) {
   if (n >= 8) return ldg_once(p);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (2 * i < n ? uint32_t(p[2 * i]) : 0u) | (2 * i + 1 < n ? uint32_t(p[2 * i + 1]) << 16 : 0u);
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  uint2 four = make_uint2(0u, 0u);
+  uint32_t two = 0u, one = 0u;
+  if (n & 4) four = *reinterpret_cast<const uint2*>(p);
+  if (n & 2) two = *reinterpret_cast<const uint32_t*>(p + (n & 4));
+  if (n & 1) one = p[n & 6];
+  const uint32_t lo = (n & 2) ? two : one, hi = (n & 2) ? one : 0u;
+  return (n & 4) ? make_uint4(four.x, four.y, lo, hi) : make_uint4(lo, hi, 0u, 0u);
 }
 
 // The first n (1..8) elements of a chunk; the rest of v is 0.
 __device__ __forceinline__ void load8(const uint16_t* p, int n, float (&v)[8]) {
-  if (n >= 8) {
-    unpack8(ldg_once(p), v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? bf16_of_bits(p[i]) : 0.0f;
-  }
+  unpack8(raw8(p, n), v);
 }
 __device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
   if (n >= 8) {
@@ -114,39 +115,38 @@ __device__ __forceinline__ void load8(const float* p, int n, float (&v)[8]) {
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
     v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
   } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : 0.0f;
+    float4 four = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float2 two = make_float2(0.0f, 0.0f);
+    float one = 0.0f;
+    if (n & 4) four = *reinterpret_cast<const float4*>(p);
+    if (n & 2) two = *reinterpret_cast<const float2*>(p + (n & 4));
+    if (n & 1) one = p[n & 6];
+    const float x = (n & 2) ? two.x : one, y = two.y, z = (n & 2) ? one : 0.0f;
+    v[0] = (n & 4) ? four.x : x, v[1] = (n & 4) ? four.y : y, v[2] = (n & 4) ? four.z : z, v[3] = four.w;
+    v[4] = (n & 4) ? x : 0.0f, v[5] = (n & 4) ? y : 0.0f, v[6] = (n & 4) ? z : 0.0f, v[7] = 0.0f;
   }
 }
-__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) {
+// The first n (up to 8) of eight bf16 as they are.
+__device__ __forceinline__ void put8(uint16_t* p, int n, const uint4& v) {
   if (n >= 8) {
-    stg_once(p, pack8(v));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = bits_of_bf16(v[i]);
+    stg_once(p, v);
+  } else if (n > 0) {
+    if (n & 4) *reinterpret_cast<uint2*>(p) = make_uint2(v.x, v.y);
+    const uint32_t lo = (n & 4) ? v.z : v.x, hi = (n & 4) ? v.w : v.y;
+    if (n & 2) *reinterpret_cast<uint32_t*>(p + (n & 4)) = lo;
+    if (n & 1) p[n & 6] = uint16_t((n & 2) ? hi : lo);
   }
 }
+__device__ __forceinline__ void store8(uint16_t* p, int n, const float (&v)[8]) { put8(p, n, pack8(v)); }
 __device__ __forceinline__ void store8(float* p, int n, const float (&v)[8]) {
   if (n >= 8) {
     stg_once(p, make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])));
     stg_once(p + 4, make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = v[i];
-  }
-}
-
-// The first n (up to 8) of eight bf16 as they are.
-__device__ __forceinline__ void put8(uint16_t* o, int n, const uint4& v) {
-  if (n >= 8) {
-    stg_once(o, v);
-  } else {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < n) o[i] = uint16_t(w[i >> 1] >> (16 * (i & 1)));
+  } else if (n > 0) {
+    if (n & 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    const float x = (n & 4) ? v[4] : v[0], y = (n & 4) ? v[5] : v[1], z = (n & 4) ? v[6] : v[2];
+    if (n & 2) *reinterpret_cast<float2*>(p + (n & 4)) = make_float2(x, y);
+    if (n & 1) p[n & 6] = (n & 2) ? z : x;
   }
 }
 
