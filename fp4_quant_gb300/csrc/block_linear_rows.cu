@@ -1,5 +1,7 @@
 // What stands around the products of the linear layers (glu_block.h): y of few
 // tokens, the join of split sums, and dz with its sums over rows.
+#include <type_traits>
+
 #include "block_act.cuh"
 #include "block_linear.cuh"
 #include "block_util.cuh"
@@ -230,15 +232,17 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
   if (part < 0 || m0 >= m1) return;
   const int32_t c = blockIdx.y * kDzCols + 8 * threadIdx.x, left = p.N - c;
   F8 sum = zeros();
-  if (left > 0) {
+  // Whole chunks and the one in which the width ends apart: a choice at each
+  // load would hold back the ones after it.
+  auto walk = [&](auto whole) {
     for (int32_t m = m0 + threadIdx.y; m < m1; m += 8 * kDzDeep) {
       uint4 a[kDzDeep], z[kDzDeep];
 #pragma unroll
       for (int i = 0; i < kDzDeep; ++i) {
         const int64_t row = m + 8 * i;
         if (row >= m1) continue;
-        a[i] = raw8(p.dy + row * p.ld_dy + c, left);
-        if (ACT != GLU_ACT_IDENTITY) z[i] = raw8(p.z + row * p.ld_z + c, left);
+        a[i] = raw8(p.dy + row * p.ld_dy + c, decltype(whole)::value ? 8 : left);
+        if (ACT != GLU_ACT_IDENTITY) z[i] = raw8(p.z + row * p.ld_z + c, decltype(whole)::value ? 8 : left);
       }
 #pragma unroll
       for (int i = 0; i < kDzDeep; ++i) {
@@ -256,7 +260,9 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
         for (int q = 0; q < 4; ++q) sum.v[q] = add_2(sum.v[q], d.v[q]);
       }
     }
-  }
+  };
+  if (left >= 8) walk(std::true_type());
+  else if (left > 0) walk(std::false_type());
   if (!p.part) return;
 #pragma unroll
   for (int q = 0; q < 4; ++q) *reinterpret_cast<float2*>(&sh[threadIdx.y][8 * threadIdx.x + 2 * q]) = sum.v[q];
