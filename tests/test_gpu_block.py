@@ -613,3 +613,49 @@ def test_results_belong_to_the_given_stream():
     assert y.data_ptr() != at
     torch.cuda.synchronize()
     assert bool((y == 1).all())
+
+
+@pytest.mark.parametrize("D", [5, 517, 1031, 4606])
+@pytest.mark.parametrize("stream", [BF, F32])
+def test_what_stands_behind_a_row_does_not_count(D, stream):
+    """The same bits whatever stands between a row's end and the next row, and
+    nothing is written there."""
+    T, K, E = 700, 3, 5
+    ld = -(-D // 8) * 8
+
+    def run(behind):
+        g = _gen(7)
+
+        def rows(M, dtype=BF):
+            buf = torch.full((M, ld), behind, dtype=dtype, device=DEV)
+            buf[:, :D] = torch.randn(M, D, generator=g, device=DEV).to(dtype)
+            return buf[:, :D]
+
+        x, b, dy, dr = rows(T, stream), rows(T), rows(T), rows(T, stream)
+        w = torch.randn(D, generator=g, device=DEV)
+        got = []
+        for gates in (1, 28, T):
+            gate = rows(gates)
+            r = torch.full((T, ld), 7.0, dtype=stream, device=DEV)
+            f = G.block_norm(x, b, w_pre=w, w_post=w, gate=gate, out={"r": r[:, :D]})
+            assert bool((r[:, D:] == 7).all())
+            r[:, D:] = behind
+            back = G.block_norm_bwd(f["r"], dy, dr, rstd_pre=f["rstd_pre"], w_pre=w, branch=b, rstd_post=f["rstd_post"], w_post=w, gate=gate)
+            got += [f["r"].clone(), f["y"], *(back[k] for k in ("dx", "dbranch", "dw_pre", "dw_post", "dgate"))]
+        tok, ys, wt = rows(T), rows(T * K), torch.rand(T, K, generator=g, device=DEV)
+        ids = torch.randint(-1, E, (T, K), generator=g, device=DEV, dtype=torch.int32)
+        ids[0] = torch.tensor([E - 1] * K)
+        at = G.route(ids, E)
+        out = torch.full((T, ld), 7.0, dtype=BF, device=DEV)
+        got.append(G.combine(ys, at, wt, residual=tok, out=out[:, :D]).clone())
+        assert bool((out[:, D:] == 7).all())
+        back = G.combine_bwd(tok, ys, at, wt)
+        got += [G.dispatch(tok, at), back["dys"], back["dw"]]
+        lin = G.linear_bwd(tok, rows(T), rows(D), z=rows(T), act=G.ACT_SILU, need_db=True)
+        return got + [lin[k] for k in ("dx", "dw", "db")]
+
+    want = run(0.0)
+    assert all(bool(torch.isfinite(t).all()) for t in want)
+    for behind in (float("nan"), float("inf")):
+        for i, (a, t) in enumerate(zip(want, run(behind))):
+            assert torch.equal(a, t), (behind, i)
