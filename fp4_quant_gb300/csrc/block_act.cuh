@@ -34,9 +34,9 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
-// act'(z): an exponential and a quotient each (the SM's special functions are
-// what this kernel would wait for); 1 - s has an absolute error of 2^-24, which
-// is what act' is good to.
+// act'(z), |z| up to 128 or NaN: an exponential and a quotient each (the SM's
+// special functions are what this kernel would wait for); 1 - s has an absolute
+// error of 2^-24, which is what act' is good to.
 template <int ACT>
 __device__ __forceinline__ float act_grad(float z) {
   if (ACT == GLU_ACT_SILU) {
@@ -56,6 +56,19 @@ __device__ __forceinline__ float act_grad(float z) {
     return fmaf(z * 0.3989422804014327f, e, normal_cdf(z, e));
   }
   return 1.0f;
+}
+
+// act' of two bf16.  From |z| = 128 on act' of the smooth ones is 0 or 1 in fp32,
+// and z is taken as that (NaN kept): z^2 and z^3 of larger ones pass fp32's
+// range, and 0 times infinity would be NaN where act' is 0 or 1 (as it is at
+// infinities, the limits).  Both at once, in bf16, which holds 128: 4096 x 1462
+// with SiLU takes 16.8 us, limited one by one in fp32 18.8; 16384 x 8192 99 us,
+// and 91 without limits.
+template <int ACT>
+__device__ __forceinline__ float2 act_grad_of(uint32_t z) {
+  if (ACT == GLU_ACT_SILU || ACT == GLU_ACT_GELU_TANH || ACT == GLU_ACT_GELU_ERF)
+    asm("max.NaN.bf16x2 %0, %0, %1;\n\tmin.NaN.bf16x2 %0, %0, %2;" : "+r"(z) : "r"(0xC300C300u), "r"(0x43004300u));
+  return make_float2(act_grad<ACT>(__uint_as_float(z << 16)), act_grad<ACT>(__uint_as_float(z & 0xFFFF0000u)));
 }
 
 }  // namespace gq

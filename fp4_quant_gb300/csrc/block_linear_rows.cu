@@ -250,9 +250,9 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzP p) {
         if (row >= m1) continue;
         F8 d = pairs(a[i]);
         if (ACT != GLU_ACT_IDENTITY) {
-          const F8 v = pairs(z[i]);
+          const uint32_t v[4] = {z[i].x, z[i].y, z[i].z, z[i].w};
 #pragma unroll
-          for (int q = 0; q < 4; ++q) d.v[q] = mul_2(d.v[q], make_float2(act_grad<ACT>(v.v[q].x), act_grad<ACT>(v.v[q].y)));
+          for (int q = 0; q < 4; ++q) d.v[q] = mul_2(d.v[q], act_grad_of<ACT>(v[q]));
           // kept in L2: the products read it next
           if (p.dz) *reinterpret_cast<uint4*>(p.dz + row * p.ld_dz + c) = packed(d);
         }

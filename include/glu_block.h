@@ -197,7 +197,8 @@ typedef struct glu_block_linear_fwd_args {
   size_t workspace_bytes;
 } glu_block_linear_fwd_args;
 
-/* Backward: dz = dy .* act'(z) (act = GLU_ACT_IDENTITY: dz = dy, z NULL),
+/* Backward: dz = dy .* act'(z) (act = GLU_ACT_IDENTITY: dz = dy, z NULL;
+ * act' of SiLU and the GELUs is 0 and 1 at -inf and +inf, their limits),
  *   dx = dz W (bf16 [M, K]), dw = dz^T x (bf16, W's shape), db = sum over the
  *   rows of dz (fp32 [N], by expert [E, N]); each is skipped where its
  *   pointer is NULL.  dz is rounded to bf16 for the products (the tensor
