@@ -50,7 +50,7 @@ __device__ __forceinline__ float act_grad(float z) {
     const float s = __fdividef(1.0f, 1.0f + __expf(-u));
     return s * fmaf(z * (1.0f - s), du, 1.0f);
   }
-  if (ACT == GLU_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+  if (ACT == GLU_ACT_RELU) return z <= 0.0f ? 0.0f : 1.0f;  // 1 at NaN too, as glu_act says
   if (ACT == GLU_ACT_GELU_ERF) {
     const float e = __expf(-0.5f * z * z);
     return fmaf(z * 0.3989422804014327f, e, normal_cdf(z, e));

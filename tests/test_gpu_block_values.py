@@ -77,7 +77,7 @@ def _grad(name, z):
     z = z.double()
     c = 2.0 * math.sqrt(2.0 / math.pi)
     if name == "relu":
-        return torch.where(torch.isnan(z), z, (z > 0).double())
+        return torch.where(z <= 0, 0.0, 1.0).double()  # 1 at NaN too, as the gated activation's
     if name == "none":
         return torch.ones_like(z)
     if name == "gelu_erf":
