@@ -584,8 +584,10 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_kernel(const NormBwdP p) {
       else row_barrier(threads);
       // every thread is done with the row before this one
       if (tid == 0 && last >= 0) load_next(last);
-      const float k1 = -rs * rs * per_d * sum[0];
-      const float k2 = -rp * rp * rp * per_d * fmaf(k1, sum[2], sum[1]);
+      // The sums come first: with rows of 1e14 or 1e-14 the powers of an rstd
+      // alone are outside fp32's range, their products with the sums are not.
+      const float k1 = -(sum[0] * per_d * rs) * rs;
+      const float k2 = -(fmaf(k1, sum[2], sum[1]) * rp * per_d * rp) * rp;
 #pragma unroll
       for (int k = 0; k < V; ++k) {
         const int c = 8 * (tid + k * threads);

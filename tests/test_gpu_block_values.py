@@ -1,5 +1,5 @@
 """The block operators on values far from one: the activations and their
-derivatives over every bf16 value.
+derivatives over every bf16 value, and rows of very large and small numbers.
 
 Tolerances are worst-case bounds, as in test_gpu_block.py.
 """
@@ -129,3 +129,20 @@ def test_one_large_z_leaves_the_others_alone():
     T._close(got["db"], dz.sum(0), own.sum(0) + (M + 8) * T.U * dz.abs().sum(0), "db")
     T._close(got["dx"], dz @ w.double(), ((N + 8) * T.U * dz.abs() + err) @ w.double().abs(), "dx")
     T._close(got["dw"], dz.t() @ x.double(), ((M + 8) * T.U * dz.abs() + err).t() @ x.double().abs(), "dw")
+
+
+@pytest.mark.parametrize("D", [264, 8192])
+@pytest.mark.parametrize("scale", [1e14, 1e-14])
+@pytest.mark.parametrize("gates", [1, 160])
+def test_norm_backward_of_branches_far_from_one(D, scale, gates):
+    """rstd_post^3 is outside fp32's range, the gradients are not."""
+    M = 160
+    g, r, b, gate, w1, w2 = T._norm_inputs(M, D, BF, F32, True, True, gates, 0.0, D)
+    b = (b.double() * scale).to(BF)
+    dy, dr = T._rows(g, M, D), T._rows(g, M, D)
+    rs = torch.rsqrt(r.float().square().mean(1) + 1e-6)
+    rp = torch.rsqrt(b.double().square().mean(1)).float()
+    got = G.block_norm_bwd(r, dy, dr, rstd_pre=rs, w_pre=w1, branch=b, rstd_post=rp, w_post=w2, gate=gate)
+    want, size = T._norm_bwd_ref(r, dy, dr, rs, w1, b, rp, w2, gate, 1.0, 0.0)
+    for k, v in got.items():
+        T._close(v, want[k], (2 * D + M + 64) * T.U * size[k], k)
