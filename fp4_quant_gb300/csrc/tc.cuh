@@ -158,11 +158,6 @@ __device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same where no memory of this thread's is handed over (a release would
-// first wait for its stores to arrive).
-__device__ __forceinline__ void peer_arrive_relaxed(uint32_t bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
 // Bounded wait that also orders what the other CTA did before it arrived.
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < kWaitBudget; ++i) {
