@@ -6,7 +6,9 @@ call returns (unless ``out`` holds it) and its workspace, and raise
 ``GluQuantError`` on a status other than 0, with nothing launched.  Matrices
 are CUDA tensors on the current device with unit column stride, a row stride
 that is a multiple of 8 elements and a 16-byte aligned base; widths are free
-(a result whose width is not a multiple of 8 is a view of a wider buffer).
+(a result whose width is not a multiple of 8 is a view of a wider buffer).  A
+matrix of rows (not a weight, a gate or an ``out``) with another row stride,
+such as the contiguous one of odd width that ``fwd`` returns, is copied first.
 Calls go to the current stream, or to ``stream`` (a ``torch.cuda.Stream`` or a
 raw handle), to which what they allocate then belongs; ordering it with the
 streams of the operands is the caller's, as for any torch call.
@@ -154,6 +156,16 @@ def _matrix(t, name, shape, device, dtype=_BF16):
     return st[-2] if shape[-2] > 1 else -(-shape[-1] // 8) * 8
 
 
+def _rows(t, name, shape, device, dtype=_BF16):
+    """A matrix of rows that a call reads, checked, and its row stride: itself, or
+    a copy whose rows start on 16 bytes."""
+    ld = _matrix(t, name, shape, device, dtype)
+    if ld % 8 == 0:
+        return t, ld
+    t = _new(shape, dtype).copy_(t.detach())
+    return t, t.stride(0)
+
+
 def _packed(t, name, shape, device, dtypes):
     """Checks a contiguous operand."""
     if t.dtype not in dtypes:
@@ -265,8 +277,8 @@ def block_norm(x, branch=None, *, w_pre=None, w_post=None, gate=None, alpha=1.0,
     shape = (M, D)
     fmt = _stream_fmt(x, "x")
     wf = _weight_fmt(w_pre, w_post)
-    ld_x = _matrix(x, "x", shape, device, x.dtype)
-    ld_b = _matrix(branch, "branch", shape, device) if branch is not None else 0
+    x, ld_x = _rows(x, "x", shape, device, x.dtype)
+    branch, ld_b = _rows(branch, "branch", shape, device) if branch is not None else (None, 0)
     gates, ld_g = _gate(gate, D, device)
     wp = _packed(w_pre, "w_pre", (D,), device, (_BF16, _F32)) if w_pre is not None else None
     wq = _packed(w_post, "w_post", (D,), device, (_BF16, _F32)) if w_post is not None else None
@@ -298,10 +310,10 @@ def block_norm_bwd(r, dy=None, dr=None, *, rstd_pre=None, w_pre=None, branch=Non
     shape = (M, D)
     fmt = _stream_fmt(r, "r")
     wf = _weight_fmt(w_pre, w_post)
-    ld_r = _matrix(r, "r", shape, device, r.dtype)
-    ld_b = _matrix(branch, "branch", shape, device) if branch is not None else 0
-    ld_dy = _matrix(dy, "dy", shape, device) if dy is not None else 0
-    ld_dr = _matrix(dr, "dr", shape, device, r.dtype) if dr is not None else 0
+    r, ld_r = _rows(r, "r", shape, device, r.dtype)
+    branch, ld_b = _rows(branch, "branch", shape, device) if branch is not None else (None, 0)
+    dy, ld_dy = _rows(dy, "dy", shape, device) if dy is not None else (None, 0)
+    dr, ld_dr = _rows(dr, "dr", shape, device, r.dtype) if dr is not None else (None, 0)
     gates, ld_g = _gate(gate, D, device)
     wp = _packed(w_pre, "w_pre", (D,), device, (_BF16, _F32)) if w_pre is not None else None
     wq = _packed(w_post, "w_post", (D,), device, (_BF16, _F32)) if w_post is not None else None
@@ -360,7 +372,7 @@ def dispatch(x, route, *, out=None, stream=None):
     device = _device(x, "x")
     T, K, slot, src = _slots(route, device)
     D = x.shape[-1]
-    ld = _matrix(x, "x", (T, D), device)
+    x, ld = _rows(x, "x", (T, D), device)
     xs = _result(None if out is None else {"out": out}, "out", (T * K, D), _BF16, device)
     a = RowsArgs(T, K, D, ld, 0, _ld(xs), 0, slot, src, None, x.data_ptr(), None, None, None, xs.data_ptr(), None)
     _call("glu_block_dispatch", a, _handle(device))
@@ -375,8 +387,8 @@ def combine(ys, route, weights=None, *, residual=None, out=None, stream=None):
     device = _device(ys, "ys")
     T, K, slot, _ = _slots(route, device)
     D = ys.shape[-1]
-    ld = _matrix(ys, "ys", (T * K, D), device)
-    ld_res = _matrix(residual, "residual", (T, D), device) if residual is not None else 0
+    ys, ld = _rows(ys, "ys", (T * K, D), device)
+    residual, ld_res = _rows(residual, "residual", (T, D), device) if residual is not None else (None, 0)
     w = _packed(weights, "weights", (T, K), device, (_F32,)) if weights is not None else None
     o = _result(None if out is None else {"out": out}, "out", (T, D), _BF16, device)
     a = RowsArgs(T, K, D, _ld(o), ld, 0, ld_res, slot, None, w, None, ys.data_ptr(), _p(residual), o.data_ptr(), None, None)
@@ -398,8 +410,8 @@ def combine_bwd(dout, ys, route, weights, *, out=None, stream=None) -> dict:
     device = _device(dout, "dout")
     T, K, slot, src = _slots(route, device)
     D = dout.shape[-1]
-    ld = _matrix(dout, "dout", (T, D), device)
-    ld_rows = _matrix(ys, "ys", (T * K, D), device)
+    dout, ld = _rows(dout, "dout", (T, D), device)
+    ys, ld_rows = _rows(ys, "ys", (T * K, D), device)
     w = _packed(weights, "weights", (T, K), device, (_F32,))
     dys = _result(out, "dys", (T * K, D), _BF16, device)
     dw = _result_packed(out, "dw", (T, K), _F32, device)
@@ -432,10 +444,10 @@ def linear(x, w, *, bias=None, act=ACT_IDENTITY, residual=None, offsets=None, ke
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     M, K = x.shape
-    ld_x = _matrix(x, "x", (M, K), device)
+    x, ld_x = _rows(x, "x", (M, K), device)
     E, N, ld_w, stride_w, off = _weight(w, offsets, K, device)
     b = _packed(bias, "bias", (E, N) if E else (N,), device, (_BF16, _F32)) if bias is not None else None
-    ld_res = _matrix(residual, "residual", (M, N), device) if residual is not None else 0
+    residual, ld_res = _rows(residual, "residual", (M, N), device) if residual is not None else (None, 0)
     y = _result(out, "y", (M, N), _BF16, device)
     z = _result(out, "z", (M, N), _BF16, device) if keep_z else None
     a = LinearFwdArgs(act, FMT_FP32 if bias is not None and bias.dtype is _F32 else FMT_BF16, E, 0, M, N, K, ld_x, ld_w, stride_w, ld_res,
@@ -461,10 +473,10 @@ def linear_bwd(dy, x, w, *, z=None, act=ACT_IDENTITY, offsets=None, need_dx=True
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     M, K = x.shape
-    ld_x = _matrix(x, "x", (M, K), device)
+    x, ld_x = _rows(x, "x", (M, K), device)
     E, N, ld_w, stride_w, off = _weight(w, offsets, K, device)
-    ld_dy = _matrix(dy, "dy", (M, N), device)
-    ld_z = _matrix(z, "z", (M, N), device) if z is not None else 0
+    dy, ld_dy = _rows(dy, "dy", (M, N), device)
+    z, ld_z = _rows(z, "z", (M, N), device) if z is not None else (None, 0)
     dx = _result(out, "dx", (M, K), _BF16, device) if need_dx else None
     dw = _result(out, "dw", tuple(w.shape), _BF16, device) if need_dw else None
     db = _result_packed(out, "db", (E, N) if E else (N,), _F32, device) if need_db else None
