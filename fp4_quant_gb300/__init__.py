@@ -14,6 +14,7 @@ raises ImportError (importing the package alone does not, so that
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 __all__ = [
@@ -24,13 +25,15 @@ __all__ = [
     "GluQuantError", "fwd", "bwd", "library_path",
     "ACT_SILU", "ACT_GELU_TANH", "ACT_RELU", "ACT_IDENTITY", "ACT_GELU_ERF", "ACT_BF16_STEPS", "FMT_MXFP8", "FMT_NVFP4", "FMT_BF16", "FMT_FP32", "FMT_MXFP8_128X4",
     "MODE_ROW", "MODE_COL", "MODE_BOTH", "LAYOUT_SPLIT", "LAYOUT_INTERLEAVED",
-    "block_norm", "block_norm_bwd", "route", "dispatch", "dispatch_bwd", "combine", "combine_bwd", "linear", "linear_bwd",
-    "block_device_errors", "block_abi_version",
 ]
 
 #: The operators around the gated activation live in ``block``, which needs
-#: torch; they are looked up there on first use.
-_BLOCK = frozenset(__all__[__all__.index("block_norm"):])
+#: torch; they are looked up there on first use, and ``import *`` takes them
+#: where torch is installed.
+_BLOCK = ("block_norm", "block_norm_bwd", "route", "dispatch", "dispatch_bwd", "combine", "combine_bwd", "linear", "linear_bwd",
+          "block_device_errors", "block_abi_version")
+if importlib.util.find_spec("torch") is not None:
+    __all__ += _BLOCK
 
 
 def __getattr__(name):

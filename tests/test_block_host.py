@@ -4,6 +4,7 @@ import os
 import re
 import shutil
 import subprocess
+import sys
 
 import pytest
 
@@ -156,3 +157,17 @@ def test_tensors_on_the_host_are_refused():
     for call in (lambda: G.block_norm(x, w_pre=x[0]), lambda: G.route(torch.zeros(2, 2, dtype=torch.int64), 4), lambda: G.linear(x, x)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def _python(code):
+    return subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+
+
+def test_the_package_is_imported_whole_without_torch():
+    """As before there were block operators; they come with torch."""
+    r = _python("import sys; sys.modules['torch'] = None\nfrom fp4_quant_gb300 import *\nassert glu_quant_fwd and 'linear' not in dir()")
+    assert r.returncode == 0, r.stderr
+    r = _python("import sys; sys.modules['torch'] = None\nimport fp4_quant_gb300 as G\nG.linear")
+    assert r.returncode != 0 and "torch" in r.stderr
+    r = _python("from fp4_quant_gb300 import *\nimport fp4_quant_gb300 as G\nassert linear is G.linear and all(hasattr(G, n) for n in G.__all__)")
+    assert r.returncode == 0, r.stderr
