@@ -19,6 +19,21 @@ def has_gpu():
     return torch.cuda.is_available()
 
 
+@pytest.fixture(scope="module", autouse=True)
+def no_wait_gave_up(request):
+    """After the last test of each GPU file: no kernel's bounded wait gave up."""
+    yield
+    if not request.module.__name__.startswith("test_gpu_"):
+        return
+    import torch
+    if not torch.cuda.is_available():
+        return
+    import fp4_quant_gb300 as G
+    from waits import assert_none_gave_up
+    torch.cuda.synchronize()
+    assert_none_gave_up(G, request.module.__name__)
+
+
 def pytest_terminal_summary(terminalreporter):
     """Report the parity counts of the run: codes and scales compared with the
     oracle and the codes that differ by one step inside the 2-ulp window
