@@ -31,7 +31,7 @@
 // where the rows of the next expert are zeroed (so that what they hold, NaN
 // included, does not count) while the sum over the whole sixteens goes on.
 // (Zeroed in the ring's stages they held the products up: 242 us against 197
-// for 64 uneven experts of 32768 x 2048 x 2048.)
+// for 64 uneven experts of 32768 x 2048 x 2048, then; 204 to 207 now.)
 //
 // Ten warps per CTA (dw: eleven, one for those last rows): one issues the loads,
 // one (of CTA 0) the products into one of two accumulators in tensor memory,
@@ -39,7 +39,9 @@
 // against 273 us at 4096 x 8192 x 7168, the issuing warps wait longer for their
 // turn).  The two issuing warps run uniformly and elect a lane, so that operands
 // and addresses stay in uniform registers: 274 to 253 us there (1900 TFLOP/s, as
-// cuBLAS).  Every wait is bounded.
+// cuBLAS).  Where there are few tiles it is behind that: 7168 x 8192 takes 26 us
+// for 32 tokens and 72 for 1024 (cuBLAS 21 and 61), the dw of 1024 x 1024 and 4096
+// tokens, 16 tiles for 76 pairs, 22 us (8.5).  Every wait is bounded.
 #include <atomic>
 #include <cstring>
 
@@ -177,9 +179,13 @@ __device__ __forceinline__ Tile tile_at(const LinearP& p, const Ctl* ctl, int32_
 }
 
 // The experts' row ranges, their order and tile counts, by the whole block.
-// The tiles go round the pairs by falling size (largest expert first), so that
-// the pairs' sums differ by no more than one tile; beyond 256 experts, where
-// ranking them would take longer than that is worth, in their own order.
+// The tiles go round the pairs, those of the largest expert first.  A dw's tiles
+// are as large as their expert's rows, so they fall and the pairs' sums differ by
+// no more than one tile.  For y and dx an expert's last token tile is smaller than
+// its others, and some pairs may get more of the one kind (152 experts of 257 rows
+// with two row tiles each: 1280 tokens for half of the 76 pairs, 1024 for the
+// others).  Beyond 256 experts, where ranking them would take longer than it is
+// worth, they go in their own order.
 template <int PROD>
 __device__ __forceinline__ void plan_tiles(const LinearP& p, Ctl* ctl, int warp, int lane) {
   const int32_t col_tiles = (p.cols + kTile - 1) / kTile;

@@ -12,7 +12,11 @@
 // across the block.  A stage is refilled after a barrier that those sums need
 // anyway: by then every thread is done with the row it held.  16384 x 7168 with
 // an fp32 stream and a gate takes 221 us forward (6.4 TB/s), 8191 x 8192 in
-// bf16 135 us backward (5.9 TB/s).
+// bf16 135 us backward (5.9 TB/s).  Rows wider than 8192 hold more chunks per
+// thread than registers (spilled: forward 90 to 120 bytes up to 16384 and 480 to
+// 530 above, backward 260 to 310, 530 to 570 with a gate row per few rows) and
+// fetch the weights for every row: 5461 x 12288 in bf16 259 us forward (2.1 TB/s)
+// and 364 backward (2.2), 2048 x 32768 forward 260 (2.1).
 #include "block.h"
 #include "block_util.cuh"
 #include "tma.cuh"

@@ -22,8 +22,12 @@
  * the stream; workspaces may be reused by the next call on that stream.
  * Indices that a call reads from device memory (offsets, slot, src) are
  * bounded in the kernels: one out of range counts as dropped.  Sums (norm
- * statistics, products, gradients of shared operands) are fp32, taken in an order that depends on the shapes only, so that a call gives
- * the same bits every time.
+ * statistics, products, gradients of shared operands) are fp32, taken in an
+ * order that depends on the shapes only, so that a call gives the same bits
+ * every time.  What stands between the end of a row and the next row (ld above
+ * the width) is never written and never counts; glu_block_combine and
+ * glu_block_combine_bwd read up to seven elements of it behind rows_in's rows,
+ * so nothing else may write there while they run.
  */
 #ifndef GLU_BLOCK_H
 #define GLU_BLOCK_H
