@@ -27,13 +27,14 @@ __all__ = [
     "MODE_ROW", "MODE_COL", "MODE_BOTH", "LAYOUT_SPLIT", "LAYOUT_INTERLEAVED",
 ]
 
-#: The operators around the gated activation live in ``block``, which needs
-#: torch; they are looked up there on first use, and ``import *`` takes them
-#: where torch is installed.
+#: The operators around the gated activation live in ``block`` and ``block8``,
+#: which need torch; they are looked up there on first use, and ``import *`` takes
+#: them where torch is installed.
 _BLOCK = ("block_norm", "block_norm_bwd", "route", "dispatch", "dispatch_bwd", "combine", "combine_bwd", "linear", "linear_bwd",
           "block_device_errors", "block_abi_version")
+_BLOCK8 = ("quant8", "quant8_weight", "linear8", "linear8_dx", "linear8_dw", "glu8", "glu8_bwd", "block8_abi_version")
 if importlib.util.find_spec("torch") is not None:
-    __all__ += _BLOCK
+    __all__ += _BLOCK + _BLOCK8
 
 
 def __getattr__(name):
@@ -41,6 +42,11 @@ def __getattr__(name):
         from . import block
         for n in _BLOCK:
             globals()[n] = getattr(block, n)
+        return globals()[name]
+    if name in _BLOCK8:
+        from . import block8
+        for n in _BLOCK8:
+            globals()[n] = getattr(block8, n)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 

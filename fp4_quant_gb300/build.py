@@ -27,7 +27,8 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden"]
 UNITS = ["api.cu", "tmap.cu", "fwd_mx.cu", "fwd_mx_b16.cu", "fwd_mx_x.cu", "fwd_mx_erf.cu", "bwd_mx.cu", "bwd_both.cu", "gemm_glu.cu", "plain.cu",
-         "block_api.cu", "block_norm.cu", "block_route.cu", "block_linear.cu", "block_linear_rows.cu", "block_tmap.cu"]
+         "block_api.cu", "block_norm.cu", "block_route.cu", "block_linear.cu", "block_linear_rows.cu", "block_tmap.cu",
+         "block8_api.cu", "block8_quant.cu", "block8_glu.cu", "block8_linear.cu"]
 
 
 def _nvcc() -> str:
@@ -71,8 +72,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(tmp, tables)
     # 2. translation units
     nvcc = _nvcc()
-    headers = [os.path.join(CSRC, h) for h in ("glu_common.cuh", "kernels.h", "tma.cuh", "mx_block.cuh", "nv_block.cuh", "ring.cuh", "bwd_common.cuh", "fwd_mx.cuh", "tc.cuh", "block.h", "block_util.cuh", "block_act.cuh", "block_linear.cuh")]
-    headers += [tables, os.path.join(INCLUDE, "glu_quant.h"), os.path.join(INCLUDE, "glu_block.h")]
+    headers = [os.path.join(CSRC, h) for h in ("glu_common.cuh", "kernels.h", "tma.cuh", "mx_block.cuh", "nv_block.cuh", "ring.cuh", "bwd_common.cuh", "fwd_mx.cuh", "tc.cuh", "block.h", "block_util.cuh", "block_act.cuh", "block_linear.cuh", "block_tiles.cuh", "block8.h", "block8_util.cuh", "block8_act.cuh")]
+    headers += [tables, os.path.join(INCLUDE, "glu_quant.h"), os.path.join(INCLUDE, "glu_block.h"), os.path.join(INCLUDE, "glu_block8.h")]
     objs, jobs = [], []
     for u in UNITS:
         src = os.path.join(CSRC, u)

@@ -1,0 +1,500 @@
+// Products of 8-bit operands with a scale per block of 128 (glu_block8.h), on the
+// tcgen05 tensor cores:
+//
+//   y  = x W^T    summed over K, blocks of 128 columns of x
+//   dx = dy W     summed over N
+//   dw = dy^T x   summed over the tokens, blocks of 128 rows
+//
+//   D[i, j] = sum over blocks b of sa(i, b) sb(j, b) sum over k in b of A[i, k] B[j, k]
+//
+// Tiles and walk are those of the bf16 layers (block_tiles.cuh): 256 rows of D by
+// up to 256 columns for a pair of CTAs, the tokens as the columns of y and dx.
+// One block of the sum is one slice of the ring (128 codes are the 128 bytes of
+// the swizzle) and one accumulator in tensor memory: while the tensor cores sum
+// the next block into the other one, eight warps read this one, scale it and add
+// it to what they hold in registers, 128 fp32 per thread.  Their share of the
+// register file is raised for that (setmaxnreg), the other four warps' lowered.
+// Two warps fetch the scales, block by block ahead, into a ring of their own; a
+// weight's scale is one number for the 128 rows of a CTA and goes into the
+// columns' scales there, so that a value costs half a two-wide multiply-add (dw:
+// a multiplication by its row's scale as well).
+#include <cstring>
+
+#include "block8.h"
+#include "block_tiles.cuh"
+#include "tc.cuh"
+#include "tma.cuh"
+
+namespace gq {
+namespace {
+
+constexpr int kBK8 = 128, kStages8 = 6;
+constexpr int kOperand8 = kHalf * kBK8;  // 16 KB
+constexpr int kStageBytes8 = 2 * kOperand8;
+constexpr int kScaleSlots = 4;
+constexpr int kLoadWarps = 4, kEpiWarps8 = 8;  // loads, products, two of scales; epilogue
+constexpr int kThreads8 = (kLoadWarps + kEpiWarps8) * 32;
+// 168 registers per thread at launch: 128 x 72 + 256 x 216 = 384 x 168
+constexpr int kFewRegs = 72, kManyRegs = 216;
+constexpr uint32_t kTmemCols8 = 2 * kTile;
+constexpr uint32_t kIdesc8 = tc::idesc_e4m3_f32(kTile, 0);  // the columns are added per tile
+
+struct Scales {
+  float col[kTile];
+  float row[kHalf];
+};
+struct Ctl8 {
+  uint64_t full[kStages8];   // CTA 0's: its arrival and the bytes of both CTAs
+  uint64_t empty[kStages8];  // each CTA's own: the products on its stage are done
+  uint64_t tfull[2];         // each CTA's own: a block's sum is complete
+  uint64_t tempty[2];        // CTA 0's: the warps of both have read it
+  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // each CTA's own scales
+  uint64_t done;             // each CTA's own: all products are done
+  uint32_t tmem;
+  alignas(16) Scales scales[kScaleSlots];
+  TilePlan plan;
+};
+constexpr int kSmem8 = 1024 + kStages8 * kStageBytes8 + int(sizeof(Ctl8));
+static_assert(kSmem8 <= 232448, "shared memory per CTA exceeds 227 KB");
+
+__device__ uint32_t g_err_linear8;
+
+struct Linear8P {
+  CUtensorMap ta, tb[3];   // tb[i]: boxes of 128 >> i rows, for tiles with fewer columns; dw: tb[0]
+  const int32_t* offsets;  // NULL: dense
+  int32_t E;               // experts (dense: 1)
+  int32_t rows;            // of x (dw: rows that the offsets may reach, dense: of the column forms)
+  int32_t width;           // rows of D: N, K (dx) or N
+  int32_t cols;            // columns of D of a dw (K)
+  int32_t depth;           // summed over (y: K, dx: N)
+  int32_t n_at;            // tiles of 256 rows of D
+  int32_t most;            // most tokens of a tile (a multiple of 32, up to 256)
+  int32_t splits;          // parts of the sum
+  // scales: of A's block b and rows of a CTA (y and dx: sa[e sa_e + row / 128 sa_row + b sa_b]; dw: sa[b width + row]),
+  // of B's (sb[b ld_sb + column])
+  const float *sa, *sb;
+  int64_t sa_e, sa_row, sa_b, ld_sb;
+  int64_t ld_out, stride_out;
+  void* out;
+  int32_t f32;             // dw in fp32
+};
+
+// Tile t; a dw sums over its expert's blocks of the column forms.
+template <int PROD>
+__device__ __forceinline__ Tile tile8_at(const Linear8P& p, const TilePlan& plan, int32_t t) {
+  Tile x = tile_at<PROD, kBK8>(p, plan, t);
+  if (PROD == kGradW && p.offsets) {
+    const int32_t rows = x.k_end - x.k0;
+    x.k0 = (x.k0 / kBK8 + x.e) * kBK8;
+    x.k_end = x.k0 + (rows + kBK8 - 1) / kBK8 * kBK8;
+  }
+  return x;
+}
+
+template <int REGS>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <int PROD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear8_kernel(const __grid_constant__ Linear8P p) {
+  constexpr bool kAmn = PROD != kForward, kBmn = PROD == kGradW;
+  constexpr uint32_t kIdesc = kIdesc8 | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  Ctl8* ctl = reinterpret_cast<Ctl8*>(stages + kStages8 * kStageBytes8);
+  const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  after_previous();
+  if (threadIdx.x == 32) {
+    prefetch_tensormap(&p.ta);
+    for (int s = 0; s < kStages8; ++s) {
+      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&ctl->tfull[b], 1);
+      mbar_init(&ctl->tempty[b], 2 * kEpiWarps8);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) {
+      mbar_init(&ctl->sfull[s], 1);
+      mbar_init(&ctl->sempty[s], kEpiWarps8);
+    }
+    mbar_init(&ctl->done, 1);
+    fence_barrier_init();
+  }
+  plan_tiles<PROD>(p, ctl->plan, warp, lane);
+  if (warp == 1) {
+    __syncwarp();
+    tc::pair_alloc(&ctl->tmem, kTmemCols8);
+    tc::pair_relinquish();
+  }
+  tc::fence_before();
+  cluster_sync();
+  tc::fence_after();
+  const uint32_t tmem = ctl->tmem;
+  const int32_t tiles = ctl->plan.first[p.offsets ? p.E : 1];
+
+  if (warp < kLoadWarps) {
+    fewer_regs<kFewRegs>();
+    if (warp == 0) {
+      // -------------------------------------------------------- producer --
+      int s = 0, held = 0;  // held: stages ever filled, up to all
+      uint32_t parity = 0;
+      const uint32_t full0 = peer_addr(&ctl->full[0], 0);
+      bool ok = true;
+      for (int32_t t = pair; t < tiles && ok; t += pairs) {
+        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
+        // the smallest box with the half's columns (more than it needs are not
+        // multiplied)
+        const int box = half > 64 ? 0 : half > 32 ? 1 : 2;
+        const uint32_t bytes = uint32_t(kOperand8 + (kHalf >> box) * kBK8);
+        const CUtensorMap* tb = &p.tb[PROD == kGradW ? 0 : box];
+        for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
+            break;
+          }
+          if (tc::elect_one()) {
+            uint8_t* a = stages + s * kStageBytes8;
+            uint8_t* b = a + kOperand8;
+            const uint32_t bar = full0 + 8u * uint32_t(s);
+            if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
+            if (PROD == kForward) pair_load_3d(a, &p.ta, k, a0, x.e, bar);
+            else if (PROD == kGradX) pair_load_3d(a, &p.ta, a0, k, x.e, bar);
+            else pair_load_2d(a, &p.ta, a0, k, bar);
+            if (PROD == kGradW) pair_load_2d(b, tb, b0, k, bar);
+            else pair_load_2d(b, tb, k, b0, bar);
+          }
+          held = max(held, s + 1);
+          if (++s == kStages8) s = 0, parity ^= 1u;
+        }
+      }
+      // never leave with loads in flight: the products on each stage's last slice
+      // (which waited for its loads) are done
+      if (s == held) s = 0, parity ^= 1u;
+      for (int j = 0; j < held; ++j) {
+        if (!__all_sync(0xFFFFFFFFu, mbar_wait(&ctl->empty[s], parity ^ 1u)) && lane == 0) atomicOr(&g_err_linear8, kErrDrain);
+        if (++s == held) s = 0, parity ^= 1u;
+      }
+    } else if (warp == 1) {
+      // ------------------------------------------------------------- MMA --
+      int s = 0;
+      uint32_t parity = 0, i = 0;  // i: blocks summed
+      const uint32_t a_addr = smem_u32(stages);
+      const uint64_t ad0 = kAmn ? tc::sw128_mnmajor_desc(a_addr, kOperand8) : tc::sw128_kmajor_desc(a_addr);
+      const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand8, kOperand8) : tc::sw128_kmajor_desc(a_addr + kOperand8);
+      bool ok = true;
+      for (int32_t t = pair; t < tiles && ok && rank == 0; t += pairs) {
+        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
+        for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
+          const uint32_t b = i & 1u;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
+            break;
+          }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
+            break;
+          }
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t ad = ad0 + uint32_t(s * (kStageBytes8 >> 4)), bd = bd0 + uint32_t(s * (kStageBytes8 >> 4));
+#pragma unroll
+            for (int j = 0; j < kBK8 / 32; ++j)
+              tc::pair_mma_e4m3(tmem + b * kTile, ad + j * (kAmn ? 256 : 2), bd + j * (kBmn ? 256 : 2), idesc, uint32_t(j));
+            tc::pair_commit(&ctl->empty[s]);
+            tc::pair_commit(&ctl->tfull[b]);
+          }
+          __syncwarp();
+          ++i;
+          if (++s == kStages8) s = 0, parity ^= 1u;
+        }
+      }
+      __syncwarp();
+      if (tc::elect_one()) {  // the lane that issued the products
+        if (rank == 0) tc::pair_commit(&ctl->done);
+        if (!mbar_wait(&ctl->done, 0)) atomicOr(&g_err_linear8, kErrDrain);
+      }
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------- scales --
+      // warp 2 has the even blocks, warp 3 the odd ones; the next one's loads are
+      // in flight while one is stored
+      uint32_t i = 0;
+      bool ok = true;
+      for (int32_t t = pair; t < tiles && ok; t += pairs) {
+        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const int32_t b0 = x.k0 / kBK8, b1 = (x.k_end + kBK8 - 1) / kBK8;
+        const int32_t row0 = x.a0 + int32_t(rank) * kHalf;
+        const float* sa = p.sa + (PROD == kGradW ? int64_t(row0) : x.e * p.sa_e + row0 / kBlock8 * p.sa_row);
+        const float* sb = p.sb + x.b0;
+        float col[8], row[4], next_col[8], next_row[4];
+        auto load = [&](int32_t b, float (&c)[8], float (&r)[4]) {
+          if (PROD == kGradW) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = row0 + 32 * j + lane < p.width ? __ldg(sa + int64_t(b) * p.width + 32 * j + lane) : 0.0f;
+          } else {
+            r[0] = row0 < p.width ? __ldg(sa + b * p.sa_b) : 0.0f;
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) c[j] = x.b0 + 32 * j + lane < x.b_end ? __ldg(sb + int64_t(b) * p.ld_sb + 32 * j + lane) : 0.0f;
+        };
+        int32_t b = b0 + int32_t((uint32_t(warp - 2) ^ i) & 1u);
+        if (b < b1) load(b, col, row);
+        for (; b < b1; b += 2) {
+          const uint32_t at = i + uint32_t(b - b0);
+          const int slot = int(at % kScaleSlots);
+          if (b + 2 < b1) load(b + 2, next_col, next_row);
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->sempty[slot], ((at / kScaleSlots) & 1u) ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
+            break;
+          }
+          Scales& o = ctl->scales[slot];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o.col[32 * j + lane] = PROD == kGradW ? col[j] : col[j] * row[0];
+          if (PROD == kGradW) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o.row[32 * j + lane] = row[j];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->sfull[slot]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) col[j] = next_col[j];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) row[j] = next_row[j];
+        }
+        i += uint32_t(b1 - b0);
+      }
+    }
+  } else {
+    // ---------------------------------------------------------- epilogue --
+    more_regs<kManyRegs>();
+    const int quarter = warp & 3, group = (warp - kLoadWarps) >> 2;
+    const uint32_t tempty0 = peer_addr(&ctl->tempty[0], 0);
+    const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
+    uint32_t i = 0;
+    bool ok = true;
+    for (int32_t t = pair; t < tiles && ok; t += pairs) {
+      const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+      float2 acc[4][16];  // columns 32 (2 q + group) .. + 31
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) acc[q][j] = make_float2(0.0f, 0.0f);
+      const int chunks = (x.n / 32 - group + 1) / 2;  // this group's
+      for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
+        const uint32_t b = i & 1u;
+        const int slot = int(i % kScaleSlots);
+        ok = mbar_wait(&ctl->sfull[slot], (i / kScaleSlots) & 1u) && mbar_wait(&ctl->tfull[b], (i >> 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
+          break;
+        }
+        tc::fence_after();
+        const Scales& sc = ctl->scales[slot];
+        const float2 row = PROD == kGradW ? both(sc.row[quarter * 32 + lane]) : make_float2(1.0f, 1.0f);
+        const uint32_t base = lanes + b * kTile + uint32_t(group * 32);
+        uint32_t r[2][32];
+        if (chunks > 0) tc::ld32(base, r[0]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (q < chunks) {
+            tc::wait_ld();
+            if (q + 1 < chunks) {
+              tc::ld32(base + uint32_t(64 * (q + 1)), r[(q + 1) & 1]);
+            }
+            const float4* s4 = reinterpret_cast<const float4*>(sc.col + 64 * q + 32 * group);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 s = s4[j];
+              float2 lo = make_float2(__uint_as_float(r[q & 1][4 * j]), __uint_as_float(r[q & 1][4 * j + 1]));
+              float2 hi = make_float2(__uint_as_float(r[q & 1][4 * j + 2]), __uint_as_float(r[q & 1][4 * j + 3]));
+              if (PROD == kGradW) lo = mul_2(lo, row), hi = mul_2(hi, row);
+              acc[q][2 * j] = fma_2(lo, make_float2(s.x, s.y), acc[q][2 * j]);
+              acc[q][2 * j + 1] = fma_2(hi, make_float2(s.z, s.w), acc[q][2 * j + 1]);
+            }
+          }
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          peer_arrive(tempty0 + 8u * b);
+          mbar_arrive(&ctl->sempty[slot]);
+        }
+        ++i;
+      }
+      if (!ok) break;
+      const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c = 64 * q + 32 * group;
+        if (c >= x.n) break;
+        if (PROD != kGradW) {
+          const int32_t token = x.b0 + c + (lane & 3), col = row0 + (lane & ~3);
+          const TokenView view = {p.width - col, x.b_end - token};
+          uint32_t w[8][2];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            w[j][0] = bf16x2_of(acc[q][2 * j].x, acc[q][2 * j].y);
+            w[j][1] = bf16x2_of(acc[q][2 * j + 1].x, acc[q][2 * j + 1].y);
+          }
+          store_quads(static_cast<uint16_t*>(p.out) + int64_t(token) * p.ld_out + col, p.ld_out, view, w, lane);
+        } else if (p.f32) {
+          // 16 columns at a time: pieces of four
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[2 * j] = __float_as_uint(acc[q][8 * h + j].x), w[2 * j + 1] = __float_as_uint(acc[q][8 * h + j].y);
+            piece_transpose(w, lane);
+            const int32_t row = row0 + (lane & ~3), at = x.b0 + c + 16 * h + 4 * (lane & 3), left = x.b_end - at;
+            float* out = static_cast<float*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              if (row + j >= p.width) continue;
+              if (left >= 4) {
+                *reinterpret_cast<uint4*>(out + j * p.ld_out) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              } else {
+#pragma unroll
+                for (int y = 0; y < 3; ++y)
+                  if (y < left) out[j * p.ld_out + y] = __uint_as_float(w[4 * j + y]);
+              }
+            }
+          }
+        } else {
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = bf16x2_of(acc[q][j].x, acc[q][j].y);
+          piece_transpose(w, lane);
+          const int32_t row = row0 + (lane & ~3), left = x.b_end - x.b0 - c - 8 * (lane & 3);
+          uint16_t* out = static_cast<uint16_t*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + x.b0 + c + 8 * (lane & 3);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (row + j >= p.width || left <= 0) continue;
+            const uint4 v = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if (left >= 8) *reinterpret_cast<uint4*>(out + j * p.ld_out) = v;
+            else put8(out + j * p.ld_out, left, v);
+          }
+        }
+      }
+    }
+    // rows that no expert has
+    if (PROD != kGradW && p.offsets) {
+      const float zero[8] = {};
+      const int64_t chunks = (p.width + 7) / 8, first = ctl->plan.cut[p.E];
+      for (int64_t q = int64_t(blockIdx.x) * kEpiWarps8 * 32 + threadIdx.x - kLoadWarps * 32; q < (p.rows - first) * chunks;
+           q += int64_t(gridDim.x) * kEpiWarps8 * 32) {
+        const int64_t m = first + q / chunks;
+        const int32_t c = int32_t(q % chunks) * 8;
+        store8(static_cast<uint16_t*>(p.out) + m * p.ld_out + c, p.width - c, zero);
+      }
+    }
+  }
+  __syncwarp();
+  tc::fence_before();
+  cluster_sync();
+  if (warp == 1) {
+    tc::fence_after();
+    tc::pair_dealloc(tmem, kTmemCols8);
+  }
+}
+
+std::atomic<int> known8[64];  // pairs at once, alike for every product
+
+template <int PROD>
+cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
+  auto kern = linear8_kernel<PROD>;
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), kSmem8);
+  if (e != cudaSuccess) return e;
+  p.n_at = (p.width + kTile - 1) / kTile;
+  // by expert the device counts the tiles: no more than one token tile per
+  // expert above the dense count
+  const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
+                                      : p.n_at * ((int64_t(p.rows) + p.most - 1) / p.most + (p.offsets ? p.E : 0)) * p.splits;
+  int pairs = 0;
+  e = pairs_at_once(known8, reinterpret_cast<const void*>(kern), kThreads8, kSmem8, d, &pairs);
+  if (e != cudaSuccess) return e;
+  if (most < pairs) pairs = int(most);
+  return launch_kernel(kern, 2 * pairs, kThreads8, kSmem8, s, p, true);
+}
+
+}  // namespace
+
+size_t linear8_workspace(const glu_block8_linear_args&) { return 0; }
+
+cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, const DevInfo& d) {
+  Linear8P p;
+  memset(&p, 0, sizeof p);
+  const bool grad = a.grad != 0;
+  const int64_t E = a.E > 0 ? a.E : 1, depth = grad ? a.N : a.K;
+  cudaError_t e = make_byte_stack_map(&p.ta, a.wq, a.K, a.N, a.ld_w, E, a.E > 0 ? a.stride_w : a.N * a.ld_w, kHalf);
+  for (int i = 0; i < 3 && e == cudaSuccess; ++i) e = make_tile_map(&p.tb[i], a.xq, 1, depth, a.M, a.ld_x, kBK8, kHalf >> i, 128);
+  if (e != cudaSuccess) return e;
+  p.offsets = a.E > 0 ? a.offsets : nullptr;
+  p.E = int32_t(E);
+  p.rows = int32_t(a.M);
+  p.width = int32_t(grad ? a.K : a.N);
+  p.depth = int32_t(depth);
+  p.most = kTile;
+  p.splits = 1;
+  p.sa = a.ws;
+  p.sa_e = blocks8(a.N) * blocks8(a.K);
+  p.sa_row = grad ? 1 : blocks8(a.K);
+  p.sa_b = grad ? blocks8(a.K) : 1;
+  p.sb = a.xs;
+  p.ld_sb = a.M;
+  p.out = a.y;
+  p.ld_out = a.ld_y;
+  return grad ? launch8<kGradX>(p, s, d) : launch8<kForward>(p, s, d);
+}
+
+cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s, const DevInfo& d) {
+  Linear8P p;
+  memset(&p, 0, sizeof p);
+  const int64_t rows = a.C * kBlock8;
+  cudaError_t e = make_tile_map(&p.ta, a.dyq, 1, a.N, rows, a.ld_dy, 128, kBK8, 128);
+  if (e == cudaSuccess) e = make_tile_map(&p.tb[0], a.xq, 1, a.K, rows, a.ld_x, 128, kBK8, 128);
+  if (e != cudaSuccess) return e;
+  p.offsets = a.E > 0 ? a.offsets : nullptr;
+  p.E = int32_t(a.E > 0 ? a.E : 1);
+  // M / 128 + E blocks: the last row of M at most, so that no expert's blocks pass C
+  p.rows = int32_t(a.E > 0 ? (a.C - a.E) * kBlock8 + kBlock8 - 1 : rows);
+  p.width = int32_t(a.N);
+  p.cols = int32_t(a.K);
+  p.most = kTile;
+  p.splits = 1;
+  p.sa = a.dys;
+  p.sb = a.xs;
+  p.ld_sb = a.K;
+  p.out = a.dw;
+  p.ld_out = a.ld_dw;
+  p.stride_out = a.stride_dw;
+  p.f32 = a.dw_fmt == GLU_FMT_FP32;
+  return launch8<kGradW>(p, s, d);
+}
+
+cudaError_t read_err_linear8(uint32_t* v, bool clear) {
+  cudaError_t e = cudaMemcpyFromSymbol(v, g_err_linear8, sizeof(uint32_t));
+  if (e == cudaSuccess && clear) {
+    const uint32_t z = 0;
+    e = cudaMemcpyToSymbol(g_err_linear8, &z, sizeof(uint32_t));
+  }
+  return e;
+}
+
+}  // namespace gq

@@ -2,7 +2,7 @@
 // argument, before anything is launched, and the launches.
 #include <climits>
 
-#include "block.h"
+#include "block8.h"
 
 namespace {
 
@@ -256,12 +256,13 @@ extern "C" int glu_block_linear_bwd_workspace(const glu_block_linear_bwd_args* a
 
 extern "C" int glu_block_device_errors(uint32_t* bits, int clear) {
   if (bits == nullptr) return GLU_EINVAL;
-  uint32_t norm = 0;
-  if (gq::read_err_linear(bits, clear != 0) != cudaSuccess || gq::read_err_norm(&norm, clear != 0) != cudaSuccess) {
+  uint32_t norm = 0, linear8 = 0;
+  if (gq::read_err_linear(bits, clear != 0) != cudaSuccess || gq::read_err_norm(&norm, clear != 0) != cudaSuccess ||
+      gq::read_err_linear8(&linear8, clear != 0) != cudaSuccess) {
     cudaGetLastError();
     return GLU_EDEVICE;
   }
-  *bits |= norm;
+  *bits |= norm | linear8;
   return GLU_OK;
 }
 extern "C" int glu_block_abi_version(void) { return GLU_BLOCK_ABI_VERSION; }

@@ -232,7 +232,7 @@ GLU_API int glu_block_linear_bwd(const glu_block_linear_bwd_args* args, void* st
 GLU_API int glu_block_linear_fwd_workspace(const glu_block_linear_fwd_args* args, size_t* bytes);
 GLU_API int glu_block_linear_bwd_workspace(const glu_block_linear_bwd_args* args, size_t* bytes);
 
-/* As glu_quant_device_errors, for the kernels of this header. */
+/* As glu_quant_device_errors, for the kernels of this header and of glu_block8.h. */
 GLU_API int glu_block_device_errors(uint32_t* bits, int clear);
 GLU_API int glu_block_abi_version(void);
 

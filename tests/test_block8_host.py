@@ -1,0 +1,165 @@
+"""Host-side checks of the 8-bit operators' C ABI and binding (no GPU needed)."""
+import ctypes
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+import torch
+
+import fp4_quant_gb300 as G
+from fp4_quant_gb300 import block8 as B
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "glu_block8.h")
+P = 1 << 12  # a 16-byte aligned placeholder address (never dereferenced)
+STRUCTS = {"glu_block8_quant_args": B.Quant8Args, "glu_block8_quant_weight_args": B.Quant8WeightArgs, "glu_block8_linear_args": B.Linear8Args,
+           "glu_block8_linear_dw_args": B.Linear8DwArgs, "glu_block8_glu_args": B.Glu8Args, "glu_block8_glu_bwd_args": B.Glu8BwdArgs}
+
+
+def test_every_declared_symbol_is_exported_and_bound():
+    names = set(re.findall(r"GLU_API\s+int\s+(glu_block8_\w+)\s*\(", open(HEADER).read()))
+    assert names == set(B._SIGNATURES)
+    lib = ctypes.CDLL(G.library_path())
+    assert all(hasattr(lib, n) for n in names)
+    assert G.block8_abi_version() == 1
+
+
+def test_binding_mirrors_the_header(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("no C compiler")
+    lines = ["#include <stdio.h>", "#include <stddef.h>", '#include "glu_block8.h"', "int main(void) {"]
+    for st, cls in STRUCTS.items():
+        lines.append(f'  printf("{st} %zu\\n", sizeof({st}));')
+        lines += [f'  printf("{st}.{n} %zu\\n", offsetof({st}, {n}));' for n, _ in cls._fields_]
+    src = tmp_path / "layout.c"
+    src.write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
+    subprocess.run(["gcc", "-std=c11", "-I", os.path.dirname(HEADER), str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = dict(line.split() for line in subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True, check=True).stdout.splitlines())
+    for st, cls in STRUCTS.items():
+        assert int(got[st]) == ctypes.sizeof(cls), st
+        for n, _ in cls._fields_:
+            assert int(got[f"{st}.{n}"]) == getattr(cls, n).offset, (st, n)
+
+
+def _status(name, cls, base, kw):
+    return B._func(name)(ctypes.byref(cls(**{**base, **kw})), None)
+
+
+QUANT = dict(M=300, K=64, ld_x=64, ld_xq=64, ld_q=64, ld_qc=64, x=P, q=P, s=P, qc=P, sc=P)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=0), G.GLU_EINVAL), (dict(K=0), G.GLU_EINVAL), (dict(x=None), G.GLU_EINVAL), (dict(xq=P, xs=P), G.GLU_EINVAL),
+    (dict(x=None, xq=P, xs=P), G.GLU_EINVAL), (dict(x=None, xq=P, q=None, s=None), G.GLU_EINVAL), (dict(s=None), G.GLU_EINVAL),
+    (dict(sc=None), G.GLU_EINVAL), (dict(q=None, s=None, qc=None, sc=None), G.GLU_EINVAL), (dict(reserved=1), G.GLU_EINVAL),
+    (dict(E=-1), G.GLU_EINVAL), (dict(E=4), G.GLU_EINVAL), (dict(offsets=P), G.GLU_EINVAL), (dict(E=4, offsets=P, qc=None, sc=None), G.GLU_EINVAL),
+    (dict(E=1025, offsets=P), G.GLU_ESHAPE), (dict(M=1 << 31), G.GLU_ESHAPE), (dict(K=(1 << 23) + 1), G.GLU_ESHAPE), (dict(ld_q=32), G.GLU_ESHAPE),
+    (dict(M=(1 << 31) - 1025, K=1 << 23, ld_x=1 << 23, ld_q=1 << 23, ld_qc=1 << 23), G.GLU_ESHAPE),
+    (dict(ld_qc=72), G.GLU_EALIGN), (dict(ld_x=68), G.GLU_EALIGN), (dict(x=P + 8), G.GLU_EALIGN), (dict(sc=P + 4), G.GLU_EALIGN)])
+def test_quant_refusals(kw, status):
+    assert _status("glu_block8_quant", B.Quant8Args, QUANT, kw) == status
+
+
+WEIGHT = dict(N=64, K=64, ld_w=64, stride_w=4096, ld_q=64, stride_q=4096, w=P, q=P, s=P, E=2)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(N=0), G.GLU_EINVAL), (dict(w=None), G.GLU_EINVAL), (dict(s=None), G.GLU_EINVAL), (dict(E=-1), G.GLU_EINVAL), (dict(reserved=2), G.GLU_EINVAL),
+    (dict(E=1025), G.GLU_ESHAPE), (dict(stride_w=4088), G.GLU_ESHAPE), (dict(ld_q=48), G.GLU_ESHAPE),
+    (dict(N=1 << 23, K=1 << 23, ld_w=1 << 23, ld_q=1 << 23, E=0), G.GLU_ESHAPE),
+    (dict(stride_q=4104), G.GLU_EALIGN), (dict(ld_w=70, stride_w=8192), G.GLU_EALIGN), (dict(q=P + 8), G.GLU_EALIGN)])
+def test_quant_weight_refusals(kw, status):
+    assert _status("glu_block8_quant_weight", B.Quant8WeightArgs, WEIGHT, kw) == status
+
+
+LINEAR = dict(M=64, N=48, K=64, ld_x=64, ld_w=64, stride_w=3072 + 64, ld_y=64, xq=P, xs=P, wq=P, ws=P, y=P, workspace=P, workspace_bytes=1 << 40)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(M=0), G.GLU_EINVAL), (dict(grad=2), G.GLU_EINVAL), (dict(xs=None), G.GLU_EINVAL), (dict(ws=None), G.GLU_EINVAL), (dict(y=None), G.GLU_EINVAL),
+    (dict(E=2), G.GLU_EINVAL), (dict(offsets=P), G.GLU_EINVAL), (dict(M=1 << 31), G.GLU_ESHAPE), (dict(N=(1 << 23) + 1), G.GLU_ESHAPE),
+    (dict(ld_x=48), G.GLU_ESHAPE), (dict(grad=1, ld_y=56), G.GLU_ESHAPE), (dict(E=2, offsets=P, stride_w=1024), G.GLU_ESHAPE),
+    (dict(ld_w=72), G.GLU_EALIGN), (dict(ld_y=68), G.GLU_EALIGN), (dict(xq=P + 8), G.GLU_EALIGN), (dict(ws=P + 4), G.GLU_EALIGN),
+    (dict(E=2, offsets=P, stride_w=3080), G.GLU_EALIGN)])
+def test_linear_refusals(kw, status):
+    assert _status("glu_block8_linear", B.Linear8Args, LINEAR, kw) == status
+
+
+DW = dict(C=3, N=48, K=64, ld_dy=48, ld_x=64, ld_dw=64, stride_dw=3072, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(C=0), G.GLU_EINVAL), (dict(dw_fmt=0), G.GLU_EINVAL), (dict(dys=None), G.GLU_EINVAL), (dict(dw=None), G.GLU_EINVAL),
+    (dict(E=2), G.GLU_EINVAL), (dict(E=4, offsets=P), G.GLU_EINVAL), (dict(C=1 << 24), G.GLU_ESHAPE), (dict(ld_dw=56), G.GLU_ESHAPE),
+    (dict(E=2, offsets=P, stride_dw=1024), G.GLU_ESHAPE), (dict(ld_dy=56), G.GLU_EALIGN), (dict(ld_dw=68), G.GLU_EALIGN), (dict(xs=P + 4), G.GLU_EALIGN)])
+def test_linear_dw_refusals(kw, status):
+    assert _status("glu_block8_linear_dw", B.Linear8DwArgs, DW, kw) == status
+
+
+GLU = dict(M=64, H=48, ld_gate=48, ld_up=48, ld_h=48, ld_hq=48, ld_gq=48, ld_uq=48, gate=P, up=P, hq=P, hs=P, gq=P, gs=P, uq=P, us=P)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(act=5), G.GLU_EINVAL), (dict(act=16), G.GLU_EINVAL), (dict(M=0), G.GLU_EINVAL), (dict(gate=None), G.GLU_EINVAL), (dict(us=None), G.GLU_EINVAL),
+    (dict(h=P), G.GLU_EINVAL), (dict(hq=None), G.GLU_EINVAL), (dict(hs=None), G.GLU_EINVAL), (dict(reserved=1), G.GLU_EINVAL),
+    (dict(H=(1 << 23) + 1), G.GLU_ESHAPE), (dict(ld_up=40), G.GLU_ESHAPE), (dict(ld_gq=56), G.GLU_EALIGN), (dict(ld_gate=52), G.GLU_EALIGN),
+    (dict(gs=P + 4), G.GLU_EALIGN)])
+def test_glu_refusals(kw, status):
+    assert _status("glu_block8_glu", B.Glu8Args, GLU, kw) == status
+
+
+GLU_BWD = dict(M=64, H=128, ld_gq=128, ld_uq=128, ld_dh=128, ld_d=256, ld_h=128, ld_dq=256, ld_dqc=256, ld_hqc=128, gq=P, gs=P, uq=P, us=P, dh=P)
+PLAIN, QUANTISED = dict(d=P, h=P), dict(dq=P, ds=P, dqc=P, dsc=P, hqc=P, hsc=P)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(**PLAIN, act=5), G.GLU_EINVAL), (dict(**PLAIN, dh=None), G.GLU_EINVAL), (dict(**PLAIN, **QUANTISED), G.GLU_EINVAL), (dict(), G.GLU_EINVAL),
+    (dict(**PLAIN, E=1, offsets=P), G.GLU_EINVAL), (dict(**{**QUANTISED, "ds": None}), G.GLU_EINVAL), (dict(**{**QUANTISED, "hsc": None}), G.GLU_EINVAL),
+    (dict(**QUANTISED, h=P), G.GLU_EINVAL), (dict(**QUANTISED, E=3), G.GLU_EINVAL), (dict(**QUANTISED, H=64), G.GLU_ESHAPE),
+    (dict(**PLAIN, H=(1 << 22) + 128), G.GLU_ESHAPE), (dict(**PLAIN, ld_d=248), G.GLU_ESHAPE), (dict(**QUANTISED, ld_hqc=112), G.GLU_ESHAPE),
+    (dict(**QUANTISED, ld_dq=264), G.GLU_EALIGN), (dict(**PLAIN, ld_dh=132), G.GLU_EALIGN), (dict(**{**QUANTISED, "dsc": P + 4}), G.GLU_EALIGN)])
+def test_glu_bwd_refusals(kw, status):
+    assert _status("glu_block8_glu_bwd", B.Glu8BwdArgs, GLU_BWD, kw) == status
+
+
+def test_null_arguments():
+    for name in B._SIGNATURES:
+        if name == "glu_block8_linear_workspace":
+            assert B._func(name)(ctypes.byref(B.Linear8Args(**LINEAR)), None) == G.GLU_EINVAL
+        elif name != "glu_block8_abi_version":
+            assert B._func(name)(None, None) == G.GLU_EINVAL
+
+
+def test_accepted_arguments_get_as_far_as_the_device():
+    if torch.cuda.is_available():
+        pytest.skip("placeholder addresses must not reach a device")
+    for name, cls, base in [("glu_block8_quant", B.Quant8Args, QUANT), ("glu_block8_quant", B.Quant8Args, {**QUANT, "E": 300, "offsets": P}),
+                            ("glu_block8_quant_weight", B.Quant8WeightArgs, WEIGHT),
+                            ("glu_block8_linear", B.Linear8Args, LINEAR), ("glu_block8_linear", B.Linear8Args, {**LINEAR, "grad": 1}),
+                            ("glu_block8_linear_dw", B.Linear8DwArgs, DW), ("glu_block8_linear_dw", B.Linear8DwArgs, {**DW, "dw_fmt": 3}),
+                            ("glu_block8_glu", B.Glu8Args, GLU), ("glu_block8_glu_bwd", B.Glu8BwdArgs, {**GLU_BWD, **PLAIN}),
+                            ("glu_block8_glu_bwd", B.Glu8BwdArgs, {**GLU_BWD, **QUANTISED})]:
+        assert _status(name, cls, base, {}) == G.GLU_EDEVICE
+
+
+def test_binding_refuses_on_the_cpu():
+    x = torch.zeros(4, 16, dtype=torch.bfloat16)
+    row = {"q": torch.zeros(4, 16, dtype=torch.float8_e4m3fn), "s": torch.ones(1, 4)}
+    for call in (lambda: G.quant8(x), lambda: G.quant8_weight(x), lambda: G.linear8(row, row), lambda: G.linear8_dx(row, row),
+                 lambda: G.linear8_dw({"qc": torch.zeros(128, 16, dtype=torch.float8_e4m3fn)}, {"qc": torch.zeros(128, 16, dtype=torch.float8_e4m3fn)}),
+                 lambda: G.glu8(x, x), lambda: G.glu8_bwd(row, row, x), lambda: G.quant8(row, rows=False, cols=True)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    with pytest.raises(ValueError, match="rows=False"):
+        G.quant8(row)
+    with pytest.raises(ValueError, match="rows, cols"):
+        G.quant8(x, rows=False)
+    with pytest.raises(ValueError, match="column form"):
+        G.quant8(x, offsets=torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="offsets"):
+        G.linear8(row, {"q": torch.zeros(2, 4, 16, dtype=torch.float8_e4m3fn), "s": torch.ones(2, 1, 1)})
+    with pytest.raises(TypeError, match="dtype"):
+        G.linear8_dw({"qc": torch.zeros(128, 16)}, {"qc": torch.zeros(128, 16)}, dtype=torch.float16)
+    with pytest.raises(ValueError, match="128"):
+        G.linear8_dw({"qc": torch.zeros(100, 16)}, {"qc": torch.zeros(100, 16)})

@@ -1,0 +1,166 @@
+"""The operators in 8 bits together, as the example runs them, and the ways in which a
+program may call them."""
+import os
+import sys
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+
+import expert_ffn8 as X  # noqa: E402
+import fp4_quant_gb300 as G  # noqa: E402
+
+DEV = torch.device("cuda:0")
+BF, F8 = torch.bfloat16, torch.float8_e4m3fn
+
+
+def _rand(*shape, seed, scale=1.0):
+    return (scale * torch.randn(*shape, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV)).to(BF)
+
+
+def _sorted(R, E, seed):
+    ids = torch.randint(-1, E, (R, 1), generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV)
+    return G.route(ids, E)
+
+
+def _reference(xs, w, offsets, dy):
+    t = {k: v.double().requires_grad_(True) for k, v in {**w, "xs": xs}.items()}
+    H = w["down"].shape[2]
+    cuts = offsets.tolist()
+    rows = [torch.zeros(0, xs.shape[1], dtype=torch.float64, device=DEV)]
+    for e, (a, b) in enumerate(zip(cuts, cuts[1:])):
+        u = t["xs"][a:b] @ t["up"][e].t()
+        rows.append((torch.nn.functional.silu(u[:, :H]) * u[:, H:]) @ t["down"][e].t())
+    y = torch.cat(rows)
+    (y * dy[:cuts[-1]].double()).sum().backward()
+    return y.detach(), {k: v.grad for k, v in t.items()}
+
+
+@pytest.mark.parametrize("R,D,H,E", [(1, 128, 128, 4), (100, 264, 128, 6), (700, 512, 256, 16), (1500, 256, 384, 3)])
+def test_experts_forward_and_backward(R, D, H, E):
+    w = X.make_weights(D, H, E, seed=R)
+    xs, dy = _rand(R, D, seed=R + 1), _rand(R, D, seed=R + 2)
+    off = _sorted(R, E, R + 3)["offsets"]
+    used = int(off[-1])
+    w8 = X.quantise(w)
+    y, s = X.forward(xs, w8, off)
+    g = X.backward(dy, w8, s, off)
+    want_y, want = _reference(xs, w, off, dy)
+    # roundings to E4M3 one behind the other: x, up, h, down in y; x or dy, down, dh's
+    # operands, gate, up, d and the other operand in the gradients: seven at most, 2^-4
+    # each at worst relative to the norm of what they round
+    assert bool((y[used:] == 0).all()) and bool((g["xs"][used:] == 0).all())
+    for name, a, b in [("y", y[:used], want_y)] + [(n, g[n], want[n]) for n in g]:
+        assert a.shape == b.shape and float((a.double() - b).norm()) <= 7 * 2.0 ** -4 * float(b.norm()), name
+    empty = [e for e in range(E) if int(off[e]) == int(off[e + 1])]
+    assert all(bool((g[n][empty] == 0).all()) for n in ("up", "down"))
+
+
+def _calls(seed):
+    """Every call once, small; what they return, flat."""
+    off = torch.tensor([0, 40, 40, 190, 200], dtype=torch.int32, device=DEV)
+    x, dy = _rand(210, 256, seed=seed), _rand(210, 128, seed=seed + 1)
+    w = G.quant8_weight(_rand(4, 128, 256, seed=seed + 2, scale=0.1))
+    gate, up, dh = (_rand(210, 256, seed=seed + 3 + i) for i in range(3))
+
+    def run():
+        x8 = G.quant8(x, cols=True, offsets=off)
+        d8 = G.quant8(dy, cols=True, offsets=off)
+        a = G.glu8(gate, up)
+        b = G.glu8_bwd(a["gate"], a["up"], dh, quant=True, offsets=off)
+        p = G.glu8_bwd(a["gate"], a["up"], dh)
+        k = G.quant8({"q": x8["q"], "s": x8["s"]}, rows=False, cols=True, offsets=off)
+        few = {"q": x8["q"][:1], "s": x8["s"][:, :1].contiguous()}
+        one = {"q": w["q"][0], "s": w["s"][0]}
+        return [x8["q"], x8["s"], x8["qc"], x8["sc"], k["qc"], k["sc"], G.linear8(x8, w, offsets=off), G.linear8_dx(d8, w, offsets=off),
+                G.linear8_dw(d8, x8, offsets=off), G.linear8_dw(d8, x8, offsets=off, dtype=torch.float32), G.linear8(few, one), G.linear8(x8, one),
+                a["h"]["q"], a["h"]["s"], a["gate"]["q"], a["up"]["s"], *b["d"].values(), *b["h"].values(), p["d"], p["h"],
+                w["q"], w["s"]]
+    return run
+
+
+def _equal(a, b):
+    return all(torch.equal(p.view(torch.uint8) if p.dtype is F8 else p, q.view(torch.uint8) if q.dtype is F8 else q) for p, q in zip(a, b))
+
+
+def test_calls_repeat_bit_for_bit():
+    run = _calls(1)
+    first = run()
+    assert all(_equal(first, run()) for _ in range(3))
+
+
+def test_calls_in_a_graph_and_two_graphs_at_once():
+    runs = [_calls(10), _calls(20)]
+    want = [r() for r in runs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for r in runs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(r())
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(3):
+        for o in outs:
+            for t in o[:-2]:  # the last two are the weights, quantised outside the graphs: their inputs
+                t.view(torch.uint8).fill_(0x55)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        assert all(_equal(a[:-2], b[:-2]) for a, b in zip(outs, want))
+
+
+def test_calls_on_a_given_stream():
+    x = _rand(300, 384, seed=5)
+    w = _rand(256, 384, seed=6, scale=0.1)
+    want = G.linear8(G.quant8(x), G.quant8_weight(w))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for stream in (s, s.cuda_stream):
+        y = G.linear8(G.quant8(x, stream=stream), G.quant8_weight(w, stream=stream), stream=stream)
+        s.synchronize()
+        assert torch.equal(y, want)
+
+
+def test_outputs_given_and_what_stands_beside_them():
+    x, w = _rand(70, 136, seed=7), _rand(200, 136, seed=8)
+    x8, w8 = G.quant8(x, cols=True), G.quant8_weight(w)
+    q = torch.full((70, 176), 7, dtype=torch.uint8, device=DEV)
+    qc = torch.full((128, 160), 7, dtype=torch.uint8, device=DEV)
+    o = G.quant8(x, cols=True, out={"q": q[:, :136].view(F8), "qc": qc[:, 16:152].view(F8)})
+    assert _equal([o["q"], o["qc"], o["s"], o["sc"]], [x8["q"], x8["qc"], x8["s"], x8["sc"]])
+    assert bool((q[:, 136:] == 7).all()) and bool((qc[:, :16] == 7).all()) and bool((qc[:, 152:] == 7).all())
+    y = torch.full((70, 208), -7.0, dtype=BF, device=DEV)
+    G.linear8(x8, w8, out=y[:, :200])
+    assert torch.equal(y[:, :200], G.linear8(x8, w8)) and bool((y[:, 200:] == -7).all())
+    d8 = G.quant8(_rand(70, 200, seed=9), rows=False, cols=True)
+    dw = torch.full((200, 144), -7.0, device=DEV)
+    G.linear8_dw(d8, x8, dtype=torch.float32, out=dw[:, :136])
+    assert torch.equal(dw[:, :136], G.linear8_dw(d8, x8, dtype=torch.float32)) and bool((dw[:, 136:] == -7).all())
+    a = G.glu8(x, x)
+    d = torch.full((70, 280), -7.0, dtype=BF, device=DEV)
+    b = G.glu8_bwd(a["gate"], a["up"], x, out={"d": d[:, :272]})
+    assert b["d"].data_ptr() == d.data_ptr() and bool((d[:, 272:] == -7).all())
+    assert torch.equal(d[:, :272], G.glu8_bwd(a["gate"], a["up"], x)["d"])
+
+
+def test_column_forms_of_parts_and_views():
+    """Halves of a projection, slices of a wider matrix: strides of their own."""
+    wide = _rand(150, 512, seed=11)
+    for view in (wide[:, 128:384], wide[:, 256:], wide[20:]):
+        a, b = G.quant8(view, cols=True), G.quant8(view.contiguous(), cols=True)
+        assert _equal([v for v in a.values()], [v for v in b.values()])
+    a, b = G.glu8(wide[:, :256], wide[:, 256:]), G.glu8(wide[:, :256].contiguous(), wide[:, 256:].contiguous())
+    assert _equal([a[k][n] for k in a for n in ("q", "s")], [b[k][n] for k in b for n in ("q", "s")])
+    odd = _rand(33, 67, seed=12)  # contiguous rows that do not start on 16 bytes are copied first
+    padded = torch.zeros(33, 72, dtype=BF, device=DEV)
+    padded[:, :67] = odd
+    assert _equal(list(G.quant8(odd, cols=True).values()), list(G.quant8(padded[:, :67], cols=True).values()))
