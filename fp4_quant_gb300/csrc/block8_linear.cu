@@ -198,7 +198,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
         const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
         for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
           const uint32_t b = i & 1u;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
           if (!ok) {
             if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
             break;
@@ -332,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
         tc::fence_before();
         __syncwarp();
         if (lane == 0) {
-          peer_arrive(tempty0 + 8u * b);
+          peer_arrive_relaxed(tempty0 + 8u * b);
           mbar_arrive(&ctl->sempty[slot]);
         }
         ++i;

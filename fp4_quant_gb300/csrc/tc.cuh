@@ -183,6 +183,26 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   }
   return false;
 }
+// The same pair for tensor memory alone, where no other memory is handed over:
+// tcgen05.fence::before_thread_sync ahead of the arrival and after_thread_sync
+// behind the wait order the tcgen05 operations, and relaxed ones are enough.  (An
+// arrival that releases at cluster scope waits for all that its thread has in
+// flight.)
+__device__ __forceinline__ void peer_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_relaxed(uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < kWaitBudget; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{.reg .pred p; mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p;}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+  }
+  return false;
+}
 // Tile loads into this CTA that complete on a barrier of either CTA of the pair
 // (`bar`: a shared::cluster address).
 __device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, uint32_t bar) {
