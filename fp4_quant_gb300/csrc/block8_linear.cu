@@ -10,18 +10,20 @@
 // Tiles and walk are those of the bf16 layers (block_tiles.cuh): 256 rows of D by
 // up to 256 columns for a pair of CTAs, the tokens as the columns of y and dx.
 // One block of the sum is one slice of the ring (128 codes are the 128 bytes of
-// the swizzle).  Its products go into two accumulators in tensor memory, of half
-// of the columns each, and while the tensor cores sum the next ones into others
-// (there are four), eight warps read these, scale them and add them to what they
-// hold in registers, 128 fp32 per thread.  An accumulator goes back as soon as it
-// is in registers: from its products' issue to there it takes the hand-over
-// between the CTAs twice, and four in flight hide that (two of all columns, each
-// held until its values were added: 301 us at 4096 x 8192 x 7168; see below).  Their share of the
+// the swizzle) and one accumulator in tensor memory: while the tensor cores sum
+// the next block into the other one, eight warps read this one, scale it and add
+// it to what they hold in registers, 128 fp32 per thread.  Their share of the
 // register file is raised for that (setmaxnreg), the other four warps' lowered.
 // Two warps fetch the scales, block by block ahead, into a ring of their own; a
 // weight's scale is one number for the 128 rows of a CTA and goes into the
 // columns' scales there, so that a value costs half a two-wide multiply-add (dw:
 // a multiplication by its row's scale as well).
+//
+// What a thread has of the accumulator decides what its scales cost: with a row
+// per thread it needs every column's, 128 KB out of shared memory per block at 128
+// bytes a clock, and 4096 x 8192 x 7168 takes 299 us (215 with the scales left
+// out, 170 with the products alone).  As fragments (a quarter of the columns, four
+// rows) it is a quarter of that.
 #include <cstring>
 
 #include "block8.h"
@@ -38,10 +40,9 @@ constexpr int kStageBytes8 = 2 * kOperand8;
 constexpr int kScaleSlots = 4;
 constexpr int kLoadWarps = 4, kEpiWarps8 = 8;  // loads, products, two of scales; epilogue
 constexpr int kThreads8 = (kLoadWarps + kEpiWarps8) * 32;
-// 168 registers per thread at launch: 128 x 72 + 256 x 216 = 384 x 168
-constexpr int kFewRegs = 72, kManyRegs = 216;
-constexpr int kAccs = 4, kAccCols = kTile / 2;  // accumulators in tensor memory and their columns
-constexpr uint32_t kTmemCols8 = kAccs * kAccCols;
+// 168 registers per thread at launch: 128 x 56 + 256 x 224 = 384 x 168
+constexpr int kFewRegs = 56, kManyRegs = 224;
+constexpr uint32_t kTmemCols8 = 2 * kTile;
 constexpr uint32_t kIdesc8 = tc::idesc_e4m3_f32(kTile, 0);  // the columns are added per tile
 
 struct Scales {
@@ -51,8 +52,8 @@ struct Scales {
 struct Ctl8 {
   uint64_t full[kStages8];   // CTA 0's: its arrival and the bytes of both CTAs
   uint64_t empty[kStages8];  // each CTA's own: the products on its stage are done
-  uint64_t tfull[kAccs];     // each CTA's own: a block's sum over half of the columns is complete
-  uint64_t tempty[kAccs];    // CTA 0's: the warps of both have read it
+  uint64_t tfull[2];         // each CTA's own: a block's sum is complete
+  uint64_t tempty[2];        // CTA 0's: the warps of both have read it
   uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // each CTA's own scales
   uint64_t done;             // each CTA's own: all products are done
   uint32_t tmem;
@@ -96,6 +97,35 @@ __device__ __forceinline__ Tile tile8_at(const Linear8P& p, const TilePlan& plan
   return x;
 }
 
+// An 8 x 8 block of 16-bit values (lane l: row l / 4, columns 2 (l % 4) and the next) transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+// The 4 x 4 block of words that a quad of lanes holds, transposed.
+__device__ __forceinline__ void word_transpose(uint32_t (&w)[4], int lane) {
+  const bool odd = lane & 1, up = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[i] : w[i + 1], 1);
+    if (odd) w[i] = got;
+    else w[i + 1] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[i] : w[i + 2], 2);
+    if (up) w[i] = got;
+    else w[i + 2] = got;
+  }
+}
+// Eight bf16 of a row (16-byte aligned), or its first n; they stay in L2 (as in linear).
+__device__ __forceinline__ void store_row8(uint16_t* o, int32_t n, const uint32_t (&w)[4]) {
+  const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
+  if (n >= 8) *reinterpret_cast<uint4*>(o) = v;
+  else put8(o, n, v);
+}
+
 template <int REGS>
 __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
@@ -123,7 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    for (int b = 0; b < kAccs; ++b) {
+    for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl->tfull[b], 1);
       mbar_init(&ctl->tempty[b], 2 * kEpiWarps8);
     }
@@ -193,43 +223,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
     } else if (warp == 1) {
       // ------------------------------------------------------------- MMA --
       int s = 0;
-      uint32_t parity = 0, i = 0;  // i: accumulators filled
+      uint32_t parity = 0, i = 0;  // i: blocks summed
       const uint32_t a_addr = smem_u32(stages);
       const uint64_t ad0 = kAmn ? tc::sw128_mnmajor_desc(a_addr, kOperand8) : tc::sw128_kmajor_desc(a_addr);
       const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand8, kOperand8) : tc::sw128_kmajor_desc(a_addr + kOperand8);
       bool ok = true;
       for (int32_t t = pair; t < tiles && ok && rank == 0; t += pairs) {
         const Tile x = tile8_at<PROD>(p, ctl->plan, t);
-        const uint32_t idesc = kIdesc | (uint32_t(x.n >> 4) << 17);
-        // B's second half: the columns behind the first quarter (K-major: rows of 128
-        // bytes; M/N-major: columns of a byte)
-        const uint32_t second = uint32_t(kBmn ? x.n / 4 : x.n / 4 * kBK8) >> 4;
-        for (int32_t k = x.k0; k < x.k_end && ok; k += kBK8) {
+        const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
+        for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
+          const uint32_t b = i & 1u;
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
+            break;
+          }
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
           if (!ok) {
             if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
             break;
           }
-          const uint64_t ad = ad0 + uint32_t(s * (kStageBytes8 >> 4)), bd = bd0 + uint32_t(s * (kStageBytes8 >> 4));
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint64_t ad = ad0 + uint32_t(s * (kStageBytes8 >> 4)), bd = bd0 + uint32_t(s * (kStageBytes8 >> 4));
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t b = i % kAccs;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&ctl->tempty[b], ((i / kAccs) & 1u) ^ 1u));
-            if (!ok) {
-              if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
-              break;
-            }
-            tc::fence_after();
-            if (tc::elect_one()) {
-#pragma unroll
-              for (int j = 0; j < kBK8 / 32; ++j)
-                tc::pair_mma_e4m3(tmem + b * kAccCols, ad + j * (kAmn ? 256 : 2), bd + (h ? second : 0u) + j * (kBmn ? 256 : 2), idesc, uint32_t(j));
-              tc::pair_commit(&ctl->tfull[b]);
-              if (h == 1) tc::pair_commit(&ctl->empty[s]);
-            }
-            __syncwarp();
-            ++i;
+            for (int j = 0; j < kBK8 / 32; ++j)
+              tc::pair_mma_e4m3(tmem + b * kTile, ad + j * (kAmn ? 256 : 2), bd + j * (kBmn ? 256 : 2), idesc, uint32_t(j));
+            tc::pair_commit(&ctl->empty[s]);
+            tc::pair_commit(&ctl->tfull[b]);
           }
+          __syncwarp();
+          ++i;
           if (++s == kStages8) s = 0, parity ^= 1u;
         }
       }
@@ -300,108 +324,106 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
     bool ok = true;
     for (int32_t t = pair; t < tiles && ok; t += pairs) {
       const Tile x = tile8_at<PROD>(p, ctl->plan, t);
-      // columns: those that CTA `group` loaded, half of the tile's; acc[2 h + q] has
-      // column 32 q of the accumulator h's share on
-      float2 acc[4][16];
+      // acc[q][i][k]: row lane / 4 + 8 i of the warp's 32, columns 8 k + 2 (lane % 4)
+      // and the next of the 32 from c0 + 32 q on
+      float2 acc[4][4][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) acc[q][j] = make_float2(0.0f, 0.0f);
-      const int share = x.n / 4, c0 = group * (x.n / 2);
-      for (int32_t k = x.k0; k < x.k_end && ok; k += kBK8) {
-        const int slot = int((i / 2) % kScaleSlots);
-        ok = mbar_wait(&ctl->sfull[slot], (i / 2 / kScaleSlots) & 1u);
-        const Scales& sc = ctl->scales[slot];
-        const float2 row = PROD == kGradW ? both(sc.row[quarter * 32 + lane]) : make_float2(1.0f, 1.0f);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t b = i % kAccs;
-          ok = ok && mbar_wait(&ctl->tfull[b], (i / kAccs) & 1u);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
-            break;
-          }
-          tc::fence_after();
-          const uint32_t base = lanes + b * kAccCols + uint32_t(group * share);
-          uint32_t r[2][32];
-          tc::ld32(base, r[0]);
-          if (share > 32) tc::ld32(base + 32, r[1]);
-          tc::wait_ld();
-          tc::fence_before();
-          __syncwarp();
-          if (lane == 0) peer_arrive_relaxed(tempty0 + 8u * b);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            if (32 * q >= share) break;
-            const float4* s4 = reinterpret_cast<const float4*>(sc.col + c0 + h * share + 32 * q);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 s = s4[j];
-              float2 lo = make_float2(__uint_as_float(r[q][4 * j]), __uint_as_float(r[q][4 * j + 1]));
-              float2 hi = make_float2(__uint_as_float(r[q][4 * j + 2]), __uint_as_float(r[q][4 * j + 3]));
-              if (PROD == kGradW) lo = mul_2(lo, row), hi = mul_2(hi, row);
-              acc[2 * h + q][2 * j] = fma_2(lo, make_float2(s.x, s.y), acc[2 * h + q][2 * j]);
-              acc[2 * h + q][2 * j + 1] = fma_2(hi, make_float2(s.z, s.w), acc[2 * h + q][2 * j + 1]);
-            }
-          }
-          ++i;
+        for (int j = 0; j < 16; ++j) acc[q][j / 4][j % 4] = make_float2(0.0f, 0.0f);
+      const int c0 = group * (x.n / 2), c1 = c0 + x.n / 2;  // this group's columns
+      for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
+        const uint32_t b = i & 1u;
+        const int slot = int(i % kScaleSlots);
+        ok = mbar_wait(&ctl->sfull[slot], (i / kScaleSlots) & 1u) && mbar_wait(&ctl->tfull[b], (i >> 1) & 1u);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) {
+          if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
+          break;
         }
+        tc::fence_after();
+        const Scales& sc = ctl->scales[slot];
+        float row[4];
+        if (PROD == kGradW) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) row[j] = sc.row[quarter * 32 + (lane >> 2) + 8 * j];
+        }
+        const float* col = sc.col + c0 + 2 * (lane & 3);
+        const uint32_t base = lanes + b * kTile + uint32_t(c0);
+        uint32_t r[2][2][16];
+        float2 s[2][4];
+        auto fetch = [&](int q) {
+          tc::ld16x32(base + uint32_t(32 * q), r[q & 1][0]);
+          tc::ld16x32(base + (16u << 16) + uint32_t(32 * q), r[q & 1][1]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s[q & 1][j] = *reinterpret_cast<const float2*>(col + 32 * q + 8 * j);
+        };
+        fetch(0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (c0 + 32 * q >= c1) break;
+          tc::wait_ld();
+          if (q < 3 && c0 + 32 * (q + 1) < c1) fetch(q + 1);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const uint32_t* v = &r[q & 1][y >> 1][4 * j + 2 * (y & 1)];
+              float2 d = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              if (PROD == kGradW) d = mul_2(d, both(row[y]));
+              acc[q][y][j] = fma_2(d, s[q & 1][j], acc[q][y][j]);
+            }
+        }
+        tc::fence_before();
         __syncwarp();
-        if (ok && lane == 0) mbar_arrive(&ctl->sempty[slot]);
+        if (lane == 0) {
+          peer_arrive_relaxed(tempty0 + 8u * b);
+          mbar_arrive(&ctl->sempty[slot]);
+        }
+        ++i;
       }
       if (!ok) break;
       const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
+      const int32_t b_end = min(x.b_end, x.b0 + c1);                     // of this group
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int own = c0 + (q >> 1) * share, c = own + 32 * (q & 1);
-        const int32_t b_end = min(x.b_end, x.b0 + own + share);  // of this share
-        if (x.b0 + c >= b_end) continue;
+        const int32_t at = x.b0 + c0 + 32 * q;
+        if (at >= b_end) break;
         if (PROD != kGradW) {
-          const int32_t token = x.b0 + c + (lane & 3), col = row0 + (lane & ~3);
-          const TokenView view = {p.width - col, b_end - token};
-          uint32_t w[8][2];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            w[j][0] = bf16x2_of(acc[q][2 * j].x, acc[q][2 * j].y);
-            w[j][1] = bf16x2_of(acc[q][2 * j + 1].x, acc[q][2 * j + 1].y);
-          }
-          store_quads(static_cast<uint16_t*>(p.out) + int64_t(token) * p.ld_out + col, p.ld_out, view, w, lane);
-        } else if (p.f32) {
-          // 16 columns at a time: pieces of four
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) w[2 * j] = __float_as_uint(acc[q][8 * h + j].x), w[2 * j + 1] = __float_as_uint(acc[q][8 * h + j].y);
-            piece_transpose(w, lane);
-            const int32_t row = row0 + (lane & ~3), at = x.b0 + c + 16 * h + 4 * (lane & 3), left = b_end - at;
-            float* out = static_cast<float*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + at;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              if (row + j >= p.width) continue;
-              if (left >= 4) {
-                *reinterpret_cast<uint4*>(out + j * p.ld_out) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-              } else {
-#pragma unroll
-                for (int y = 0; y < 3; ++y)
-                  if (y < left) out[j * p.ld_out + y] = __uint_as_float(w[4 * j + y]);
-              }
-            }
-          }
-        } else {
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = bf16x2_of(acc[q][j].x, acc[q][j].y);
-          piece_transpose(w, lane);
-          const int32_t row = row0 + (lane & ~3), left = b_end - x.b0 - c - 8 * (lane & 3);
-          uint16_t* out = static_cast<uint16_t*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + x.b0 + c + 8 * (lane & 3);
+          // eight tokens at a time: their rows' 8 x 8 blocks transposed, then four
+          // lanes' words, so that a lane has eight columns of one token
+          const int32_t n = row0 + 8 * (lane & 3), left = p.width - n;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (row + j >= p.width || left <= 0) continue;
-            const uint4 v = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            if (left >= 8) *reinterpret_cast<uint4*>(out + j * p.ld_out) = v;
-            else put8(out + j * p.ld_out, left, v);
+            uint32_t w[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) w[y] = transpose8x8(bf16x2_of(acc[q][y][j].x, acc[q][y][j].y));
+            word_transpose(w, lane);
+            const int32_t token = at + 8 * j + (lane >> 2);
+            if (token < b_end && left > 0) store_row8(static_cast<uint16_t*>(p.out) + int64_t(token) * p.ld_out + n, left, w);
+          }
+        } else {
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const int32_t row = row0 + (lane >> 2) + 8 * y;
+            if (p.f32) {
+              float* out = static_cast<float*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + at + 2 * (lane & 3);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int32_t left = b_end - at - 8 * j - 2 * (lane & 3);
+                if (row >= p.width || left <= 0) continue;
+                if (left > 1) *reinterpret_cast<float2*>(out + 8 * j) = acc[q][y][j];
+                else out[8 * j] = acc[q][y][j].x;
+              }
+            } else {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) w[j] = bf16x2_of(acc[q][y][j].x, acc[q][y][j].y);
+              word_transpose(w, lane);
+              const int32_t c = at + 8 * (lane & 3), left = b_end - c;
+              if (row < p.width && left > 0)
+                store_row8(static_cast<uint16_t*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + c, left, w);
+            }
           }
         }
       }
