@@ -37,7 +37,7 @@ namespace {
 constexpr int kBK8 = 128, kStages8 = 6;
 constexpr int kOperand8 = kHalf * kBK8;  // 16 KB
 constexpr int kStageBytes8 = 2 * kOperand8;
-constexpr int kScaleSlots = 4;
+constexpr int kScaleSlots = 2;  // as many as accumulators, whose barriers count the scales too
 constexpr int kLoadWarps = 4, kEpiWarps8 = 8;  // loads, products, two of scales; epilogue
 constexpr int kThreads8 = (kLoadWarps + kEpiWarps8) * 32;
 // 168 registers per thread at launch: 128 x 56 + 256 x 224 = 384 x 168
@@ -52,9 +52,9 @@ struct Scales {
 struct Ctl8 {
   uint64_t full[kStages8];   // CTA 0's: its arrival and the bytes of both CTAs
   uint64_t empty[kStages8];  // each CTA's own: the products on its stage are done
-  uint64_t tfull[2];         // each CTA's own: a block's sum is complete
+  uint64_t tfull[2];         // each CTA's own: a block's sum is complete, and its scales are there
   uint64_t tempty[2];        // CTA 0's: the warps of both have read it
-  uint64_t sfull[kScaleSlots], sempty[kScaleSlots];  // each CTA's own scales
+  uint64_t sempty[kScaleSlots];  // each CTA's own: its warps have used the scales
   uint64_t done;             // each CTA's own: all products are done
   uint32_t tmem;
   alignas(16) Scales scales[kScaleSlots];
@@ -154,13 +154,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       mbar_init(&ctl->empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&ctl->tfull[b], 1);
+      mbar_init(&ctl->tfull[b], 2);
       mbar_init(&ctl->tempty[b], 2 * kEpiWarps8);
     }
-    for (int s = 0; s < kScaleSlots; ++s) {
-      mbar_init(&ctl->sfull[s], 1);
-      mbar_init(&ctl->sempty[s], kEpiWarps8);
-    }
+    for (int s = 0; s < kScaleSlots; ++s) mbar_init(&ctl->sempty[s], kEpiWarps8);
     mbar_init(&ctl->done, 1);
     fence_barrier_init();
   }
@@ -233,14 +230,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
         const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
         for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
           const uint32_t b = i & 1u;
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
-          if (!ok) {
-            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
-            break;
-          }
           ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->full[s], parity));
           if (!ok) {
             if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
+            break;
+          }
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait_relaxed(&ctl->tempty[b], ((i >> 1) & 1u) ^ 1u));
+          if (!ok) {
+            if (lane == 0) atomicOr(&g_err_linear8, kErrWaitEmpty);
             break;
           }
           tc::fence_after();
@@ -305,7 +302,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
             for (int j = 0; j < 4; ++j) o.row[32 * j + lane] = row[j];
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->sfull[slot]);
+          if (lane == 0) mbar_arrive(&ctl->tfull[slot]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) col[j] = next_col[j];
 #pragma unroll
@@ -332,38 +329,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
 #pragma unroll
         for (int j = 0; j < 16; ++j) acc[q][j / 4][j % 4] = make_float2(0.0f, 0.0f);
       const int c0 = group * (x.n / 2), c1 = c0 + x.n / 2;  // this group's columns
-      for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
-        const uint32_t b = i & 1u;
-        const int slot = int(i % kScaleSlots);
-        ok = mbar_wait(&ctl->sfull[slot], (i / kScaleSlots) & 1u) && mbar_wait(&ctl->tfull[b], (i >> 1) & 1u);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) {
-          if (lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
-          break;
-        }
+      const int chunks = x.n > kTile / 2 ? 4 : 2;  // of 32 columns; what is read past c1 is not stored
+      uint32_t r[2][2][16];
+      float2 s[2][4];
+      // block i's sum and scales are there
+      auto ready = [&] {
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait(&ctl->tfull[i & 1u], (i >> 1) & 1u));
+        if (!ok && lane == 0) atomicOr(&g_err_linear8, kErrWaitFull);
         tc::fence_after();
+      };
+      auto fetch = [&](int q) {
+        const uint32_t at = lanes + (i & 1u) * kTile + uint32_t(c0 + 32 * q);
+        tc::ld16x32(at, r[q & 1][0]);
+        tc::ld16x32(at + (16u << 16), r[q & 1][1]);
+        const float* col = ctl->scales[i % kScaleSlots].col + c0 + 32 * q + 2 * (lane & 3);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[q & 1][j] = *reinterpret_cast<const float2*>(col + 8 * j);
+      };
+      if (x.k0 < x.k_end) {
+        ready();
+        if (ok) fetch(0);
+      }
+      for (int32_t k = x.k0; k < x.k_end && ok; k += kBK8) {
+        const int slot = int(i % kScaleSlots);
         const Scales& sc = ctl->scales[slot];
         float row[4];
         if (PROD == kGradW) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) row[j] = sc.row[quarter * 32 + (lane >> 2) + 8 * j];
         }
-        const float* col = sc.col + c0 + 2 * (lane & 3);
-        const uint32_t base = lanes + b * kTile + uint32_t(c0);
-        uint32_t r[2][2][16];
-        float2 s[2][4];
-        auto fetch = [&](int q) {
-          tc::ld16x32(base + uint32_t(32 * q), r[q & 1][0]);
-          tc::ld16x32(base + (16u << 16) + uint32_t(32 * q), r[q & 1][1]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) s[q & 1][j] = *reinterpret_cast<const float2*>(col + 32 * q + 8 * j);
-        };
-        fetch(0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          if (c0 + 32 * q >= c1) break;
+          if (q >= chunks) break;
           tc::wait_ld();
-          if (q < 3 && c0 + 32 * (q + 1) < c1) fetch(q + 1);
+          // the next chunk, of the next block behind the last one, is on its way
+          // while this one is added
+          if (q + 1 < chunks) {
+            fetch(q + 1);
+          } else {
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) peer_arrive_relaxed(tempty0 + 8u * (i & 1u));
+            ++i;
+            if (k + kBK8 < x.k_end) {
+              ready();
+              if (ok) fetch(0);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -374,13 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
               acc[q][y][j] = fma_2(d, s[q & 1][j], acc[q][y][j]);
             }
         }
-        tc::fence_before();
         __syncwarp();
-        if (lane == 0) {
-          peer_arrive_relaxed(tempty0 + 8u * b);
-          mbar_arrive(&ctl->sempty[slot]);
-        }
-        ++i;
+        if (lane == 0) mbar_arrive(&ctl->sempty[slot]);
       }
       if (!ok) break;
       const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
