@@ -23,7 +23,7 @@ cudaError_t make_byte_stack_map(CUtensorMap* map, const void* base, int64_t cols
 cudaError_t launch_quant8(const glu_block8_quant_args& a, cudaStream_t s);
 cudaError_t launch_quant8_weight(const glu_block8_quant_weight_args& a, cudaStream_t s);
 cudaError_t launch_glu8(const glu_block8_glu_args& a, cudaStream_t s);
-cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s);
+cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, const DevInfo& d);
 size_t linear8_workspace(const glu_block8_linear_args& a);
 cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s, const DevInfo& d);

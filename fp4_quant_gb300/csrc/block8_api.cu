@@ -191,7 +191,7 @@ extern "C" int glu_block8_linear_dw(const glu_block8_linear_dw_args* a, void* st
 }
 extern "C" int glu_block8_glu(const glu_block8_glu_args* a, void* stream) { GQ_ENTRY(check_glu(a), gq::launch_glu8(*a, s)); }
 extern "C" int glu_block8_glu_bwd(const glu_block8_glu_bwd_args* a, void* stream) {
-  GQ_ENTRY(check_glu_bwd(a), gq::launch_glu8_bwd(*a, s));
+  GQ_ENTRY(check_glu_bwd(a), gq::launch_glu8_bwd(*a, s, d));
 }
 extern "C" int glu_block8_linear_workspace(const glu_block8_linear_args* a, size_t* bytes) {
   if (bytes == nullptr) return GLU_EINVAL;

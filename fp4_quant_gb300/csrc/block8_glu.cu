@@ -26,7 +26,7 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_const
   const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
   const int32_t k = kt * kBlock8 + c8 * 8, left = p.H - k;
   const int64_t row0 = (int64_t(tile) * kGluWarps + warp) * 2 * kFwdRows + (lane >> 4) * kFwdRows;
-  const int32_t rows = left > 0 ? int32_t(min(int64_t(p.M) - row0, int64_t(kFwdRows))) : 0;
+  const int32_t have = int32_t(min(int64_t(p.M) - row0, int64_t(kFwdRows))), rows = left > 0 ? have : 0;
   uint4 g[kFwdRows], u[kFwdRows];
 #pragma unroll
   for (int i = 0; i < kFwdRows; ++i) {
@@ -36,33 +36,40 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_const
       u[i] = raw8(p.up + (row0 + i) * p.ld_up + k, left);
     }
   }
+  // the blocks' maxima: of gate, up and h of row i as values 4 i, 4 i + 1, 4 i + 2,
+  // which lanes of that number fit
+  F8 h[kFwdRows];
+  float m[16];
 #pragma unroll
   for (int i = 0; i < kFwdRows; ++i) {
     const F8 gv = pairs(g[i]), uv = pairs(u[i]);
-    F8 h;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float a0, a1, d;
       act8<ACT>(gv.v[j].x, a0, d);
       act8<ACT>(gv.v[j].y, a1, d);
-      h.v[j] = mul_2(make_float2(a0, a1), uv.v[j]);
+      h[i].v[j] = mul_2(make_float2(a0, a1), uv.v[j]);
     }
-    const uint32_t a = amax_bits(g[i]), b = amax_bits(u[i]);
-    const uint32_t m = row_max2(__vmaxu2(__byte_perm(a, b, 0x5410), __byte_perm(a, b, 0x7632)));
-    const Fit8 fg = fit8(__uint_as_float(m << 16)), fu = fit8(__uint_as_float(m & 0xFFFF0000u));
-    Fit8 fh;
-    if (H8) fh = fit8(row_max(amax8(h)));
+    m[4 * i] = top_half(amax_bits(g[i]));
+    m[4 * i + 1] = top_half(amax_bits(u[i]));
+    m[4 * i + 2] = H8 ? amax8(h[i]) : 0.0f;
+    m[4 * i + 3] = 0.0f;
+  }
+  const Fit8 f = fit8(scatter_max(m, lane));
+  {
+    float* s = (c8 & 3) == 0 ? p.gs : (c8 & 3) == 1 ? p.us : H8 && (c8 & 3) == 2 ? p.hs : nullptr;
+    if (s && c8 / 4 < have) s[int64_t(kt) * p.M + row0 + c8 / 4] = f.s;
+  }
+#pragma unroll
+  for (int i = 0; i < kFwdRows; ++i) {
+    const float rg = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i, 16), ru = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i + 1, 16);
+    const float rh = H8 ? __shfl_sync(0xFFFFFFFFu, f.r, 4 * i + 2, 16) : 0.0f;
     if (i >= rows) continue;
-    const int64_t r = row0 + i, at = int64_t(kt) * p.M + r;
-    put_bytes8(p.gq + r * p.ld_gq + k, left, codes8<true>(gv, fg.r, fg.bad));
-    put_bytes8(p.uq + r * p.ld_uq + k, left, codes8<true>(uv, fu.r, fu.bad));
-    if (H8) put_bytes8(p.hq + r * p.ld_hq + k, left, codes8<false>(h, fh.r, fh.bad));
-    else put8(p.h + r * p.ld_h + k, left, packed(h));
-    if (c8 == 0) {
-      p.gs[at] = fg.s;
-      p.us[at] = fu.s;
-      if (H8) p.hs[at] = fh.s;
-    }
+    const int64_t r = row0 + i;
+    put_bytes8(p.gq + r * p.ld_gq + k, left, codes8<true>(pairs(g[i]), rg));
+    put_bytes8(p.uq + r * p.ld_uq + k, left, codes8<true>(pairs(u[i]), ru));
+    if (H8) put_bytes8(p.hq + r * p.ld_hq + k, left, codes8<false>(h[i], rh));
+    else put8(p.h + r * p.ld_h + k, left, packed(h[i]));
   }
 }
 
@@ -75,7 +82,7 @@ struct GluBwdP {
   uint8_t *dq, *dqc, *hqc;
   float *ds, *dsc, *hsc;
   int64_t ld_gq, ld_uq, ld_dh, ld_d, ld_h, ld_dq, ld_dqc, ld_hqc;
-  int32_t M, H, E, k_tiles, col_blocks;
+  int32_t M, H, E, k_tiles, col_blocks, tiles;
 };
 
 struct Grads {
@@ -96,6 +103,50 @@ __device__ __forceinline__ Grads glu_grads(const uint2& gq, float gs, const uint
     o.dg.v[j] = mul_2(mul_2(dy.v[j], w), d);
   }
   return o;
+}
+
+// A row's chunks of eight bf16, one per lane of 16 (`left` elements from the lane's
+// first on), to where the row begins `off` elements (1 .. 7) behind 16 bytes: a
+// lane stores the 16 bytes in which its chunk begins, with the last `off` elements
+// of the lane before it.  What fills no 16 bytes here goes element by element.
+// `row`: the lane's first element.  All 32 lanes take part.
+__device__ __forceinline__ void put_shifted(uint16_t* row, int off, int left, bool store, uint4 v, int c8) {
+  uint32_t before[4], own[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) before[j] = __shfl_up_sync(0xFFFFFFFFu, own[j], 1, 16);
+  if (!store) return;
+  const int n = min(left, 8);
+  // elements -off .. 7 - off of the lane's chunk: words of the pair (before, own)
+  auto element = [&](int e) {  // -8 .. 7
+    const uint32_t w = e < 0 ? before[(e + 8) >> 1] : own[e >> 1];
+    return uint16_t(w >> (16 * (e & 1)));
+  };
+  if (c8 > 0 && n >= 8 - off) {
+    uint32_t w[4];
+    uint32_t all[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) all[j] = before[j], all[4 + j] = own[j];
+    // word j of the result: elements 2 j - off and the next, of which `all` holds element e at (e + 8) / 2
+    const int words = (8 - off) >> 1, odd = off & 1;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t lo = 0, hi = 0;
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (words == q) lo = all[j + q], hi = all[j + q + 1];
+      w[j] = odd ? __funnelshift_r(lo, hi, 16) : lo;
+    }
+    stg_once(row - off, make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+#pragma unroll
+    for (int e = -7; e < 8; ++e)
+      if (e >= (c8 > 0 ? -off : 0) && e < min(n, 8 - off)) row[e] = element(e);
+  }
+  if (c8 == 15 || left <= 8) {  // no lane behind this one
+#pragma unroll
+    for (int e = 1; e < 8; ++e)
+      if (e >= 8 - off && e < n) row[e] = element(e);
+  }
 }
 
 constexpr int kBwdRows = 4;
@@ -121,139 +172,180 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_bwd_kernel(const __grid_c
       us[i] = __ldg(p.us + at);
     }
   }
+  const int off = p.H % 8;
 #pragma unroll
   for (int i = 0; i < kBwdRows; ++i) {
-    if (i >= rows) break;
-    const Grads o = glu_grads<ACT>(g[i], gs[i], u[i], us[i], dh[i]);
     const int64_t r = row0 + i;
-    uint16_t* d = p.d + r * p.ld_d + k;
-    put8(d, left, packed(o.dg));
-    // dUp begins at column H, on 16 bytes only where H is a multiple of eight
-    if (p.H % 8 == 0) {
-      put8(d + p.H, left, packed(o.du));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < left) d[p.H + j] = bits_of_bf16(j & 1 ? o.du.v[j / 2].y : o.du.v[j / 2].x);
+    const bool store = i < rows;
+    uint4 du = make_uint4(0, 0, 0, 0);
+    if (store) {
+      const Grads o = glu_grads<ACT>(g[i], gs[i], u[i], us[i], dh[i]);
+      put8(p.d + r * p.ld_d + k, left, packed(o.dg));
+      du = packed(o.du);
+      if (off == 0) put8(p.d + r * p.ld_d + p.H + k, left, du);
+      if (p.h) put8(p.h + r * p.ld_h + k, left, packed(o.h));
     }
-    if (p.h) put8(p.h + r * p.ld_h + k, left, packed(o.h));
+    if (off != 0) put_shifted(p.d + r * p.ld_d + p.H + k, off, left, store, du, c8);
   }
 }
 
-// Backward, quantised: a block of 16 warps takes 128 rows by 128 columns, a lane
-// four rows of eight columns, and holds the three results of its 32 elements in
-// registers while the maxima of their columns are found.
+// Backward, quantised: blocks of 16 warps, one per SM, walk tiles of 128 rows by
+// 128 columns.  A lane has four rows of eight columns, and holds the three results
+// of its 32 elements in registers while the maxima of rows and columns are found;
+// the next tile's operands are on their way into shared memory meanwhile.
 constexpr int kTileWarps = 16, kTileRows = 4;
 
-struct TileFits {
+struct TileIn {
+  uint16_t dh[kBlock8][kBlock8];
+  uint8_t g[kBlock8][kBlock8], u[kBlock8][kBlock8];
+  float gs[kBlock8], us[kBlock8];
+};
+struct TileShared {
+  TileIn in[2];
   float part[3][kTileWarps][kBlock8];
   float r[3][kBlock8];
-  uint32_t bad[3][kBlock8 / 4];
+  int32_t offsets[kMaxExperts + 1];
 };
+
+// 16 bytes (4 for n = 4) to shared memory, zeros where `there` is false.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(there ? 16u : 0u)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(there ? 4u : 0u)
+               : "memory");
+}
 
 template <int ACT>
 __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const __grid_constant__ GluBwdP p) {
-  __shared__ TileFits fits;
+  extern __shared__ __align__(16) uint8_t raw[];
+  TileShared& sh = *reinterpret_cast<TileShared*>(raw);
+  constexpr int kThreads = kTileWarps * 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
-  const RowTile t = row_tile(p.offsets, p.E, p.M, tile);
-  const int32_t k = kt * kBlock8 + c8 * 8;
-  const int32_t row0 = warp * 8 + (lane >> 4) * kTileRows, rows = t.r1 - t.r0 - row0;
-  uint2 g[kTileRows], u[kTileRows];
-  uint4 dh[kTileRows];
-  float gs[kTileRows], us[kTileRows];
-#pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    g[i] = u[i] = make_uint2(0, 0);
-    dh[i] = make_uint4(0, 0, 0, 0);
-    gs[i] = us[i] = 0.0f;
-    if (i < rows) {
-      const int64_t r = t.r0 + row0 + i, at = int64_t(kt) * p.M + r;
-      g[i] = bytes8(p.gq + r * p.ld_gq + k, 8);
-      u[i] = bytes8(p.uq + r * p.ld_uq + k, 8);
-      dh[i] = ldg_once(p.dh + r * p.ld_dh + k);
-      gs[i] = __ldg(p.gs + at);
-      us[i] = __ldg(p.us + at);
-    }
+  const int row0 = warp * 8 + (lane >> 4) * kTileRows;
+  after_previous();
+  if (p.offsets) {
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) sh.offsets[e] = __ldg(p.offsets + e);
+    __syncthreads();
   }
-  F8 v[3][kTileRows];
+  auto rows_of = [&](int32_t w) { return row_tile(p.offsets ? sh.offsets : nullptr, p.E, p.M, w / p.k_tiles); };
+  auto load = [&](int32_t w, const RowTile& t, TileIn& in) {
+    const int32_t kt = w % p.k_tiles, k = kt * kBlock8, rows = t.r1 - t.r0;
+    // rows of no tile are not read (their first row's address stands in)
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i) {
-    const Grads o = glu_grads<ACT>(g[i], gs[i], u[i], us[i], dh[i]);
-    v[0][i] = o.dg;
-    v[1][i] = o.du;
-    v[2][i] = o.h;
-  }
-  // rows of d: lane 2 i + x of a half fits row i of dGate (x = 0) or dUp
-  float mine = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kTileRows; ++i)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float m = row_max(amax8(v[x][i]));
-      if (c8 == 2 * i + x) mine = m;
+    for (int j = 0; j < 4; ++j) {
+      const int q = threadIdx.x + j * kThreads, r = q >> 4, c = (q & 15) * 8;
+      copy16(&in.dh[r][c], p.dh + int64_t(r < rows ? t.r0 + r : 0) * p.ld_dh + k + c, r < rows);
     }
-  const Fit8 f = fit8(mine);
-  if (c8 < 2 * kTileRows && c8 / 2 < rows)
-    p.ds[int64_t(kt + (c8 & 1) * p.k_tiles) * p.M + t.r0 + row0 + c8 / 2] = f.s;
 #pragma unroll
-  for (int i = 0; i < kTileRows; ++i)
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const float r = __shfl_sync(0xFFFFFFFFu, f.r, 2 * i + x, 16);
-      const uint32_t bad = __shfl_sync(0xFFFFFFFFu, f.bad, 2 * i + x, 16);
-      if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8<false>(v[x][i], r, bad));
+    for (int j = 0; j < 2; ++j) {
+      const int q = threadIdx.x + j * kThreads, r = q >> 3, c = (q & 7) * 16;
+      const int64_t m = r < rows ? t.r0 + r : 0;
+      copy16(&in.g[r][c], p.gq + m * p.ld_gq + k + c, r < rows);
+      copy16(&in.u[r][c], p.uq + m * p.ld_uq + k + c, r < rows);
     }
-  if (tile >= p.col_blocks) return;
-  if (!t.cols) {  // rows of no expert: their blocks are zeros
-#pragma unroll
-    for (int x = 0; x < 3; ++x)
-#pragma unroll
-      for (int i = 0; i < kTileRows; ++i) v[x][i] = zeros();
-  }
-#pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    float m[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      m[j] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kTileRows; ++i) m[j] = max_nan(m[j], fabsf(j & 1 ? v[x][i].v[j / 2].y : v[x][i].v[j / 2].x));
-      m[j] = max_nan(m[j], __shfl_xor_sync(0xFFFFFFFFu, m[j], 16));
+    if (threadIdx.x < 2 * kBlock8) {
+      const int r = threadIdx.x % kBlock8;
+      const float* s = (threadIdx.x < kBlock8 ? p.gs : p.us) + int64_t(kt) * p.M + (r < rows ? t.r0 + r : 0);
+      copy4(threadIdx.x < kBlock8 ? &in.gs[r] : &in.us[r], s, r < rows);
     }
-    if (lane < 16) {
-      float4* o = reinterpret_cast<float4*>(&fits.part[x][warp][c8 * 8]);
-      o[0] = make_float4(m[0], m[1], m[2], m[3]);
-      o[1] = make_float4(m[4], m[5], m[6], m[7]);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  RowTile t = {0, 0, false};
+  if (int32_t(blockIdx.x) < p.tiles) {
+    t = rows_of(blockIdx.x);
+    load(blockIdx.x, t, sh.in[0]);
+  }
+  int buf = 0;
+  for (int32_t w = blockIdx.x; w < p.tiles; w += gridDim.x, buf ^= 1) {
+    RowTile next = {0, 0, false};
+    if (w + int32_t(gridDim.x) < p.tiles) {
+      next = rows_of(w + gridDim.x);
+      load(w + gridDim.x, next, sh.in[buf ^ 1]);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-  }
-  __syncthreads();
-  if (threadIdx.x < 3 * kBlock8) {
-    const int x = threadIdx.x / kBlock8, c = threadIdx.x % kBlock8;
-    float a = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kTileWarps; ++i) a = max_nan(a, fits.part[x][i][c]);
-    const Fit8 fc = fit8(a);
-    fits.r[x][c] = fc.r;
-    reinterpret_cast<uint8_t*>(fits.bad[x])[c] = uint8_t(fc.bad);
-    if (x < 2) p.dsc[int64_t(tile) * 2 * p.H + x * p.H + kt * kBlock8 + c] = fc.s;
-    else if (p.hsc) p.hsc[int64_t(tile) * p.H + kt * kBlock8 + c] = fc.s;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int x = 0; x < 3; ++x) {
-    if (x == 2 && p.hqc == nullptr) break;
-    float2 r[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const float2*>(&fits.r[x][c8 * 8 + 2 * j]);
-    const uint2 bad = *reinterpret_cast<const uint2*>(&fits.bad[x][c8 * 2]);
+    __syncthreads();
+    const TileIn& in = sh.in[buf];
+    const int32_t tile = w / p.k_tiles, kt = w - tile * p.k_tiles, k = kt * kBlock8 + c8 * 8, rows = t.r1 - t.r0 - row0;
+    F8 v[3][kTileRows];
+    float m[2 * kTileRows];
 #pragma unroll
     for (int i = 0; i < kTileRows; ++i) {
-      uint2 o = codes8<false>(v[x][i], r);
-      o.x |= bad.x, o.y |= bad.y;
-      const int64_t row = int64_t(tile) * kBlock8 + row0 + i;
-      put_bytes8(x < 2 ? p.dqc + row * p.ld_dqc + x * p.H + k : p.hqc + row * p.ld_hqc + k, 8, o);
+      const int r = row0 + i;
+      const Grads o = glu_grads<ACT>(*reinterpret_cast<const uint2*>(&in.g[r][c8 * 8]), in.gs[r], *reinterpret_cast<const uint2*>(&in.u[r][c8 * 8]),
+                                     in.us[r], *reinterpret_cast<const uint4*>(&in.dh[r][c8 * 8]));
+      v[0][i] = o.dg;
+      v[1][i] = o.du;
+      v[2][i] = o.h;
+      m[2 * i] = amax8(o.dg);
+      m[2 * i + 1] = amax8(o.du);
     }
+    // rows of d: lane 2 i + x of eight fits row i of dGate (x = 0) or dUp
+    const Fit8 f = fit8(scatter_max(m, lane));
+    if (c8 < 2 * kTileRows && c8 / 2 < rows) p.ds[int64_t(kt + (c8 & 1) * p.k_tiles) * p.M + t.r0 + row0 + c8 / 2] = f.s;
+#pragma unroll
+    for (int i = 0; i < kTileRows; ++i)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float r = __shfl_sync(0xFFFFFFFFu, f.r, 2 * i + x, 16);
+        if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8<false>(v[x][i], r));
+      }
+    if (tile < p.col_blocks) {  // the same for the whole block
+      if (!t.cols) {  // rows of no expert: their blocks are zeros
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+#pragma unroll
+          for (int i = 0; i < kTileRows; ++i) v[x][i] = zeros();
+      }
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        float c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          auto at = [&](int i) { return fabsf(j & 1 ? v[x][i].v[j / 2].y : v[x][i].v[j / 2].x); };
+          c[j] = max_nan(max_nan(at(0), at(1)), at(2), at(3));
+        }
+        // the half-warps' maxima: a lane of each keeps four columns
+        const bool up = lane & 16;
+        float o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? c[j] : c[4 + j], 16);
+          o[j] = max_nan(up ? c[4 + j] : c[j], got);
+        }
+        *reinterpret_cast<float4*>(&sh.part[x][warp][c8 * 8 + (up ? 4 : 0)]) = make_float4(o[0], o[1], o[2], o[3]);
+      }
+      __syncthreads();
+      if (threadIdx.x < 3 * kBlock8) {
+        const int x = threadIdx.x / kBlock8, c = threadIdx.x % kBlock8;
+        float a = sh.part[x][0][c];
+#pragma unroll
+        for (int i = 1; i < kTileWarps; ++i) a = max_nan(a, sh.part[x][i][c]);
+        const Fit8 fc = fit8(a);
+        sh.r[x][c] = fc.r;
+        if (x < 2) p.dsc[int64_t(tile) * 2 * p.H + x * p.H + kt * kBlock8 + c] = fc.s;
+        else if (p.hsc) p.hsc[int64_t(tile) * p.H + kt * kBlock8 + c] = fc.s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        if (x == 2 && p.hqc == nullptr) break;
+        float2 r[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const float2*>(&sh.r[x][c8 * 8 + 2 * j]);
+        const int64_t row = int64_t(tile) * kBlock8 + row0;
+        uint8_t* out = x < 2 ? p.dqc + row * p.ld_dqc + x * p.H + k : p.hqc + row * p.ld_hqc + k;
+        const int64_t ld = x < 2 ? p.ld_dqc : p.ld_hqc;
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) put_bytes8(out + i * ld, 8, codes8<false>(v[x][i], r));
+      }
+    } else {
+      __syncthreads();  // this tile's operands are read before the next but one's arrive
+    }
+    t = next;
   }
 }
 
@@ -265,13 +357,17 @@ cudaError_t launch_fwd(const GluP& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 template <int ACT>
-cudaError_t launch_bwd(const GluBwdP& p, cudaStream_t s) {
+cudaError_t launch_bwd(GluBwdP& p, cudaStream_t s, const DevInfo& d) {
   if (p.d) {
     const int64_t per = kGluWarps * 2 * kBwdRows, tiles = (p.M + per - 1) / per * p.k_tiles;
     glu8_bwd_kernel<ACT><<<unsigned(tiles), kGluWarps * 32, 0, s>>>(p);
   } else {
-    const int64_t tiles = int64_t(p.col_blocks + (p.E > 0 ? 1 : 0)) * p.k_tiles;
-    glu8_bwd_tile_kernel<ACT><<<unsigned(tiles), kTileWarps * 32, 0, s>>>(p);
+    p.tiles = (p.col_blocks + (p.E > 0 ? 1 : 0)) * p.k_tiles;
+    auto kern = glu8_bwd_tile_kernel<ACT>;
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), int(sizeof(TileShared)));
+    if (e != cudaSuccess) return e;
+    return launch_kernel(kern, unsigned(p.tiles < d.sms ? p.tiles : d.sms), kTileWarps * 32, sizeof(TileShared), s, p, true);
   }
   return cudaGetLastError();
 }
@@ -307,7 +403,7 @@ cudaError_t launch_glu8(const glu_block8_glu_args& a, cudaStream_t s) {
   }
 }
 
-cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s) {
+cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s, const DevInfo& d) {
   GluBwdP p;
   p.gq = static_cast<const uint8_t*>(a.gq);
   p.uq = static_cast<const uint8_t*>(a.uq);
@@ -337,11 +433,11 @@ cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s) {
   p.k_tiles = int32_t(blocks8(a.H));
   p.col_blocks = int32_t(col_blocks8(a.M, a.E));
   switch (a.act) {
-    case GLU_ACT_SILU: return launch_bwd<GLU_ACT_SILU>(p, s);
-    case GLU_ACT_GELU_TANH: return launch_bwd<GLU_ACT_GELU_TANH>(p, s);
-    case GLU_ACT_RELU: return launch_bwd<GLU_ACT_RELU>(p, s);
-    case GLU_ACT_GELU_ERF: return launch_bwd<GLU_ACT_GELU_ERF>(p, s);
-    default: return launch_bwd<GLU_ACT_IDENTITY>(p, s);
+    case GLU_ACT_SILU: return launch_bwd<GLU_ACT_SILU>(p, s, d);
+    case GLU_ACT_GELU_TANH: return launch_bwd<GLU_ACT_GELU_TANH>(p, s, d);
+    case GLU_ACT_RELU: return launch_bwd<GLU_ACT_RELU>(p, s, d);
+    case GLU_ACT_GELU_ERF: return launch_bwd<GLU_ACT_GELU_ERF>(p, s, d);
+    default: return launch_bwd<GLU_ACT_IDENTITY>(p, s, d);
   }
 }
 

@@ -25,13 +25,12 @@ struct QuantP {
 struct ColFits {
   float part[kQuantWarps][kBlock8];
   float r[kBlock8];
-  uint32_t bad[kBlock8 / 4];  // a byte per column
 };
 
 // A warp has rows 16 w .. 16 w + 15 of the tile: its lower half-warp the first
 // eight, the upper one the others, a lane eight columns of each.
 template <bool KEPT, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kQuantWarps * 32) quant8_kernel(const __grid_constant__ QuantP p) {
+__global__ void __launch_bounds__(kQuantWarps * 32, 4) quant8_kernel(const __grid_constant__ QuantP p) {
   __shared__ ColFits fits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
@@ -79,8 +78,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quant8_kernel(const __grid_c
 #pragma unroll
     for (int i = 0; i < kRowsPerLane; ++i) {
       const float r = __shfl_sync(0xFFFFFFFFu, f.r, i, 16);
-      const uint32_t bad = __shfl_sync(0xFFFFFFFFu, f.bad, i, 16);
-      if (i < rows && left > 0) put_bytes8(p.q + int64_t(t.r0 + row0 + i) * p.ld_q + k, left, codes8<true>(pairs(w[i]), r, bad));
+      if (i < rows && left > 0) put_bytes8(p.q + int64_t(t.r0 + row0 + i) * p.ld_q + k, left, codes8<true>(pairs(w[i]), r));
     }
   }
   if (!cols) return;
@@ -131,19 +129,15 @@ __global__ void __launch_bounds__(kQuantWarps * 32) quant8_kernel(const __grid_c
     for (int i = 0; i < kQuantWarps; ++i) a = max_nan(a, fits.part[i][threadIdx.x]);
     const Fit8 f = fit8(a);
     fits.r[threadIdx.x] = f.r;
-    reinterpret_cast<uint8_t*>(fits.bad)[threadIdx.x] = uint8_t(f.bad);
     if (kt * kBlock8 + int32_t(threadIdx.x) < p.K) p.sc[int64_t(tile) * p.K + kt * kBlock8 + threadIdx.x] = f.s;
   }
   __syncthreads();
   float2 r[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const float2*>(&fits.r[c8 * 8 + 2 * j]);
-  const uint2 bad = *reinterpret_cast<const uint2*>(&fits.bad[c8 * 2]);
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
-    uint2 o = codes8<!KEPT>(value(i), r);
-    o.x |= bad.x, o.y |= bad.y;
-    if (left > 0) put_bytes8(p.qc + (int64_t(tile) * kBlock8 + row0 + i) * p.ld_qc + k, left, o);
+    if (left > 0) put_bytes8(p.qc + (int64_t(tile) * kBlock8 + row0 + i) * p.ld_qc + k, left, codes8<!KEPT>(value(i), r));
   }
 }
 
@@ -155,7 +149,7 @@ struct WeightP {
   int32_t N, K, n_tiles, k_tiles;
 };
 
-__global__ void __launch_bounds__(kQuantWarps * 32) weight8_kernel(const __grid_constant__ WeightP p) {
+__global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __grid_constant__ WeightP p) {
   __shared__ float part[kQuantWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t rt = blockIdx.x / p.k_tiles, kt = blockIdx.x - rt * p.k_tiles, e = rt / p.n_tiles, nt = rt - e * p.n_tiles;
@@ -180,7 +174,7 @@ __global__ void __launch_bounds__(kQuantWarps * 32) weight8_kernel(const __grid_
   uint8_t* dst = p.q + e * p.stride_q + int64_t(row0) * p.ld_q + k;
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i)
-    if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8<true>(pairs(w[i]), f.r, f.bad));
+    if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8<true>(pairs(w[i]), f.r));
 }
 
 }  // namespace

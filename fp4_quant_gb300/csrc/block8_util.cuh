@@ -9,51 +9,47 @@ namespace gq {
 constexpr float kTop8 = 448.0f;               // the largest E4M3 value
 constexpr float kLeast8 = 0x1p-100f;          // a block's maximum counts as this at least
 
-// What a block's codes are made with: v * r rounded, unless the block holds a
-// NaN or an infinity (bad: all ones in the codes' seven value bits, NaN).
+// What a block's codes are made with (values times r, rounded) and its scale;
+// both NaN where it holds a NaN or an infinity, which makes its codes NaN too.
 struct Fit8 {
   float r, s;
-  uint32_t bad;
 };
 __device__ __forceinline__ Fit8 fit8(float amax) {
-  Fit8 f;
-  const bool ok = amax <= 3.402823466e38f;
-  const float a = fmaxf(amax, kLeast8);
-  f.r = ok ? __fdiv_rn(kTop8, a) : 0.0f;
-  f.s = ok ? __fdiv_rn(a, kTop8) : __uint_as_float(0x7FC00000u);
-  f.bad = ok ? 0u : 0x7F7F7F7Fu;
-  return f;
+  const float a = amax <= 3.402823466e38f ? fmaxf(amax, kLeast8) : __uint_as_float(0x7FC00000u);
+  return {__fdiv_rn(kTop8, a), __fdiv_rn(a, kTop8)};
 }
 
-// For bf16 values the exact quotient 448 v / a is either the midpoint of two
-// codes or 2^-13 (relative) away from it at least: with 8-bit integers m, a' and an
-// odd one of 5 bits t, |7 m 2^x - t a'| is 0 or 1 at least, and t a' < 2^13.
-// RN(448 / a) * v is within 2^-22 of it, so rounded to 16 significant bits it is
-// on the quotient's side of every midpoint, and on the midpoint where that is.
-__device__ __forceinline__ float snap8(float t) { return __uint_as_float((__float_as_uint(t) + 0x80u) & 0xFFFFFF00u); }
-
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
+__device__ __forceinline__ uint32_t e4m3x2_of(float2 v) {
   uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(v.y), "f"(v.x));
   return r;
 }
-// Codes of eight values, scaled by r (one for all, or pairs).  SNAP: they are bf16 values.
+
+// Codes of eight values, scaled by r (a pair for each two of them).  SNAP: the
+// values are bf16.  Then the exact quotient 448 v / a is either the midpoint of two
+// codes or 2^-13 (relative) away from it at least: with 8-bit integers m, a' and
+// an odd one of 5 bits t, |7 m 2^x - t a'| is 0 or 1 at least, and t a' < 2^13.
+// v RN(448 / a) is within 2^-22 of it, so rounded to 16 significant bits it is on
+// the quotient's side of every midpoint, and on the midpoint where that is.  The
+// rounding is Veltkamp's: t 257 - (t 257 - t), two values at a time.
 template <bool SNAP>
 __device__ __forceinline__ uint2 codes8(const F8& v, const float2 (&r)[4]) {
   uint32_t h[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 t = mul_2(v.v[i], r[i]);
-    h[i] = SNAP ? e4m3x2_of(snap8(t.x), snap8(t.y)) : e4m3x2_of(t.x, t.y);
+    float2 t = mul_2(v.v[i], r[i]);
+    if (SNAP) {
+      const float2 p = mul_2(t, both(257.0f)), d = fma_2(t, both(-1.0f), p);
+      t = fma_2(d, both(-1.0f), p);
+    }
+    h[i] = e4m3x2_of(t);
   }
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
 template <bool SNAP>
-__device__ __forceinline__ uint2 codes8(const F8& v, float r, uint32_t bad) {
+__device__ __forceinline__ uint2 codes8(const F8& v, float r) {
   const float2 q[4] = {both(r), both(r), both(r), both(r)};
-  uint2 c = codes8<SNAP>(v, q);
-  c.x |= bad, c.y |= bad;
-  return c;
+  return codes8<SNAP>(v, q);
 }
 
 // What eight codes stand for without their scale, exact in fp32.
@@ -99,11 +95,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // |max| of eight values
 __device__ __forceinline__ float amax8(const F8& f) {
-  float m = 0.0f;
+  float m = max_nan(fabsf(f.v[0].x), fabsf(f.v[0].y));
 #pragma unroll
-  for (int i = 0; i < 4; ++i) m = max_nan(m, max_nan(fabsf(f.v[i].x), fabsf(f.v[i].y)));
+  for (int i = 1; i < 4; ++i) m = max_nan(m, fabsf(f.v[i].x), fabsf(f.v[i].y));
   return m;
 }
 // Largest bits of |v| of bf16 pairs (infinities and NaN above all others).
@@ -120,10 +121,23 @@ __device__ __forceinline__ uint32_t row_max2(uint32_t v) {
   for (int o = 8; o > 0; o >>= 1) v = __vmaxu2(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
   return v;
 }
-__device__ __forceinline__ float row_max(float v) {
+// N values per lane (a power of two up to 16): lane l of the 16 gets the maximum
+// over them of value l % N.  Halves, quarters, ... swap what the others keep, so
+// that it takes N - 1 exchanges and one for each halving that is left.
+template <int N>
+__device__ __forceinline__ float scatter_max(float (&v)[N], int lane) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  return v;
+  for (int o = N / 2; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, up ? v[i] : v[i + o], o);
+      v[i] = max_nan(up ? v[i + o] : v[i], got);
+    }
+  }
+#pragma unroll
+  for (int o = N; o < 16; o <<= 1) v[0] = max_nan(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], o));
+  return v[0];
 }
 
 // The rows of one 128-row tile: block `tile` of the column form, and rows r0 ..
@@ -145,7 +159,7 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int32_t E, i
     return t;
   }
   const int lane = threadIdx.x & 31;
-  auto first = [&](int32_t e) { return min(max(__ldg(offsets + e), 0), M) / kBlock8 + e; };
+  auto first = [&](int32_t e) { return min(max(offsets[e], 0), M) / kBlock8 + e; };
   // the last expert of 0 .. E (E: the rows behind the last) that begins at or before the tile
   const int32_t step = E / 32 + 1;
   int32_t e = lane * step;
@@ -157,7 +171,7 @@ __device__ __forceinline__ RowTile row_tile(const int32_t* offsets, int32_t E, i
     hit = __ballot_sync(0xFFFFFFFFu, o + lane < step && e + o <= E && first(min(e + o, E)) <= tile);
     if (hit) at = base + o + 31 - __clz(hit);
   }
-  const int32_t begin = min(max(__ldg(offsets + at), 0), M), end = at < E ? min(max(__ldg(offsets + at + 1), begin), M) : M;
+  const int32_t begin = min(max(offsets[at], 0), M), end = at < E ? min(max(offsets[at + 1], begin), M) : M;
   const int64_t r0 = begin + int64_t(tile - (begin / kBlock8 + at)) * kBlock8;
   t.r0 = int32_t(min(max(r0, int64_t(begin)), int64_t(end)));
   t.r1 = min(end, t.r0 + kBlock8);

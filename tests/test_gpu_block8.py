@@ -471,6 +471,18 @@ def test_glu_backward(M, H, act):
     assert n["h"] is None and torch.equal(n["d"], o["d"])
 
 
+@pytest.mark.parametrize("H", [*range(121, 138), 255, 257, 261])
+def test_glu_backward_halves_at_every_offset(H):
+    """dUp begins H elements behind a row's start: all remainders of eight, and what
+    stands beside the matrices stays."""
+    gate8, up8, dh = _kept_pair(19, H, H)
+    wide = torch.full((19, -(-2 * H // 8) * 8 + 16), -7.0, dtype=BF, device=DEV)
+    o = G.glu8_bwd(gate8, up8, dh, out={"d": wide[:, 8:8 + 2 * H]})
+    d, ed, _, _ = _grads64(G.ACT_SILU, gate8, up8, dh)
+    assert bool(((o["d"].to(F64) - d).abs() <= HALF * (d.abs() + ed) + ed + 2.0 ** -133).all())
+    assert bool((wide[:, :8] == -7).all()) and bool((wide[:, 8 + 2 * H:] == -7).all())
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("M,H,E,spare,empty", [(1, 128, 0, 0, ()), (200, 256, 0, 0, ()), (300, 128, 5, 40, (2,)), (1000, 384, 3, 0, ()), (20, 128, 64, 3, (0, 9))])
 def test_glu_backward_quantised(M, H, E, spare, empty, act):
