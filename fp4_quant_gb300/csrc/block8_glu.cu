@@ -45,10 +45,9 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_const
     const F8 gv = pairs(g[i]), uv = pairs(u[i]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float a0, a1, d;
-      act8<ACT>(gv.v[j].x, a0, d);
-      act8<ACT>(gv.v[j].y, a1, d);
-      h[i].v[j] = mul_2(make_float2(a0, a1), uv.v[j]);
+      float2 a, d;
+      act8<ACT>(gv.v[j], a, d);
+      h[i].v[j] = mul_2(a, uv.v[j]);
     }
     m[4 * i] = top_half(amax_bits(g[i]));
     m[4 * i + 1] = top_half(amax_bits(u[i]));
@@ -96,8 +95,7 @@ __device__ __forceinline__ Grads glu_grads(const uint2& gq, float gs, const uint
   for (int j = 0; j < 4; ++j) {
     const float2 z = mul_2(g.v[j], both(gs)), w = mul_2(u.v[j], both(us));
     float2 a, d;
-    act8<ACT>(z.x, a.x, d.x);
-    act8<ACT>(z.y, a.y, d.y);
+    act8<ACT>(z, a, d);
     o.h.v[j] = mul_2(a, w);
     o.du.v[j] = mul_2(dy.v[j], a);
     o.dg.v[j] = mul_2(mul_2(dy.v[j], w), d);

@@ -9,14 +9,27 @@ namespace gq {
 constexpr float kTop8 = 448.0f;               // the largest E4M3 value
 constexpr float kLeast8 = 0x1p-100f;          // a block's maximum counts as this at least
 
+// 1 / x to 2^-23; x and the result are not below 2^-126.
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // What a block's codes are made with (values times r, rounded) and its scale;
-// both NaN where it holds a NaN or an infinity, which makes its codes NaN too.
+// both NaN where it holds a NaN or an infinity, which makes its codes NaN too.  s
+// is a / 448 rounded once: the product with the rounded 1 / 448, corrected by its
+// remainder (Markstein, 1990).  r is 1 / s, which stays in range for all a.
 struct Fit8 {
   float r, s;
 };
 __device__ __forceinline__ Fit8 fit8(float amax) {
-  const float a = amax <= 3.402823466e38f ? fmaxf(amax, kLeast8) : __uint_as_float(0x7FC00000u);
-  return {__fdiv_rn(kTop8, a), __fdiv_rn(a, kTop8)};
+  constexpr float kInv = 1.0f / kTop8;
+  const float a = amax <= 3.402823466e38f ? fmaxf(amax, kLeast8) : __uint_as_float(0x7FC00000u), q = a * kInv;
+  Fit8 f;
+  f.s = fmaf(fmaf(-q, kTop8, a), kInv, q);
+  f.r = rcp_fast(f.s);
+  return f;
 }
 
 __device__ __forceinline__ uint32_t e4m3x2_of(float2 v) {
@@ -29,7 +42,7 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float2 v) {
 // values are bf16.  Then the exact quotient 448 v / a is either the midpoint of two
 // codes or 2^-13 (relative) away from it at least: with 8-bit integers m, a' and
 // an odd one of 5 bits t, |7 m 2^x - t a'| is 0 or 1 at least, and t a' < 2^13.
-// v RN(448 / a) is within 2^-22 of it, so rounded to 16 significant bits it is on
+// v r is within 2^-22 + 2^-24 of it (s, r and the product are rounded), so rounded to 16 significant bits it is on
 // the quotient's side of every midpoint, and on the midpoint where that is.  The
 // rounding is Veltkamp's: t 257 - (t 257 - t), two values at a time.
 template <bool SNAP>
