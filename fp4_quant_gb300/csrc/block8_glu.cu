@@ -18,10 +18,10 @@ struct GluP {
 };
 
 // Forward: a warp takes 2 x kFwdRows rows of a 128-column strip.
-constexpr int kFwdRows = 4;
+constexpr int kFwdRows = 2;
 
 template <int ACT, bool H8>
-__global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_constant__ GluP p) {
+__global__ void __launch_bounds__(kGluWarps * 32, 4) glu8_kernel(const __grid_constant__ GluP p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
   const int32_t k = kt * kBlock8 + c8 * 8, left = p.H - k;
@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_const
   // the blocks' maxima: of gate, up and h of row i as values 4 i, 4 i + 1, 4 i + 2,
   // which lanes of that number fit
   F8 h[kFwdRows];
-  float m[16];
+  float m[4 * kFwdRows];
 #pragma unroll
   for (int i = 0; i < kFwdRows; ++i) {
     const F8 gv = pairs(g[i]), uv = pairs(u[i]);
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(kGluWarps * 32) glu8_kernel(const __grid_const
   const Fit8 f = fit8(scatter_max(m, lane));
   {
     float* s = (c8 & 3) == 0 ? p.gs : (c8 & 3) == 1 ? p.us : H8 && (c8 & 3) == 2 ? p.hs : nullptr;
-    if (s && c8 / 4 < have) s[int64_t(kt) * p.M + row0 + c8 / 4] = f.s;
+    if (s && c8 < 4 * kFwdRows && c8 / 4 < have) s[int64_t(kt) * p.M + row0 + c8 / 4] = f.s;
   }
 #pragma unroll
   for (int i = 0; i < kFwdRows; ++i) {
@@ -103,54 +103,56 @@ __device__ __forceinline__ Grads glu_grads(const uint2& gq, float gs, const uint
   return o;
 }
 
+template <int FIRST>
+__device__ __forceinline__ void shifted(const uint32_t (&all)[8], bool odd, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = odd ? __funnelshift_r(all[FIRST + j], all[FIRST + j + 1], 16) : all[FIRST + j];
+}
+
 // A row's chunks of eight bf16, one per lane of 16 (`left` elements from the lane's
 // first on), to where the row begins `off` elements (1 .. 7) behind 16 bytes: a
 // lane stores the 16 bytes in which its chunk begins, with the last `off` elements
 // of the lane before it.  What fills no 16 bytes here goes element by element.
 // `row`: the lane's first element.  All 32 lanes take part.
 __device__ __forceinline__ void put_shifted(uint16_t* row, int off, int left, bool store, uint4 v, int c8) {
-  uint32_t before[4], own[4] = {v.x, v.y, v.z, v.w};
+  uint32_t all[8] = {0, 0, 0, 0, v.x, v.y, v.z, v.w};  // the lane before's, its own
 #pragma unroll
-  for (int j = 0; j < 4; ++j) before[j] = __shfl_up_sync(0xFFFFFFFFu, own[j], 1, 16);
+  for (int j = 0; j < 4; ++j) all[j] = __shfl_up_sync(0xFFFFFFFFu, all[4 + j], 1, 16);
   if (!store) return;
   const int n = min(left, 8);
-  // elements -off .. 7 - off of the lane's chunk: words of the pair (before, own)
-  auto element = [&](int e) {  // -8 .. 7
-    const uint32_t w = e < 0 ? before[(e + 8) >> 1] : own[e >> 1];
-    return uint16_t(w >> (16 * (e & 1)));
-  };
-  if (c8 > 0 && n >= 8 - off) {
-    uint32_t w[4];
-    uint32_t all[8];
+  const bool whole = c8 > 0 && n >= 8 - off;
+  // word j of the 16 bytes has elements 2 j - off and the next of its own, and `all`
+  // has element e in the half (e + 8) % 2 of word (e + 8) / 2
+  uint32_t w[4];
+  switch ((8 - off) >> 1) {
+    case 0: shifted<0>(all, off & 1, w); break;
+    case 1: shifted<1>(all, off & 1, w); break;
+    case 2: shifted<2>(all, off & 1, w); break;
+    default: shifted<3>(all, off & 1, w); break;
+  }
+  if (whole) stg_once(row - off, make_uint4(w[0], w[1], w[2], w[3]));
+  // the rest: the chunk's elements up to its 16 bytes' end, and those behind it where
+  // no lane follows, two at a time where the half begins on four bytes
+  const bool last = c8 == 15 || left <= 8;
+  if (whole && !last) return;
+  const int end = 8 - off, lo = whole ? end : c8 > 0 ? -off : 0, hi = last ? n : min(n, end);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) all[j] = before[j], all[4 + j] = own[j];
-    // word j of the result: elements 2 j - off and the next, of which `all` holds element e at (e + 8) / 2
-    const int words = (8 - off) >> 1, odd = off & 1;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t lo = 0, hi = 0;
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (words == q) lo = all[j + q], hi = all[j + q + 1];
-      w[j] = odd ? __funnelshift_r(lo, hi, 16) : lo;
+  for (int e = -6; e < 8; e += 2) {
+    const uint32_t word = all[(e + 8) >> 1];
+    if (off % 2 == 0 && e >= lo && e + 1 < hi) {
+      *reinterpret_cast<uint32_t*>(row + e) = word;
+    } else {
+      if (e >= lo && e < hi) row[e] = uint16_t(word);
+      if (e + 1 >= lo && e + 1 < hi) row[e + 1] = uint16_t(word >> 16);
     }
-    stg_once(row - off, make_uint4(w[0], w[1], w[2], w[3]));
-  } else {
-#pragma unroll
-    for (int e = -7; e < 8; ++e)
-      if (e >= (c8 > 0 ? -off : 0) && e < min(n, 8 - off)) row[e] = element(e);
   }
-  if (c8 == 15 || left <= 8) {  // no lane behind this one
-#pragma unroll
-    for (int e = 1; e < 8; ++e)
-      if (e >= 8 - off && e < n) row[e] = element(e);
-  }
+  if (lo <= -7 && hi > -7) row[-7] = uint16_t(all[0] >> 16);
 }
 
 constexpr int kBwdRows = 4;
 
 template <int ACT>
-__global__ void __launch_bounds__(kGluWarps * 32) glu8_bwd_kernel(const __grid_constant__ GluBwdP p) {
+__global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __grid_constant__ GluBwdP p) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
   const int32_t k = kt * kBlock8 + c8 * 8, left = p.H - k;
@@ -269,28 +271,35 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
     const TileIn& in = sh.in[buf];
     const int32_t tile = w / p.k_tiles, kt = w - tile * p.k_tiles, k = kt * kBlock8 + c8 * 8, rows = t.r1 - t.r0 - row0;
     F8 v[3][kTileRows];
-    float m[2 * kTileRows];
+    if (t.r1 - t.r0 > warp * 8) {
+      float m[2 * kTileRows];
 #pragma unroll
-    for (int i = 0; i < kTileRows; ++i) {
-      const int r = row0 + i;
-      const Grads o = glu_grads<ACT>(*reinterpret_cast<const uint2*>(&in.g[r][c8 * 8]), in.gs[r], *reinterpret_cast<const uint2*>(&in.u[r][c8 * 8]),
-                                     in.us[r], *reinterpret_cast<const uint4*>(&in.dh[r][c8 * 8]));
-      v[0][i] = o.dg;
-      v[1][i] = o.du;
-      v[2][i] = o.h;
-      m[2 * i] = amax8(o.dg);
-      m[2 * i + 1] = amax8(o.du);
-    }
-    // rows of d: lane 2 i + x of eight fits row i of dGate (x = 0) or dUp
-    const Fit8 f = fit8(scatter_max(m, lane));
-    if (c8 < 2 * kTileRows && c8 / 2 < rows) p.ds[int64_t(kt + (c8 & 1) * p.k_tiles) * p.M + t.r0 + row0 + c8 / 2] = f.s;
-#pragma unroll
-    for (int i = 0; i < kTileRows; ++i)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float r = __shfl_sync(0xFFFFFFFFu, f.r, 2 * i + x, 16);
-        if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8<false>(v[x][i], r));
+      for (int i = 0; i < kTileRows; ++i) {
+        const int r = row0 + i;
+        const Grads o = glu_grads<ACT>(*reinterpret_cast<const uint2*>(&in.g[r][c8 * 8]), in.gs[r], *reinterpret_cast<const uint2*>(&in.u[r][c8 * 8]),
+                                       in.us[r], *reinterpret_cast<const uint4*>(&in.dh[r][c8 * 8]));
+        v[0][i] = o.dg;
+        v[1][i] = o.du;
+        v[2][i] = o.h;
+        m[2 * i] = amax8(o.dg);
+        m[2 * i + 1] = amax8(o.du);
       }
+      // rows of d: lane 2 i + x of eight fits row i of dGate (x = 0) or dUp
+      const Fit8 f = fit8(scatter_max(m, lane));
+      if (c8 < 2 * kTileRows && c8 / 2 < rows) p.ds[int64_t(kt + (c8 & 1) * p.k_tiles) * p.M + t.r0 + row0 + c8 / 2] = f.s;
+#pragma unroll
+      for (int i = 0; i < kTileRows; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float r = __shfl_sync(0xFFFFFFFFu, f.r, 2 * i + x, 16);
+          if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8<false>(v[x][i], r));
+        }
+    } else {  // none of the warp's rows: zeros, for the columns
+#pragma unroll
+      for (int x = 0; x < 3; ++x)
+#pragma unroll
+        for (int i = 0; i < kTileRows; ++i) v[x][i] = zeros();
+    }
     if (tile < p.col_blocks) {  // the same for the whole block
       if (!t.cols) {  // rows of no expert: their blocks are zeros
 #pragma unroll
@@ -304,7 +313,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           auto at = [&](int i) { return fabsf(j & 1 ? v[x][i].v[j / 2].y : v[x][i].v[j / 2].x); };
-          c[j] = max_nan(max_nan(at(0), at(1)), at(2), at(3));
+          c[j] = max_nan(max_nan(at(0), at(1)), max_nan(at(2), at(3)));
         }
         // the half-warps' maxima: a lane of each keeps four columns
         const bool up = lane & 16;

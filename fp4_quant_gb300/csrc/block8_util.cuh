@@ -108,17 +108,12 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // |max| of eight values
 __device__ __forceinline__ float amax8(const F8& f) {
-  float m = max_nan(fabsf(f.v[0].x), fabsf(f.v[0].y));
+  float m[4];
 #pragma unroll
-  for (int i = 1; i < 4; ++i) m = max_nan(m, fabsf(f.v[i].x), fabsf(f.v[i].y));
-  return m;
+  for (int i = 0; i < 4; ++i) m[i] = max_nan(fabsf(f.v[i].x), fabsf(f.v[i].y));
+  return max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
 }
 // Largest bits of |v| of bf16 pairs (infinities and NaN above all others).
 __device__ __forceinline__ uint32_t amax_bits(const uint4& w) {
