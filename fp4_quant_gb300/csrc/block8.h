@@ -25,6 +25,9 @@ cudaError_t launch_quant8_weight(const glu_block8_quant_weight_args& a, cudaStre
 cudaError_t launch_glu8(const glu_block8_glu_args& a, cudaStream_t s);
 cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, const DevInfo& d);
+// y of few tokens: the weights are read once (block8_linear_few.cu).
+bool linear8_few(const glu_block8_linear_args& a);
+cudaError_t launch_linear8_few(const glu_block8_linear_args& a, cudaStream_t s);
 size_t linear8_workspace(const glu_block8_linear_args& a);
 cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t read_err_linear8(uint32_t* v, bool clear);

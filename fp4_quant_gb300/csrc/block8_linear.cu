@@ -27,6 +27,7 @@
 #include <cstring>
 
 #include "block8.h"
+#include "block_linear.cuh"
 #include "block_tiles.cuh"
 #include "tc.cuh"
 #include "tma.cuh"
@@ -83,6 +84,8 @@ struct Linear8P {
   int64_t ld_out, stride_out;
   void* out;
   int32_t f32;             // dw in fp32
+  float* part;             // splits > 1: [splits, rows, ld_part]
+  int64_t ld_part;
 };
 
 // Tile t; a dw sums over its expert's blocks of the column forms.
@@ -396,7 +399,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       for (int q = 0; q < 4; ++q) {
         const int32_t at = x.b0 + c0 + 32 * q;
         if (at >= b_end) break;
-        if (PROD != kGradW) {
+        if (PROD != kGradW && p.splits > 1) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              const int32_t n = row0 + (lane >> 2) + 8 * y, token = at + 8 * j + 2 * (lane & 3);
+              float* out = p.part + (int64_t(x.split) * p.rows + token) * p.ld_part + n;
+              if (n < p.width && token < b_end) out[0] = acc[q][y][j].x;
+              if (n < p.width && token + 1 < b_end) out[p.ld_part] = acc[q][y][j].y;
+            }
+        } else if (PROD != kGradW) {
           // eight tokens at a time: their rows' 8 x 8 blocks transposed, then four
           // lanes' words, so that a lane has eight columns of one token
           const int32_t n = row0 + 8 * (lane & 3), left = p.width - n;
@@ -476,13 +489,45 @@ cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
   return launch_kernel(kern, 2 * pairs, kThreads8, kSmem8, s, p, true);
 }
 
+// How the tokens of a dense y or dx are cut into tiles (at most `most` each) and the
+// sum into parts, a function of the shape alone (76 pairs): the plan with the least
+// estimated time.  A block of the sum takes 0.4 us in a tile of 32 tokens and 0.55
+// in one of 256 (7168 x 8192 of 32 tokens 31 us, 4096 tokens 215), the busiest
+// pair's tiles follow each other, and the join of split sums reads and writes the
+// fp32 parts.
+struct TokenPlan8 {
+  int most, splits;
+};
+TokenPlan8 token_plan8(int64_t rows, int64_t width, int64_t depth) {
+  const int64_t at = (width + kTile - 1) / kTile, blocks = blocks8(depth);
+  TokenPlan8 best = {kTile, 1};
+  double least = 1e30;
+  for (int n = 1; n <= 8 && blocks / n >= 4; ++n)
+    for (int most = kTile; most >= 64; most -= kStep) {
+      const int64_t bt = (rows + most - 1) / most, each = ((rows + bt - 1) / bt + kStep - 1) / kStep * kStep;
+      double us = double((at * bt * n + 75) / 76) * (double((blocks + n - 1) / n) * (0.38 + 0.17 * double(each) / kTile) + 1.5);
+      if (n > 1) us += 3.0 + double(n) * double(rows) * double(width) * 8e-6 / 4.0;
+      if (us < least * 0.98) least = us, best = {most, n};
+    }
+  return best;
+}
+TokenPlan8 plan8(const glu_block8_linear_args& a) {
+  if (a.E > 0 || linear8_few(a)) return {kTile, 1};
+  return a.grad ? token_plan8(a.M, a.K, a.N) : token_plan8(a.M, a.N, a.K);
+}
+
 }  // namespace
 
-size_t linear8_workspace(const glu_block8_linear_args&) { return 0; }
+size_t linear8_workspace(const glu_block8_linear_args& a) {
+  const int splits = plan8(a).splits;
+  return splits > 1 ? size_t(splits) * size_t(a.M) * size_t(((a.grad ? a.K : a.N) + 7) / 8 * 8) * 4 : 0;
+}
 
 cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, const DevInfo& d) {
+  if (linear8_few(a)) return launch_linear8_few(a, s);
   Linear8P p;
   memset(&p, 0, sizeof p);
+  const TokenPlan8 plan = plan8(a);
   const bool grad = a.grad != 0;
   const int64_t E = a.E > 0 ? a.E : 1, depth = grad ? a.N : a.K;
   cudaError_t e = make_byte_stack_map(&p.ta, a.wq, a.K, a.N, a.ld_w, E, a.E > 0 ? a.stride_w : a.N * a.ld_w, kHalf);
@@ -493,8 +538,10 @@ cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, cons
   p.rows = int32_t(a.M);
   p.width = int32_t(grad ? a.K : a.N);
   p.depth = int32_t(depth);
-  p.most = kTile;
-  p.splits = 1;
+  p.most = plan.most;
+  p.splits = plan.splits;
+  p.part = static_cast<float*>(a.workspace);
+  p.ld_part = (p.width + 7) / 8 * 8;
   p.sa = a.ws;
   p.sa_e = blocks8(a.N) * blocks8(a.K);
   p.sa_row = grad ? 1 : blocks8(a.K);
@@ -503,7 +550,16 @@ cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, cons
   p.ld_sb = a.M;
   p.out = a.y;
   p.ld_out = a.ld_y;
-  return grad ? launch8<kGradX>(p, s, d) : launch8<kForward>(p, s, d);
+  e = grad ? launch8<kGradX>(p, s, d) : launch8<kForward>(p, s, d);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  glu_block_linear_fwd_args j = {};  // the join of a bf16 layer without bias, activation and residual
+  j.act = GLU_ACT_IDENTITY;
+  j.b_fmt = GLU_FMT_BF16;
+  j.M = a.M;
+  j.N = p.width;
+  j.ld_y = a.ld_y;
+  j.y = a.y;
+  return launch_linear_join(j, p.part, p.splits, s);
 }
 
 cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s, const DevInfo& d) {

@@ -86,6 +86,22 @@ def test_linear_refusals(kw, status):
     assert _status("glu_block8_linear", B.Linear8Args, LINEAR, kw) == status
 
 
+def test_linear_workspace():
+    """Parts of split sums: none for few tokens, by expert and where tiles abound."""
+    def need(**kw):
+        n = ctypes.c_size_t(99)
+        assert B._func("glu_block8_linear_workspace")(ctypes.byref(B.Linear8Args(**{**LINEAR, **kw})), ctypes.byref(n)) == G.GLU_OK
+        return n.value
+    big = dict(N=1030, K=8192, ld_x=8192, ld_w=8192, ld_y=1032)
+    assert need(M=16, **big) == 0 and need(M=4096, **big) == 0 and need(M=200, E=4, **big) == 0
+    n = need(M=200, **big)
+    assert n > 0 and n % (200 * 1032 * 4) == 0
+    assert need(M=200, N=8192, K=1030, grad=1) == n
+    assert _status("glu_block8_linear", B.Linear8Args, LINEAR, dict(M=200, **big, workspace_bytes=n - 1)) == G.GLU_EINVAL
+    assert _status("glu_block8_linear", B.Linear8Args, LINEAR, dict(M=200, **big, workspace=None)) == G.GLU_EINVAL
+    assert _status("glu_block8_linear", B.Linear8Args, LINEAR, dict(M=200, **big, workspace=P + 8, workspace_bytes=n)) == G.GLU_EALIGN
+
+
 DW = dict(C=3, N=48, K=64, ld_dy=48, ld_x=64, ld_dw=64, stride_dw=3072, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2)
 
 

@@ -302,6 +302,14 @@ def test_products(M, N, K, grad):
     _check_product(y, x, w, grad, None)
 
 
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("M,N,K", [(17, 256, 4096), (64, 257, 2049), (130, 2304, 1100), (200, 1024, 2304), (300, 128, 8192), (5, 5000, 136), (16, 2500, 1000), (9, 33, 4111)])
+def test_products_of_few_rows(M, N, K, grad):
+    """Sums cut into parts and joined, and up to sixteen tokens at every number of blocks."""
+    x, w = _operands(M, N, K, 0, grad, M + N)
+    _check_product((G.linear8_dx if grad else G.linear8)(x, w), x, w, grad, None)
+
+
 EXPERTS = [(1, 64, 128, 4, 0, ()), (7, 136, 264, 64, 0, (0,)), (300, 256, 384, 3, 30, (1,)), (1000, 520, 200, 16, 100, (0, 7, 15)), (513, 128, 128, 2, 0, ()),
            (2000, 384, 256, 5, 0, (2,)), (40, 32, 32, 1024, 3, ()), (600, 128, 256, 300, 0, (5,)), (64, 128, 128, 3, 64, ())]
 
