@@ -39,9 +39,8 @@ __device__ __forceinline__ void few8_copy(uint4* slot, const uint8_t* row, int32
                "l"(bytes ? row + k : row), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void few8_copy(float* slot, const float* from, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(slot))), "l"(from), "r"(there ? 4u : 0u)
-               : "memory");
+__device__ __forceinline__ void few8_copy(float* slot, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(uint32_t(__cvta_generic_to_shared(slot))), "l"(from) : "memory");
 }
 
 // TT: groups of eight tokens; DEEP: slots, one more than the blocks in flight.  A
@@ -68,6 +67,11 @@ __global__ void __launch_bounds__(kFewWarps8 * 32) few8_kernel(const __grid_cons
   const int32_t blocks = (p.K + kBlock8 - 1) / kBlock8, s0 = blocks * warp / kFewWarps8, s1 = blocks * (warp + 1) / kFewWarps8;
   const float* ws = p.ws + int64_t(n0 / kBlock8) * blocks;  // 16 rows of W never cross one of its blocks
   uint4* mine = ring + warp * DEEP * kSlot8<TT> * 32 + lane;
+  // what belongs to tokens past M is never copied
+#pragma unroll
+  for (int i = 0; i < DEEP; ++i)
+#pragma unroll
+    for (int j = 4; j < kSlot8<TT>; ++j) mine[(i * kSlot8<TT> + j) * 32] = make_uint4(0, 0, 0, 0);
   after_previous();
   auto copy = [&](int32_t s, int slot) {
     if (s < s1) {
@@ -80,14 +84,14 @@ __global__ void __launch_bounds__(kFewWarps8 * 32) few8_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
           const int32_t m = 8 * j + g;
-          few8_copy(q + (4 + 2 * j + i) * 32, p.x + int64_t(min(m, p.M - 1)) * p.ld_x, k + 64 * i, m < p.M ? left - 64 * i : 0);
+          if (m < p.M) few8_copy(q + (4 + 2 * j + i) * 32, p.x + int64_t(m) * p.ld_x, k + 64 * i, left - 64 * i);
         }
       }
-      few8_copy(reinterpret_cast<float*>(q + (4 + 2 * TT) * 32), ws + s, true);
+      few8_copy(reinterpret_cast<float*>(q + (4 + 2 * TT) * 32), ws + s);
 #pragma unroll
       for (int i = 0; i < 2 * TT; ++i) {
         const int32_t m = 8 * (i / 2) + 2 * t + (i & 1);
-        few8_copy(reinterpret_cast<float*>(q + (4 + 2 * TT + (1 + i) / 4) * 32) + (1 + i) % 4, p.xs + int64_t(s) * p.M + min(m, p.M - 1), m < p.M);
+        if (m < p.M) few8_copy(reinterpret_cast<float*>(q + (4 + 2 * TT + (1 + i) / 4) * 32) + (1 + i) % 4, p.xs + int64_t(s) * p.M + m);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
