@@ -35,7 +35,7 @@
 namespace gq {
 namespace {
 
-constexpr int kBK8 = 128, kStages8 = 6;
+constexpr int kBK8 = 128, kStages8 = 4;
 constexpr int kOperand8 = kHalf * kBK8;  // 16 KB
 constexpr int kStageBytes8 = 2 * kOperand8;
 constexpr int kScaleSlots = 2;  // as many as accumulators, whose barriers count the scales too
@@ -61,7 +61,13 @@ struct Ctl8 {
   alignas(16) Scales scales[kScaleSlots];
   TilePlan plan;
 };
-constexpr int kSmem8 = 1024 + kStages8 * kStageBytes8 + int(sizeof(Ctl8));
+// A tile's results on their way out, by rows of the output: 256 tokens of 128
+// columns (bf16), or 128 rows of 256 (bf16) or of 128 at a time (fp32).  Rows 16
+// bytes further apart than they are long: the eight rows of a fragment then begin
+// in different banks.
+constexpr int kTokenPitch = kHalf * 2 + 16, kRowPitch = kTile * 2 + 16;
+constexpr int kOut8 = kTile * kTokenPitch > kHalf * kRowPitch ? kTile * kTokenPitch : kHalf * kRowPitch;
+constexpr int kSmem8 = 1024 + kStages8 * kStageBytes8 + kOut8 + int(sizeof(Ctl8));
 static_assert(kSmem8 <= 232448, "shared memory per CTA exceeds 227 KB");
 
 __device__ uint32_t g_err_linear8;
@@ -106,27 +112,21 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
   return r;
 }
-// The 4 x 4 block of words that a quad of lanes holds, transposed.
-__device__ __forceinline__ void word_transpose(uint32_t (&w)[4], int lane) {
-  const bool odd = lane & 1, up = lane & 2;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[i] : w[i + 1], 1);
-    if (odd) w[i] = got;
-    else w[i + 1] = got;
+// Barrier of the epilogue's warps.
+__device__ __forceinline__ void epilogue_barrier() { asm volatile("barrier.sync 1, %0;" ::"n"(kEpiWarps8 * 32) : "memory"); }
+
+// `bytes` of an output row from shared memory (both on 16 bytes): whole 16 bytes by
+// the copy engine, as part of this thread's bulk group, the rest (elements of
+// `size`) by the thread.
+__device__ __forceinline__ void put_row(void* out, const uint8_t* row, int32_t bytes, int size) {
+  const uint32_t whole = uint32_t(bytes) & ~15u;
+  if (whole) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(out), "r"(smem_u32(row)), "r"(whole) : "memory");
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[i] : w[i + 2], 2);
-    if (up) w[i] = got;
-    else w[i + 2] = got;
+  for (int32_t i = int32_t(whole); i < bytes; i += size) {
+    if (size == 4) *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(out) + i) = *reinterpret_cast<const uint32_t*>(row + i);
+    else *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(out) + i) = *reinterpret_cast<const uint16_t*>(row + i);
   }
-}
-// Eight bf16 of a row (16-byte aligned), or its first n; they stay in L2 (as in linear).
-__device__ __forceinline__ void store_row8(uint16_t* o, int32_t n, const uint32_t (&w)[4]) {
-  const uint4 v = make_uint4(w[0], w[1], w[2], w[3]);
-  if (n >= 8) *reinterpret_cast<uint4*>(o) = v;
-  else put8(o, n, v);
 }
 
 template <int REGS>
@@ -144,7 +144,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
   constexpr uint32_t kIdesc = kIdesc8 | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  Ctl8* ctl = reinterpret_cast<Ctl8*>(stages + kStages8 * kStageBytes8);
+  uint8_t* out_rows = stages + kStages8 * kStageBytes8;
+  Ctl8* ctl = reinterpret_cast<Ctl8*>(out_rows + kOut8);
   const int warp = __shfl_sync(0xFFFFFFFFu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -321,8 +322,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
     const uint32_t tempty0 = peer_addr(&ctl->tempty[0], 0);
     const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16);
     uint32_t i = 0;
+    // a warp whose wait gave up waits for nothing more and stores nothing, but keeps
+    // to the barriers that it shares with the others
     bool ok = true;
-    for (int32_t t = pair; t < tiles && ok; t += pairs) {
+    for (int32_t t = pair; t < tiles; t += pairs) {
       const Tile x = tile8_at<PROD>(p, ctl->plan, t);
       // acc[q][i][k]: row lane / 4 + 8 i of the warp's 32, columns 8 k + 2 (lane % 4)
       // and the next of the 32 from c0 + 32 q on
@@ -349,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[q & 1][j] = *reinterpret_cast<const float2*>(col + 8 * j);
       };
-      if (x.k0 < x.k_end) {
+      if (x.k0 < x.k_end && ok) {
         ready();
         if (ok) fetch(0);
       }
@@ -392,62 +395,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->sempty[slot]);
       }
-      if (!ok) break;
       const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
       const int32_t b_end = min(x.b_end, x.b0 + c1);                     // of this group
+      if (PROD != kGradW && p.splits > 1) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int32_t at = x.b0 + c0 + 32 * q;
-        if (at >= b_end) break;
-        if (PROD != kGradW && p.splits > 1) {
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const int32_t n = row0 + (lane >> 2) + 8 * y, token = at + 8 * j + 2 * (lane & 3);
+              const int32_t n = row0 + (lane >> 2) + 8 * y, token = x.b0 + c0 + 32 * q + 8 * j + 2 * (lane & 3);
               float* out = p.part + (int64_t(x.split) * p.rows + token) * p.ld_part + n;
+              if (!ok) continue;
               if (n < p.width && token < b_end) out[0] = acc[q][y][j].x;
               if (n < p.width && token + 1 < b_end) out[p.ld_part] = acc[q][y][j].y;
             }
-        } else if (PROD != kGradW) {
-          // eight tokens at a time: their rows' 8 x 8 blocks transposed, then four
-          // lanes' words, so that a lane has eight columns of one token
-          const int32_t n = row0 + 8 * (lane & 3), left = p.width - n;
+        continue;
+      }
+      // into shared memory, where the last tile's rows have left, and out from there
+      // while the next tile is summed
+      const int er = (warp - kLoadWarps) * 32 + lane;  // 0 .. 255
+      const int32_t cta0 = x.a0 + int32_t(rank) * kHalf;  // of D: this CTA's rows
+      if (PROD != kGradW) {
+        bulk_wait_read0();
+        epilogue_barrier();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int y = 0; y < 4; ++y) w[y] = transpose8x8(bf16x2_of(acc[q][y][j].x, acc[q][y][j].y));
-            word_transpose(w, lane);
-            const int32_t token = at + 8 * j + (lane >> 2);
-            if (token < b_end && left > 0) store_row8(static_cast<uint16_t*>(p.out) + int64_t(token) * p.ld_out + n, left, w);
+          for (int j = 0; j < 4; ++j)
+            if (c0 + 32 * q + 8 * j < c1) {
+#pragma unroll
+              for (int y = 0; y < 4; ++y)  // an 8 x 8 block: rows of D by tokens, transposed
+                *reinterpret_cast<uint32_t*>(out_rows + (c0 + 32 * q + 8 * j + (lane >> 2)) * kTokenPitch +
+                                             (quarter * 32 + 8 * y + 2 * (lane & 3)) * 2) =
+                    transpose8x8(bf16x2_of(acc[q][y][j].x, acc[q][y][j].y));
           }
-        } else {
+        fence_proxy_async();
+        epilogue_barrier();
+        const int32_t left = min(p.width - cta0, int32_t(kHalf));
+        if (ok && x.b0 + er < x.b_end && left > 0)
+          put_row(static_cast<uint16_t*>(p.out) + int64_t(x.b0 + er) * p.ld_out + cta0, out_rows + er * kTokenPitch, left * 2, 2);
+        bulk_commit();
+      } else {
+        const int64_t base = x.e * p.stride_out + int64_t(cta0) * p.ld_out + x.b0;
 #pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const int32_t row = row0 + (lane >> 2) + 8 * y;
-            if (p.f32) {
-              float* out = static_cast<float*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + at + 2 * (lane & 3);
+        for (int h = 0; h < 2; ++h) {  // fp32: the columns of either group in turn
+          if (!p.f32 && h == 1) break;
+          bulk_wait_read0();
+          epilogue_barrier();
+          if (!p.f32 || group == h) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int32_t left = b_end - at - 8 * j - 2 * (lane & 3);
-                if (row >= p.width || left <= 0) continue;
-                if (left > 1) *reinterpret_cast<float2*>(out + 8 * j) = acc[q][y][j];
-                else out[8 * j] = acc[q][y][j].x;
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                uint8_t* row = out_rows + (quarter * 32 + (lane >> 2) + 8 * y) * kRowPitch;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const int c = 32 * q + 8 * j + 2 * (lane & 3);
+                  if (p.f32) *reinterpret_cast<float2*>(row + c * 4) = acc[q][y][j];
+                  else *reinterpret_cast<uint32_t*>(row + (c0 + c) * 2) = bf16x2_of(acc[q][y][j].x, acc[q][y][j].y);
+                }
               }
-            } else {
-              uint32_t w[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) w[j] = bf16x2_of(acc[q][y][j].x, acc[q][y][j].y);
-              word_transpose(w, lane);
-              const int32_t c = at + 8 * (lane & 3), left = b_end - c;
-              if (row < p.width && left > 0)
-                store_row8(static_cast<uint16_t*>(p.out) + x.e * p.stride_out + int64_t(row) * p.ld_out + c, left, w);
-            }
           }
+          fence_proxy_async();
+          epilogue_barrier();
+          const int32_t first = p.f32 ? kHalf * h : 0, left = min(x.b_end - x.b0 - first, p.f32 ? kHalf : kTile);
+          if (ok && er < kHalf && cta0 + er < p.width && left > 0) {
+            const int64_t at = base + er * p.ld_out + first;
+            if (p.f32) put_row(static_cast<float*>(p.out) + at, out_rows + er * kRowPitch, left * 4, 4);
+            else put_row(static_cast<uint16_t*>(p.out) + at, out_rows + er * kRowPitch, left * 2, 2);
+          }
+          bulk_commit();
         }
       }
     }
+    bulk_wait0();
     // rows that no expert has
     if (PROD != kGradW && p.offsets) {
       const float zero[8] = {};
