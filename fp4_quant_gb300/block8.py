@@ -221,10 +221,12 @@ def _product(x8, w8, offsets, out, grad):
     y = _result(None if out is None else {"out": out}, "out", (M, K if grad else N), _BF16, device)
     a = Linear8Args(M, N, K, ld_x, ld_w, _stack(wq, E, N, ld_w), _ld(y), x8["q"].data_ptr(), xs, wq.data_ptr(), ws, off, y.data_ptr(),
                     None, 0, E, int(grad))
-    n = _size(0)
-    _call("glu_block8_linear_workspace", a, n)
-    ws = _scratch(n.value)
-    a.workspace, a.workspace_bytes = _p(ws), n.value
+    ws = None
+    if E == 0 and M > 1:  # by expert and for one token it takes none
+        n = _size(0)
+        _call("glu_block8_linear_workspace", a, n)
+        ws = _scratch(n.value)
+        a.workspace, a.workspace_bytes = _p(ws), n.value
     _call("glu_block8_linear", a, _handle(device))
     return y
 
