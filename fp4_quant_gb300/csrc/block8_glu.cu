@@ -20,11 +20,11 @@ struct GluP {
 // Forward: a warp takes 2 x kFwdRows rows of a 128-column strip.
 constexpr int kFwdRows = 2;
 
-template <int ACT, bool H8>
-__global__ void __launch_bounds__(kGluWarps * 32, 4) glu8_kernel(const __grid_constant__ GluP p) {
+// WHOLE (here and below): the strip's 128 columns are all there.
+template <int ACT, bool H8, bool WHOLE>
+__device__ __forceinline__ void glu_tile(const GluP& p, int32_t tile, int32_t kt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
-  const int32_t k = kt * kBlock8 + c8 * 8, left = p.H - k;
+  const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.H - k;
   const int64_t row0 = (int64_t(tile) * kGluWarps + warp) * 2 * kFwdRows + (lane >> 4) * kFwdRows;
   const int32_t have = int32_t(min(int64_t(p.M) - row0, int64_t(kFwdRows))), rows = left > 0 ? have : 0;
   uint4 g[kFwdRows], u[kFwdRows];
@@ -70,6 +70,14 @@ __global__ void __launch_bounds__(kGluWarps * 32, 4) glu8_kernel(const __grid_co
     if (H8) put_bytes8(p.hq + r * p.ld_hq + k, left, codes8<false>(h[i], rh));
     else put8(p.h + r * p.ld_h + k, left, packed(h[i]));
   }
+}
+
+template <int ACT, bool H8>
+__global__ void __launch_bounds__(kGluWarps * 32, 4) glu8_kernel(const __grid_constant__ GluP p) {
+  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
+  after_previous();
+  if ((kt + 1) * kBlock8 <= p.H) glu_tile<ACT, H8, true>(p, tile, kt);
+  else glu_tile<ACT, H8, false>(p, tile, kt);
 }
 
 struct GluBwdP {
@@ -151,11 +159,10 @@ __device__ __forceinline__ void put_shifted(uint16_t* row, int off, int left, bo
 
 constexpr int kBwdRows = 4;
 
-template <int ACT>
-__global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __grid_constant__ GluBwdP p) {
+template <int ACT, bool WHOLE>
+__device__ __forceinline__ void glu_bwd_tile(const GluBwdP& p, int32_t tile, int32_t kt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
-  const int32_t k = kt * kBlock8 + c8 * 8, left = p.H - k;
+  const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.H - k;
   const int64_t row0 = (int64_t(tile) * kGluWarps + warp) * 2 * kBwdRows + (lane >> 4) * kBwdRows;
   const int32_t rows = left > 0 ? int32_t(min(int64_t(p.M) - row0, int64_t(kBwdRows))) : 0;
   uint2 g[kBwdRows], u[kBwdRows];
@@ -185,8 +192,16 @@ __global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __gri
       if (off == 0) put8(p.d + r * p.ld_d + p.H + k, left, du);
       if (p.h) put8(p.h + r * p.ld_h + k, left, packed(o.h));
     }
-    if (off != 0) put_shifted(p.d + r * p.ld_d + p.H + k, off, left, store, du, c8);
+    if (off != 0) put_shifted(p.d + r * p.ld_d + p.H + k, off, WHOLE ? p.H - k : left, store, du, c8);
   }
+}
+
+template <int ACT>
+__global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __grid_constant__ GluBwdP p) {
+  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
+  after_previous();
+  if ((kt + 1) * kBlock8 <= p.H) glu_bwd_tile<ACT, true>(p, tile, kt);
+  else glu_bwd_tile<ACT, false>(p, tile, kt);
 }
 
 // Backward, quantised: blocks of 16 warps, one per SM, walk tiles of 128 rows by
@@ -359,15 +374,13 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
 template <int ACT>
 cudaError_t launch_fwd(const GluP& p, cudaStream_t s) {
   const int64_t per = kGluWarps * 2 * kFwdRows, tiles = (p.M + per - 1) / per * p.k_tiles;
-  if (p.hq) glu8_kernel<ACT, true><<<unsigned(tiles), kGluWarps * 32, 0, s>>>(p);
-  else glu8_kernel<ACT, false><<<unsigned(tiles), kGluWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(p.hq ? glu8_kernel<ACT, true> : glu8_kernel<ACT, false>, unsigned(tiles), kGluWarps * 32, 0, s, p, true);
 }
 template <int ACT>
 cudaError_t launch_bwd(GluBwdP& p, cudaStream_t s, const DevInfo& d) {
   if (p.d) {
     const int64_t per = kGluWarps * 2 * kBwdRows, tiles = (p.M + per - 1) / per * p.k_tiles;
-    glu8_bwd_kernel<ACT><<<unsigned(tiles), kGluWarps * 32, 0, s>>>(p);
+    return launch_kernel(glu8_bwd_kernel<ACT>, unsigned(tiles), kGluWarps * 32, 0, s, p, true);
   } else {
     p.tiles = (p.col_blocks + (p.E > 0 ? 1 : 0)) * p.k_tiles;
     auto kern = glu8_bwd_tile_kernel<ACT>;
@@ -376,7 +389,6 @@ cudaError_t launch_bwd(GluBwdP& p, cudaStream_t s, const DevInfo& d) {
     if (e != cudaSuccess) return e;
     return launch_kernel(kern, unsigned(p.tiles < d.sms ? p.tiles : d.sms), kTileWarps * 32, sizeof(TileShared), s, p, true);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace

@@ -29,14 +29,13 @@ struct ColFits {
 
 // A warp has rows 16 w .. 16 w + 15 of the tile: its lower half-warp the first
 // eight, the upper one the others, a lane eight columns of each.
-template <bool KEPT, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kQuantWarps * 32, 4) quant8_kernel(const __grid_constant__ QuantP p) {
-  __shared__ ColFits fits;
+// WHOLE: the tile's 128 columns are all there.
+template <bool KEPT, bool ROWS, bool COLS, bool WHOLE>
+__device__ __forceinline__ void quant_tile(const QuantP& p, ColFits& fits, int32_t tile, int32_t kt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
   const RowTile t = row_tile(p.offsets, p.E, p.M, tile);
   const bool cols = COLS && tile < p.col_blocks;
-  const int32_t k = kt * kBlock8 + c8 * 8, left = p.K - k;  // of the row from this lane's columns on
+  const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.K - k;  // of the row from this lane's columns on
   const int32_t row0 = warp * 16 + (lane >> 4) * kRowsPerLane, rows = t.r1 - t.r0 - row0;
   uint4 w[kRowsPerLane];     // bf16
   uint2 c[kRowsPerLane];     // KEPT: codes and scales
@@ -141,6 +140,15 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 4) quant8_kernel(const __gri
   }
 }
 
+template <bool KEPT, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(kQuantWarps * 32, KEPT ? 3 : 4) quant8_kernel(const __grid_constant__ QuantP p) {
+  __shared__ ColFits fits;
+  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
+  after_previous();
+  if ((kt + 1) * kBlock8 <= p.K) quant_tile<KEPT, ROWS, COLS, true>(p, fits, tile, kt);
+  else quant_tile<KEPT, ROWS, COLS, false>(p, fits, tile, kt);
+}
+
 struct WeightP {
   const uint16_t* w;
   uint8_t* q;
@@ -149,11 +157,10 @@ struct WeightP {
   int32_t N, K, n_tiles, k_tiles;
 };
 
-__global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __grid_constant__ WeightP p) {
-  __shared__ float part[kQuantWarps];
+template <bool WHOLE>
+__device__ __forceinline__ void weight_tile(const WeightP& p, float (&part)[kQuantWarps], int32_t rt, int32_t kt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t rt = blockIdx.x / p.k_tiles, kt = blockIdx.x - rt * p.k_tiles, e = rt / p.n_tiles, nt = rt - e * p.n_tiles;
-  const int32_t k = kt * kBlock8 + c8 * 8, left = p.K - k;
+  const int32_t e = rt / p.n_tiles, nt = rt - e * p.n_tiles, k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.K - k;
   const int32_t row0 = nt * kBlock8 + warp * 16 + (lane >> 4) * kRowsPerLane, rows = p.N - row0;
   const uint16_t* src = p.w + e * p.stride_w + int64_t(row0) * p.ld_w + k;
   uint4 w[kRowsPerLane];
@@ -175,6 +182,14 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __gr
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i)
     if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8<true>(pairs(w[i]), f.r));
+}
+
+__global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __grid_constant__ WeightP p) {
+  __shared__ float part[kQuantWarps];
+  const int32_t rt = blockIdx.x / p.k_tiles, kt = blockIdx.x - rt * p.k_tiles;
+  after_previous();
+  if ((kt + 1) * kBlock8 <= p.K) weight_tile<true>(p, part, rt, kt);
+  else weight_tile<false>(p, part, rt, kt);
 }
 
 }  // namespace
@@ -204,8 +219,7 @@ cudaError_t launch_quant8(const glu_block8_quant_args& a, cudaStream_t s) {
               : a.qc == nullptr ? quant8_kernel<false, true, false>
               : a.q == nullptr ? quant8_kernel<false, false, true>
                                : quant8_kernel<false, true, true>;
-  kern<<<unsigned(tiles * p.k_tiles), kQuantWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(kern, unsigned(tiles * p.k_tiles), kQuantWarps * 32, 0, s, p, true);
 }
 
 cudaError_t launch_quant8_weight(const glu_block8_quant_weight_args& a, cudaStream_t s) {
@@ -222,8 +236,7 @@ cudaError_t launch_quant8_weight(const glu_block8_quant_weight_args& a, cudaStre
   p.n_tiles = int32_t(blocks8(a.N));
   p.k_tiles = int32_t(blocks8(a.K));
   const int64_t tiles = int64_t(a.E > 0 ? a.E : 1) * p.n_tiles * p.k_tiles;
-  weight8_kernel<<<unsigned(tiles), kQuantWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_kernel(weight8_kernel, unsigned(tiles), kQuantWarps * 32, 0, s, p, true);
 }
 
 }  // namespace gq
