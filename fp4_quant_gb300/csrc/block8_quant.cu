@@ -29,13 +29,15 @@ struct ColFits {
 
 // A warp has rows 16 w .. 16 w + 15 of the tile: its lower half-warp the first
 // eight, the upper one the others, a lane eight columns of each.
-// WHOLE: the tile's 128 columns are all there.
-template <bool KEPT, bool ROWS, bool COLS, bool WHOLE>
-__device__ __forceinline__ void quant_tile(const QuantP& p, ColFits& fits, int32_t tile, int32_t kt) {
+template <bool KEPT, bool ROWS, bool COLS>
+__global__ void __launch_bounds__(kQuantWarps * 32, 4) quant8_kernel(const __grid_constant__ QuantP p) {
+  __shared__ ColFits fits;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
+  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
+  after_previous();
   const RowTile t = row_tile(p.offsets, p.E, p.M, tile);
   const bool cols = COLS && tile < p.col_blocks;
-  const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.K - k;  // of the row from this lane's columns on
+  const int32_t k = kt * kBlock8 + c8 * 8, left = p.K - k;  // of the row from this lane's columns on
   const int32_t row0 = warp * 16 + (lane >> 4) * kRowsPerLane, rows = t.r1 - t.r0 - row0;
   uint4 w[kRowsPerLane];     // bf16
   uint2 c[kRowsPerLane];     // KEPT: codes and scales
@@ -140,15 +142,6 @@ __device__ __forceinline__ void quant_tile(const QuantP& p, ColFits& fits, int32
   }
 }
 
-template <bool KEPT, bool ROWS, bool COLS>
-__global__ void __launch_bounds__(kQuantWarps * 32, KEPT ? 3 : 4) quant8_kernel(const __grid_constant__ QuantP p) {
-  __shared__ ColFits fits;
-  const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
-  after_previous();
-  if ((kt + 1) * kBlock8 <= p.K) quant_tile<KEPT, ROWS, COLS, true>(p, fits, tile, kt);
-  else quant_tile<KEPT, ROWS, COLS, false>(p, fits, tile, kt);
-}
-
 struct WeightP {
   const uint16_t* w;
   uint8_t* q;
@@ -157,14 +150,16 @@ struct WeightP {
   int32_t N, K, n_tiles, k_tiles;
 };
 
-template <bool WHOLE>
-__device__ __forceinline__ void weight_tile(const WeightP& p, float (&part)[kQuantWarps], int32_t rt, int32_t kt) {
+__global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __grid_constant__ WeightP p) {
+  __shared__ float part[kQuantWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
-  const int32_t e = rt / p.n_tiles, nt = rt - e * p.n_tiles, k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.K - k;
+  const int32_t rt = blockIdx.x / p.k_tiles, kt = blockIdx.x - rt * p.k_tiles, e = rt / p.n_tiles, nt = rt - e * p.n_tiles;
+  const int32_t k = kt * kBlock8 + c8 * 8, left = p.K - k;
   const int32_t row0 = nt * kBlock8 + warp * 16 + (lane >> 4) * kRowsPerLane, rows = p.N - row0;
   const uint16_t* src = p.w + e * p.stride_w + int64_t(row0) * p.ld_w + k;
   uint4 w[kRowsPerLane];
   uint32_t u = 0;
+  after_previous();
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) w[i] = i < rows && left > 0 ? raw8(src + i * p.ld_w, left) : make_uint4(0, 0, 0, 0);
 #pragma unroll
@@ -182,14 +177,6 @@ __device__ __forceinline__ void weight_tile(const WeightP& p, float (&part)[kQua
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i)
     if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8<true>(pairs(w[i]), f.r));
-}
-
-__global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __grid_constant__ WeightP p) {
-  __shared__ float part[kQuantWarps];
-  const int32_t rt = blockIdx.x / p.k_tiles, kt = blockIdx.x - rt * p.k_tiles;
-  after_previous();
-  if ((kt + 1) * kBlock8 <= p.K) weight_tile<true>(p, part, rt, kt);
-  else weight_tile<false>(p, part, rt, kt);
 }
 
 }  // namespace
