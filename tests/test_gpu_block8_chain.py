@@ -164,3 +164,72 @@ def test_column_forms_of_parts_and_views():
     padded = torch.zeros(33, 72, dtype=BF, device=DEV)
     padded[:, :67] = odd
     assert _equal(list(G.quant8(odd, cols=True).values()), list(G.quant8(padded[:, :67], cols=True).values()))
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^31 elements: the last rows are those of a call on them alone."""
+    M, K = (1 << 18) + 5, 8200
+    x = torch.empty(M, K, dtype=BF, device=DEV).fill_(0.5)
+    x[-300:] = _rand(300, K, seed=1)
+    big, last = G.quant8(x, cols=True), G.quant8(x[-133:], cols=True)  # 133 = 128 + M % 128: the last two column blocks
+    assert _equal([big["q"][-133:], big["s"][:, -133:], big["qc"][-256:], big["sc"][-2:]], [last["q"], last["s"], last["qc"], last["sc"]])
+    again = G.quant8({"q": big["q"], "s": big["s"]}, rows=False, cols=True)
+    assert _equal([again["qc"][-256:]], [G.quant8({"q": last["q"], "s": last["s"]}, rows=False, cols=True)["qc"]])
+    del again, last
+    a, b = G.glu8(x, x), G.glu8(x[-133:], x[-133:])
+    assert _equal([a["h"]["q"][-133:], a["gate"]["s"][:, -133:]], [b["h"]["q"], b["gate"]["s"]])
+    d = G.glu8_bwd(a["gate"], a["up"], x)
+    assert torch.equal(d["d"][-133:], G.glu8_bwd(b["gate"], b["up"], x[-133:])["d"])
+
+
+def test_products_with_results_beyond_32_bits():
+    M, N, K = 1 << 17, 16520, 128
+    x8 = G.quant8(_rand(M, K, seed=2))
+    w8 = G.quant8_weight(_rand(N, K, seed=3))
+    y = G.linear8(x8, w8)
+    tail = {"q": x8["q"][-300:], "s": x8["s"][:, -300:].contiguous()}
+    assert torch.equal(y[-300:], G.linear8(tail, w8)) and torch.equal(y[:20], G.linear8({"q": x8["q"][:20], "s": x8["s"][:, :20].contiguous()}, w8))
+    del y
+    E, N, K = 64, 8192, 4104
+    off = torch.tensor([0] * (E - 1) + [100, 300], dtype=torch.int32, device=DEV)
+    d8, x8 = (G.quant8(_rand(300, n, seed=n), rows=False, cols=True, offsets=off) for n in (N, K))
+    dw = G.linear8_dw(d8, x8, offsets=off)
+    b = 100 // 128 + E - 1  # the last expert's two blocks
+    alone = G.linear8_dw(*({"qc": t["qc"][128 * b:128 * b + 256], "sc": t["sc"][b:b + 2].contiguous()} for t in (d8, x8)))
+    assert torch.equal(dw[-1], alone) and bool((dw[1:E - 2] == 0).all())
+
+
+def test_calls_on_two_streams_at_once():
+    x, w, dy = _rand(600, 1024, seed=20), G.quant8_weight(_rand(1024, 1024, seed=21, scale=0.1)), _rand(600, 1024, seed=22)
+    x8, d8 = G.quant8(x, cols=True), G.quant8(dy, cols=True)
+    few = {"q": x8["q"][:9], "s": x8["s"][:, :9].contiguous()}
+    want = [G.linear8(x8, w), G.linear8_dx(d8, w), G.linear8_dw(d8, x8), G.linear8(few, w), G.glu8(x, dy)["h"]["q"]]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(5):
+        for s in streams:
+            got.append([G.linear8(x8, w, stream=s), G.linear8_dx(d8, w, stream=s), G.linear8_dw(d8, x8, stream=s), G.linear8(few, w, stream=s),
+                        G.glu8(x, dy, stream=s)["h"]["q"]])
+    torch.cuda.synchronize()
+    assert all(_equal(g, want) for g in got)
+
+
+def test_offsets_out_of_range_stay_inside():
+    """Cuts past the last row count as the last row; nothing outside is touched."""
+    x, w = _rand(200, 256, seed=30), G.quant8_weight(_rand(3, 128, 256, seed=31))
+    good = torch.tensor([0, 50, 200, 200], dtype=torch.int32, device=DEV)
+    wild = torch.tensor([0, 50, 10 ** 6, 2 ** 31 - 1], dtype=torch.int32, device=DEV)
+    a, b = G.quant8(x, cols=True, offsets=good), G.quant8(x, cols=True, offsets=wild)
+    assert _equal([a["q"], a["qc"], a["sc"]], [b["q"], b["qc"], b["sc"]])
+    assert torch.equal(G.linear8(a, w, offsets=good), G.linear8(a, w, offsets=wild))
+    for bad in ([0, -5, 70, 200], [0, 150, 20, 300], [7, 3, 2, 1], [2 ** 31 - 1, 0, -1, 5]):
+        off = torch.tensor(bad, dtype=torch.int32, device=DEV)
+        q = G.quant8(x, cols=True, offsets=off)
+        G.linear8(a, w, offsets=off)
+        G.linear8_dx(G.quant8(_rand(200, 128, seed=32)), w, offsets=off)
+        G.linear8_dw(q, q, offsets=off)
+        g = G.glu8(x, x)
+        G.glu8_bwd(g["gate"], g["up"], x, quant=True, offsets=off)
+    torch.cuda.synchronize()
+    assert torch.equal(G.linear8(a, w, offsets=good), G.linear8(a, w, offsets=wild))
