@@ -20,7 +20,7 @@ inline int64_t col_blocks8(int64_t M, int32_t E) { return E > 0 ? M / kBlock8 + 
 cudaError_t make_byte_stack_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t row_stride, int64_t count,
                                 int64_t stride, int box_rows);
 
-cudaError_t launch_quant8(const glu_block8_quant_args& a, cudaStream_t s);
+cudaError_t launch_quant8(const glu_block8_quant_args& a, cudaStream_t s, const DevInfo& d);
 cudaError_t launch_quant8_weight(const glu_block8_quant_weight_args& a, cudaStream_t s);
 cudaError_t launch_glu8(const glu_block8_glu_args& a, cudaStream_t s);
 cudaError_t launch_glu8_bwd(const glu_block8_glu_bwd_args& a, cudaStream_t s, const DevInfo& d);

@@ -179,7 +179,7 @@ int check_glu_bwd(const glu_block8_glu_bwd_args* a) {
   const cudaStream_t s = static_cast<cudaStream_t>(stream); \
   return launched(launch)
 
-extern "C" int glu_block8_quant(const glu_block8_quant_args* a, void* stream) { GQ_ENTRY(check_quant(a), gq::launch_quant8(*a, s)); }
+extern "C" int glu_block8_quant(const glu_block8_quant_args* a, void* stream) { GQ_ENTRY(check_quant(a), gq::launch_quant8(*a, s, d)); }
 extern "C" int glu_block8_quant_weight(const glu_block8_quant_weight_args* a, void* stream) {
   GQ_ENTRY(check_quant_weight(a), gq::launch_quant8_weight(*a, s));
 }

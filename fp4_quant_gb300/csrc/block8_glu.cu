@@ -222,16 +222,6 @@ struct TileShared {
   int32_t offsets[kMaxExperts + 1];
 };
 
-// 16 bytes (4 for n = 4) to shared memory, zeros where `there` is false.
-__device__ __forceinline__ void copy16(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(there ? 16u : 0u)
-               : "memory");
-}
-__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(there ? 4u : 0u)
-               : "memory");
-}
-
 template <int ACT>
 __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const __grid_constant__ GluBwdP p) {
   extern __shared__ __align__(16) uint8_t raw[];
@@ -251,14 +241,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int q = threadIdx.x + j * kThreads, r = q >> 4, c = (q & 15) * 8;
-      copy16(&in.dh[r][c], p.dh + int64_t(r < rows ? t.r0 + r : 0) * p.ld_dh + k + c, r < rows);
+      copy16(&in.dh[r][c], p.dh + int64_t(r < rows ? t.r0 + r : 0) * p.ld_dh + k + c, r < rows ? 16u : 0u);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int q = threadIdx.x + j * kThreads, r = q >> 3, c = (q & 7) * 16;
       const int64_t m = r < rows ? t.r0 + r : 0;
-      copy16(&in.g[r][c], p.gq + m * p.ld_gq + k + c, r < rows);
-      copy16(&in.u[r][c], p.uq + m * p.ld_uq + k + c, r < rows);
+      copy16(&in.g[r][c], p.gq + m * p.ld_gq + k + c, r < rows ? 16u : 0u);
+      copy16(&in.u[r][c], p.uq + m * p.ld_uq + k + c, r < rows ? 16u : 0u);
     }
     if (threadIdx.x < 2 * kBlock8) {
       const int r = threadIdx.x % kBlock8;

@@ -102,6 +102,16 @@ __device__ __forceinline__ void put_bytes8(uint8_t* p, int n, const uint2& v) {
   }
 }
 
+// The first n of 16 bytes to shared memory (both on 16 bytes), the rest zeros; or a
+// word, or zero.
+__device__ __forceinline__ void copy16(void* dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(uint32_t(__cvta_generic_to_shared(dst))), "l"(src), "r"(there ? 4u : 0u)
+               : "memory");
+}
+
 // max that keeps a NaN
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
