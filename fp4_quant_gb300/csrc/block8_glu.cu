@@ -1,6 +1,10 @@
 // The gated activation that keeps gate and up in 8 bits, and its backward from
-// those (glu_block8.h).  Bound by HBM: every operand is read and every result
-// written once; 16 lanes share a row of 128 columns, eight each.
+// those (glu_block8.h).  Every operand is read and every result written once; 16
+// lanes share a row of 128 columns, eight each.  What binds is the issue of
+// instructions, at 55 to 65 % of its rate, not DRAM: 30 per value forward (4096 x
+// 7168 in 40 us, 5.1 TB/s), 50 for the bf16 backward of a ragged width (8191 x 1462
+// in 31 us, a fifth of it for dUp's rows, which begin inside 16 bytes), about 40 for
+// the quantised one (32768 x 1024 of 64 experts in 82 us).
 #include "block8_act.cuh"
 
 namespace gq {
@@ -17,7 +21,8 @@ struct GluP {
   int32_t M, H, k_tiles;
 };
 
-// Forward: a warp takes 2 x kFwdRows rows of a 128-column strip.
+// Forward: a warp takes 2 x kFwdRows rows of a 128-column strip (four rows per
+// lane: 53 us, two, with four blocks per SM: 45, in isolation).
 constexpr int kFwdRows = 2;
 
 // WHOLE (here and below): the strip's 128 columns are all there.
@@ -207,7 +212,9 @@ __global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __gri
 // Backward, quantised: blocks of 16 warps, one per SM, walk tiles of 128 rows by
 // 128 columns.  A lane has four rows of eight columns, and holds the three results
 // of its 32 elements in registers while the maxima of rows and columns are found;
-// the next tile's operands are on their way into shared memory meanwhile.
+// the next tile's operands are on their way into shared memory meanwhile (a block
+// per tile: 113 us for 32768 x 1024, this way 94, with cheaper activations and
+// scales 82).
 constexpr int kTileWarps = 16, kTileRows = 4;
 
 struct TileIn {

@@ -21,9 +21,18 @@
 //
 // What a thread has of the accumulator decides what its scales cost: with a row
 // per thread it needs every column's, 128 KB out of shared memory per block at 128
-// bytes a clock, and 4096 x 8192 x 7168 takes 299 us (215 with the scales left
-// out, 170 with the products alone).  As fragments (a quarter of the columns, four
-// rows) it is a quarter of that.
+// bytes a clock, and 4096 x 8192 x 7168 took 299 us (215 with the scales left out).
+// As fragments (a quarter of the columns, four rows) it is a quarter of that: 235.
+//
+// 4096 x 8192 x 7168 now takes 203 us (2370 TFLOP/s) and its dx 199; 32768 rows of 64
+// uneven experts x 2048 x 2048 179, their dw 258.  What binds is the epilogue's way
+// through a block, about 1000 cycles for 512 of products: a wait, eight reads of
+// tensor memory, 64 two-wide additions per thread, the hand-back.  Without the
+// additions 166 us, with the products and barriers alone 164.  So the epilogue
+// waits for one barrier per block, which counts the products and the scales, a
+// block's first chunk is on its way behind the last one's additions, and the
+// results leave through shared memory by bulk copies while the next tile is summed
+// (stored from registers: 211, dw by expert 319).
 #include <cstring>
 
 #include "block8.h"

@@ -6,10 +6,11 @@
 // / 4) a lane holds 16 from 16 (lane % 4) on and 16 from 64 bytes further on (whole
 // sectors in each copy); the order of a sum is free, so words 2 j and 2 j + 1 of them
 // serve as the instruction's k = 4 t .. and 4 t + 16 .. of step j, with x taken the
-// same way.  A block's sum is scaled and added in fp32.  Every
-// lane copies what it will use itself into slots of shared memory that only it
-// reads (cp.async), so a warp keeps several blocks in flight without registers or
-// barriers.
+// same way.  A block's sum is scaled and added in fp32.  Every lane copies what it
+// will use itself into slots of shared memory that only it reads (cp.async), so a
+// warp keeps several blocks in flight without registers or barriers.  One token of
+// 7168 x 8192: 12 us, 4.8 TB/s (27 with a lane's 32 bytes next to each other, half
+// sectors at a time; 25 in a tile of 32 tokens of the pairs' kernel).
 #include "block8.h"
 #include "block_util.cuh"
 
