@@ -8,31 +8,35 @@
 //   D[i, j] = sum over blocks b of sa(i, b) sb(j, b) sum over k in b of A[i, k] B[j, k]
 //
 // Tiles and walk are those of the bf16 layers (block_tiles.cuh): 256 rows of D by
-// up to 256 columns for a pair of CTAs, the tokens as the columns of y and dx.
-// One block of the sum is one slice of the ring (128 codes are the 128 bytes of
-// the swizzle) and one accumulator in tensor memory: while the tensor cores sum
-// the next block into the other one, eight warps read this one, scale it and add
-// it to what they hold in registers, 128 fp32 per thread.  Their share of the
-// register file is raised for that (setmaxnreg), the other four warps' lowered.
-// Two warps fetch the scales, block by block ahead, into a ring of their own; a
-// weight's scale is one number for the 128 rows of a CTA and goes into the
-// columns' scales there, so that a value costs half a two-wide multiply-add (dw:
-// a multiplication by its row's scale as well).
+// up to 256 columns for a pair of CTAs.  One block of the sum is one slice of the
+// ring (128 codes are the 128 bytes of the swizzle) and one accumulator in tensor
+// memory: while the tensor cores sum the next block into the other one, eight warps
+// read this one, scale it and add it to what they hold in registers, 128 fp32 per
+// thread.  Their share of the register file is raised for that (setmaxnreg), the
+// other four warps' lowered.  Two of those fetch the scales, block by block ahead.
 //
-// What a thread has of the accumulator decides what its scales cost: with a row
-// per thread it needs every column's, 128 KB out of shared memory per block at 128
-// bytes a clock, and 4096 x 8192 x 7168 took 299 us (215 with the scales left out).
-// As fragments (a quarter of the columns, four rows) it is a quarter of that: 235.
+// What a thread has of the accumulator decides what its scales cost.  With the
+// tokens as the rows of D (ROWS: many tokens) it has one row of 128 columns, where
+// the token's scale and the weight's are one number per block: 4096 x 8192 x 7168
+// takes 174 us (2760 TFLOP/s), its dx 168, 32768 rows of 64 uneven experts x 2048 x
+// 2048 158.  With few tokens they are the columns, whose number the instruction
+// leaves free in steps of 32, and so they are in the columns' place for dw, whose
+// rows and columns both have scales of their own.  A thread with one row would need
+// all the columns' scales then, 128 KB out of shared memory per block at 128 bytes a
+// clock (4096 x 8192 x 7168 took 299 us that way, 215 with the scales left out).
+// So it reads the accumulator as fragments, a quarter of the columns of four rows
+// (203 us; dw of 4096 x 8192 x 7168 258).
 //
-// 4096 x 8192 x 7168 now takes 203 us (2370 TFLOP/s) and its dx 199; 32768 rows of 64
-// uneven experts x 2048 x 2048 179, their dw 258.  What binds is the epilogue's way
-// through a block, about 1000 cycles for 512 of products: a wait, eight reads of
-// tensor memory, 64 two-wide additions per thread, the hand-back.  Without the
-// additions 166 us, with the products and barriers alone 164.  So the epilogue
-// waits for one barrier per block, which counts the products and the scales, a
-// block's first chunk is on its way behind the last one's additions, and the
-// results leave through shared memory by bulk copies while the next tile is summed
-// (stored from registers: 211, dw by expert 319).
+// What binds is a block's way between the tensor cores and the registers: a block's
+// 512 cycles of products, the hand-over to the epilogue's warps and back between the
+// CTAs, eight reads of tensor memory; without the additions 166 us, with the
+// products and barriers alone 164.  So the epilogue waits for one barrier per block,
+// which counts the products and the scales, a block's first chunk is on its way
+// behind the last one's additions, accumulators go back by relaxed arrivals between
+// tcgen05 fences (release at cluster scope waits for all that a thread has in
+// flight: 499 us at first, 301 without), and the results leave through shared memory
+// by bulk copies while the next tile is summed (stored from registers 8 us more; dw
+// by expert 319 against 258).
 #include <cstring>
 
 #include "block8.h"
@@ -103,14 +107,28 @@ struct Linear8P {
   int64_t ld_part;
 };
 
-// Tile t; a dw sums over its expert's blocks of the column forms.
-template <int PROD>
-__device__ __forceinline__ Tile tile8_at(const Linear8P& p, const TilePlan& plan, int32_t t) {
-  Tile x = tile_at<PROD, kBK8>(p, plan, t);
+struct Tile8 : Tile {
+  int32_t a_end;  // ROWS: rows of D end here (of the width: they go on, and are cut where they are stored)
+};
+// Tile t; a dw sums over its expert's blocks of the column forms.  ROWS: the
+// tokens are the rows of D and the width its columns.
+template <int PROD, bool ROWS>
+__device__ __forceinline__ Tile8 tile8_at(const Linear8P& p, const TilePlan& plan, int32_t t) {
+  Tile8 x;
+  static_cast<Tile&>(x) = tile_at<PROD, kBK8>(p, plan, t);
   if (PROD == kGradW && p.offsets) {
     const int32_t rows = x.k_end - x.k0;
     x.k0 = (x.k0 / kBK8 + x.e) * kBK8;
     x.k_end = x.k0 + (rows + kBK8 - 1) / kBK8 * kBK8;
+  }
+  x.a_end = p.width;
+  if (ROWS) {
+    const int32_t a0 = x.a0;
+    x.a0 = x.b0;
+    x.a_end = x.b_end;
+    x.b0 = a0;
+    x.b_end = min(p.width, a0 + kTile);
+    x.n = kTile;
   }
   return x;
 }
@@ -147,9 +165,9 @@ __device__ __forceinline__ void more_regs() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-template <int PROD>
+template <int PROD, bool ROWS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear8_kernel(const __grid_constant__ Linear8P p) {
-  constexpr bool kAmn = PROD != kForward, kBmn = PROD == kGradW;
+  constexpr bool kAmn = !ROWS && PROD != kForward, kBmn = ROWS ? PROD == kGradX : PROD == kGradW;
   constexpr uint32_t kIdesc = kIdesc8 | (kAmn ? 1u << 15 : 0u) | (kBmn ? 1u << 16 : 0u);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -195,7 +213,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       const uint32_t full0 = peer_addr(&ctl->full[0], 0);
       bool ok = true;
       for (int32_t t = pair; t < tiles && ok; t += pairs) {
-        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const Tile8 x = tile8_at<PROD, ROWS>(p, ctl->plan, t);
         const int32_t a0 = x.a0 + int32_t(rank) * kHalf, half = x.n / 2, b0 = x.b0 + int32_t(rank) * half;
         // the smallest box with the half's columns (more than it needs are not
         // multiplied)
@@ -213,11 +231,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
             uint8_t* b = a + kOperand8;
             const uint32_t bar = full0 + 8u * uint32_t(s);
             if (rank == 0) mbar_arrive_expect_tx(&ctl->full[s], 2 * bytes);
-            if (PROD == kForward) pair_load_3d(a, &p.ta, k, a0, x.e, bar);
+            if (ROWS) {
+              pair_load_2d(a, &p.tb[0], k, a0, bar);
+              if (PROD == kForward) pair_load_3d(b, &p.ta, k, b0, x.e, bar);
+              else pair_load_3d(b, &p.ta, b0, k, x.e, bar);
+            } else if (PROD == kForward) pair_load_3d(a, &p.ta, k, a0, x.e, bar);
             else if (PROD == kGradX) pair_load_3d(a, &p.ta, a0, k, x.e, bar);
             else pair_load_2d(a, &p.ta, a0, k, bar);
             if (PROD == kGradW) pair_load_2d(b, tb, b0, k, bar);
-            else pair_load_2d(b, tb, k, b0, bar);
+            else if (!ROWS) pair_load_2d(b, tb, k, b0, bar);
           }
           held = max(held, s + 1);
           if (++s == kStages8) s = 0, parity ^= 1u;
@@ -239,7 +261,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       const uint64_t bd0 = kBmn ? tc::sw128_mnmajor_desc(a_addr + kOperand8, kOperand8) : tc::sw128_kmajor_desc(a_addr + kOperand8);
       bool ok = true;
       for (int32_t t = pair; t < tiles && ok && rank == 0; t += pairs) {
-        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const Tile8 x = tile8_at<PROD, ROWS>(p, ctl->plan, t);
         const uint32_t idesc = kIdesc | (uint32_t(x.n >> 3) << 17);
         for (int32_t k = x.k0; k < x.k_end; k += kBK8) {
           const uint32_t b = i & 1u;
@@ -280,13 +302,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       uint32_t i = 0;
       bool ok = true;
       for (int32_t t = pair; t < tiles && ok; t += pairs) {
-        const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+        const Tile8 x = tile8_at<PROD, ROWS>(p, ctl->plan, t);
         const int32_t b0 = x.k0 / kBK8, b1 = (x.k_end + kBK8 - 1) / kBK8;
         const int32_t row0 = x.a0 + int32_t(rank) * kHalf;
-        const float* sa = p.sa + (PROD == kGradW ? int64_t(row0) : x.e * p.sa_e + row0 / kBlock8 * p.sa_row);
-        const float* sb = p.sb + x.b0;
+        // ROWS: the tokens' are the rows', the weight's one for either half of the columns
+        const float* sa = p.sa + (PROD == kGradW ? int64_t(row0) : x.e * p.sa_e + (ROWS ? x.b0 : row0) / kBlock8 * p.sa_row);
+        const float* sb = p.sb + (ROWS ? row0 : x.b0);
         float col[8], row[4], next_col[8], next_row[4];
         auto load = [&](int32_t b, float (&c)[8], float (&r)[4]) {
+          if (ROWS) {
+            c[0] = lane < 2 && x.b0 + kHalf * lane < p.width ? __ldg(sa + b * p.sa_b + lane * p.sa_row) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[j] = row0 + 32 * j + lane < x.a_end ? __ldg(sb + int64_t(b) * p.ld_sb + 32 * j + lane) : 0.0f;
+            return;
+          }
           if (PROD == kGradW) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[j] = row0 + 32 * j + lane < p.width ? __ldg(sa + int64_t(b) * p.width + 32 * j + lane) : 0.0f;
@@ -308,9 +337,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
             break;
           }
           Scales& o = ctl->scales[slot];
+          if (ROWS) {
+            if (lane < 2) o.col[lane] = col[0];
+          } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o.col[32 * j + lane] = PROD == kGradW ? col[j] : col[j] * row[0];
-          if (PROD == kGradW) {
+            for (int j = 0; j < 8; ++j) o.col[32 * j + lane] = PROD == kGradW ? col[j] : col[j] * row[0];
+          }
+          if (ROWS || PROD == kGradW) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) o.row[32 * j + lane] = row[j];
           }
@@ -335,9 +368,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
     // to the barriers that it shares with the others
     bool ok = true;
     for (int32_t t = pair; t < tiles; t += pairs) {
-      const Tile x = tile8_at<PROD>(p, ctl->plan, t);
+      const Tile8 x = tile8_at<PROD, ROWS>(p, ctl->plan, t);
       // acc[q][i][k]: row lane / 4 + 8 i of the warp's 32, columns 8 k + 2 (lane % 4)
-      // and the next of the 32 from c0 + 32 q on
+      // and the next of the 32 from c0 + 32 q on; ROWS: row `lane`, columns 8 i + 2 k
+      // and the next
       float2 acc[4][4][4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -355,6 +389,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       };
       auto fetch = [&](int q) {
         const uint32_t at = lanes + (i & 1u) * kTile + uint32_t(c0 + 32 * q);
+        if (ROWS) {
+          tc::ld32(at, reinterpret_cast<uint32_t(&)[32]>(r[q & 1]));
+          return;
+        }
         tc::ld16x32(at, r[q & 1][0]);
         tc::ld16x32(at + (16u << 16), r[q & 1][1]);
         const float* col = ctl->scales[i % kScaleSlots].col + c0 + 32 * q + 2 * (lane & 3);
@@ -369,6 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
         const int slot = int(i % kScaleSlots);
         const Scales& sc = ctl->scales[slot];
         float row[4];
+        if (ROWS) row[0] = sc.row[quarter * 32 + lane] * sc.col[group];
         if (PROD == kGradW) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) row[j] = sc.row[quarter * 32 + (lane >> 2) + 8 * j];
@@ -395,8 +434,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
           for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
-              const uint32_t* v = &r[q & 1][y >> 1][4 * j + 2 * (y & 1)];
+              const uint32_t* v = ROWS ? &r[q & 1][y >> 1][8 * (y & 1) + 2 * j] : &r[q & 1][y >> 1][4 * j + 2 * (y & 1)];
               float2 d = make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]));
+              if (ROWS) {
+                acc[q][y][j] = fma_2(d, both(row[0]), acc[q][y][j]);
+                continue;
+              }
               if (PROD == kGradW) d = mul_2(d, both(row[y]));
               acc[q][y][j] = fma_2(d, s[q & 1][j], acc[q][y][j]);
             }
@@ -406,7 +449,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       }
       const int32_t row0 = x.a0 + int32_t(rank) * kHalf + quarter * 32;  // of D: this warp's 32
       const int32_t b_end = min(x.b_end, x.b0 + c1);                     // of this group
-      if (PROD != kGradW && p.splits > 1) {
+      if (!ROWS && PROD != kGradW && p.splits > 1) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -425,7 +468,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
       // while the next tile is summed
       const int er = (warp - kLoadWarps) * 32 + lane;  // 0 .. 255
       const int32_t cta0 = x.a0 + int32_t(rank) * kHalf;  // of D: this CTA's rows
-      if (PROD != kGradW) {
+      if (ROWS) {
+        bulk_wait_read0();
+        epilogue_barrier();
+        uint8_t* row = out_rows + (quarter * 32 + lane) * kRowPitch + c0 * 2;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float2(&v)[4] = acc[q][y];
+            *reinterpret_cast<uint4*>(row + (32 * q + 8 * y) * 2) =
+                make_uint4(bf16x2_of(v[0].x, v[0].y), bf16x2_of(v[1].x, v[1].y), bf16x2_of(v[2].x, v[2].y), bf16x2_of(v[3].x, v[3].y));
+          }
+        fence_proxy_async();
+        epilogue_barrier();
+        if (ok && er < kHalf && cta0 + er < x.a_end)
+          put_row(static_cast<uint16_t*>(p.out) + int64_t(cta0 + er) * p.ld_out + x.b0, out_rows + er * kRowPitch, (x.b_end - x.b0) * 2, 2);
+        bulk_commit();
+      } else if (PROD != kGradW) {
         bulk_wait_read0();
         epilogue_barrier();
 #pragma unroll
@@ -502,9 +562,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
 
 std::atomic<int> known8[64];  // pairs at once, alike for every product
 
-template <int PROD>
+template <int PROD, bool ROWS>
 cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
-  auto kern = linear8_kernel<PROD>;
+  auto kern = linear8_kernel<PROD, ROWS>;
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void*>(kern), kSmem8);
   if (e != cudaSuccess) return e;
@@ -547,6 +607,14 @@ TokenPlan8 plan8(const glu_block8_linear_args& a) {
   return a.grad ? token_plan8(a.M, a.K, a.N) : token_plan8(a.M, a.N, a.K);
 }
 
+// Whether the tokens are the rows of D: a thread then has one token, whose scale
+// and the weight's are one number per block.  From 128 tokens per W on: with 64 experts
+// x 2048 x 2048 64 rows each take 78 us this way and 76 the other, 128 rows 80 and 80,
+// 256 rows 109 and 117, 512 158 and 180; dense 7168 x 8192, 512 tokens 37 and 41.
+bool token_rows8(const glu_block8_linear_args& a, const TokenPlan8& plan) {
+  return plan.splits == 1 && a.M / (a.E > 0 ? a.E : 1) >= 128;
+}
+
 }  // namespace
 
 size_t linear8_workspace(const glu_block8_linear_args& a) {
@@ -581,7 +649,8 @@ cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, cons
   p.ld_sb = a.M;
   p.out = a.y;
   p.ld_out = a.ld_y;
-  e = grad ? launch8<kGradX>(p, s, d) : launch8<kForward>(p, s, d);
+  if (token_rows8(a, plan)) return grad ? launch8<kGradX, true>(p, s, d) : launch8<kForward, true>(p, s, d);
+  e = grad ? launch8<kGradX, false>(p, s, d) : launch8<kForward, false>(p, s, d);
   if (e != cudaSuccess || p.splits == 1) return e;
   glu_block_linear_fwd_args j = {};  // the join of a bf16 layer without bias, activation and residual
   j.act = GLU_ACT_IDENTITY;
@@ -615,7 +684,7 @@ cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s
   p.ld_out = a.ld_dw;
   p.stride_out = a.stride_dw;
   p.f32 = a.dw_fmt == GLU_FMT_FP32;
-  return launch8<kGradW>(p, s, d);
+  return launch8<kGradW, false>(p, s, d);
 }
 
 cudaError_t read_err_linear8(uint32_t* v, bool clear) {
