@@ -580,39 +580,36 @@ cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
   return launch_kernel(kern, 2 * pairs, kThreads8, kSmem8, s, p, true);
 }
 
-// How the tokens of a dense y or dx are cut into tiles (at most `most` each) and the
-// sum into parts, a function of the shape alone (76 pairs): the plan with the least
-// estimated time.  A block of the sum takes 0.4 us in a tile of 32 tokens and 0.55
-// in one of 256 (7168 x 8192 of 32 tokens 31 us, 4096 tokens 215), the busiest
-// pair's tiles follow each other, and the join of split sums reads and writes the
-// fp32 parts.
+// How the tokens of y or dx are cut into tiles: `rows`, as the rows of D, 256 at a
+// time, or as its columns, at most `most` at a time and the sum in parts; a function
+// of the shape alone (76 pairs).  As rows a thread has one token, whose scale and the
+// weight's are one number per block.  By expert from 128 tokens per W on: with 64
+// experts x 2048 x 2048 64 rows each take 78 us as rows and 76 as columns, 128 rows 80
+// and 80, 256 rows 109 and 117, 512 158 and 180.  Dense the plan with the least
+// estimated time: a block of the sum takes 0.42 us with the tokens as rows (7168 deep,
+// 4096 x 8192: 174 us), as columns 0.4 us for 32 of them and 0.55 for 256 (8192 deep,
+// 7168 wide: 31 us for 32 tokens; 4096 tokens 203), the busiest pair's tiles follow
+// each other, and the join of split sums reads and writes the fp32 parts.
 struct TokenPlan8 {
   int most, splits;
+  bool rows;
 };
 TokenPlan8 token_plan8(int64_t rows, int64_t width, int64_t depth) {
   const int64_t at = (width + kTile - 1) / kTile, blocks = blocks8(depth);
-  TokenPlan8 best = {kTile, 1};
-  double least = 1e30;
+  TokenPlan8 best = {kTile, 1, rows >= 128};
+  double least = best.rows ? double((at * ((rows + kTile - 1) / kTile) + 75) / 76) * (double(blocks) * 0.42 + 1.5) : 1e30;
   for (int n = 1; n <= 8 && blocks / n >= 4; ++n)
     for (int most = kTile; most >= 64; most -= kStep) {
       const int64_t bt = (rows + most - 1) / most, each = ((rows + bt - 1) / bt + kStep - 1) / kStep * kStep;
       double us = double((at * bt * n + 75) / 76) * (double((blocks + n - 1) / n) * (0.38 + 0.17 * double(each) / kTile) + 1.5);
       if (n > 1) us += 3.0 + double(n) * double(rows) * double(width) * 8e-6 / 4.0;
-      if (us < least * 0.98) least = us, best = {most, n};
+      if (us < least * 0.98) least = us, best = {most, n, false};
     }
   return best;
 }
 TokenPlan8 plan8(const glu_block8_linear_args& a) {
-  if (a.E > 0 || linear8_few(a)) return {kTile, 1};
+  if (a.E > 0 || linear8_few(a)) return {kTile, 1, a.M >= 128 * int64_t(a.E)};
   return a.grad ? token_plan8(a.M, a.K, a.N) : token_plan8(a.M, a.N, a.K);
-}
-
-// Whether the tokens are the rows of D: a thread then has one token, whose scale
-// and the weight's are one number per block.  From 128 tokens per W on: with 64 experts
-// x 2048 x 2048 64 rows each take 78 us this way and 76 the other, 128 rows 80 and 80,
-// 256 rows 109 and 117, 512 158 and 180; dense 7168 x 8192, 512 tokens 37 and 41.
-bool token_rows8(const glu_block8_linear_args& a, const TokenPlan8& plan) {
-  return plan.splits == 1 && a.M / (a.E > 0 ? a.E : 1) >= 128;
 }
 
 }  // namespace
@@ -649,7 +646,7 @@ cudaError_t launch_linear8(const glu_block8_linear_args& a, cudaStream_t s, cons
   p.ld_sb = a.M;
   p.out = a.y;
   p.ld_out = a.ld_y;
-  if (token_rows8(a, plan)) return grad ? launch8<kGradX, true>(p, s, d) : launch8<kForward, true>(p, s, d);
+  if (plan.rows) return grad ? launch8<kGradX, true>(p, s, d) : launch8<kForward, true>(p, s, d);
   e = grad ? launch8<kGradX, false>(p, s, d) : launch8<kForward, false>(p, s, d);
   if (e != cudaSuccess || p.splits == 1) return e;
   glu_block_linear_fwd_args j = {};  // the join of a bf16 layer without bias, activation and residual
