@@ -415,7 +415,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (q >= chunks) break;
-          tc::wait_ld();
+          tc::wait_ld(r[q & 1]);
           // the next chunk, of the next block behind the last one, is on its way
           // while this one is added
           if (q + 1 < chunks) {

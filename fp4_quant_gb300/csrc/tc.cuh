@@ -120,6 +120,19 @@ __device__ __forceinline__ void ld16x32(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// The same, tied to the registers that the loads fill, so that nothing that reads
+// them can be moved ahead of it.
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[2][16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0][0]), "+r"(r[0][1]), "+r"(r[0][2]), "+r"(r[0][3]), "+r"(r[0][4]),
+                 "+r"(r[0][5]), "+r"(r[0][6]), "+r"(r[0][7]), "+r"(r[0][8]), "+r"(r[0][9]), "+r"(r[0][10]),
+                 "+r"(r[0][11]), "+r"(r[0][12]), "+r"(r[0][13]), "+r"(r[0][14]), "+r"(r[0][15]), "+r"(r[1][0]),
+                 "+r"(r[1][1]), "+r"(r[1][2]), "+r"(r[1][3]), "+r"(r[1][4]), "+r"(r[1][5]), "+r"(r[1][6]),
+                 "+r"(r[1][7]), "+r"(r[1][8]), "+r"(r[1][9]), "+r"(r[1][10]), "+r"(r[1][11]), "+r"(r[1][12]),
+                 "+r"(r[1][13]), "+r"(r[1][14]), "+r"(r[1][15])
+               :
+               : "memory");
+}
 
 // ---- two CTAs of a cluster as a pair (cta_group::2) -----------------------
 // One MMA of 256 rows: each CTA holds 128 rows of A, half of B's columns and

@@ -73,7 +73,7 @@ def test_quant_weight_refusals(kw, status):
     assert _status("glu_block8_quant_weight", B.Quant8WeightArgs, WEIGHT, kw) == status
 
 
-LINEAR = dict(M=64, N=48, K=64, ld_x=64, ld_w=64, stride_w=3072 + 64, ld_y=64, xq=P, xs=P, wq=P, ws=P, y=P, workspace=P, workspace_bytes=1 << 40)
+LINEAR = dict(M=64, N=32, K=64, ld_x=64, ld_w=64, stride_w=2048 + 64, ld_y=64, xq=P, xs=P, wq=P, ws=P, y=P, workspace=P, workspace_bytes=1 << 40)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -81,7 +81,7 @@ LINEAR = dict(M=64, N=48, K=64, ld_x=64, ld_w=64, stride_w=3072 + 64, ld_y=64, x
     (dict(E=2), G.GLU_EINVAL), (dict(offsets=P), G.GLU_EINVAL), (dict(M=1 << 31), G.GLU_ESHAPE), (dict(N=(1 << 23) + 1), G.GLU_ESHAPE),
     (dict(ld_x=48), G.GLU_ESHAPE), (dict(grad=1, ld_y=56), G.GLU_ESHAPE), (dict(E=2, offsets=P, stride_w=1024), G.GLU_ESHAPE),
     (dict(ld_w=72), G.GLU_EALIGN), (dict(ld_y=68), G.GLU_EALIGN), (dict(xq=P + 8), G.GLU_EALIGN), (dict(ws=P + 4), G.GLU_EALIGN),
-    (dict(E=2, offsets=P, stride_w=3080), G.GLU_EALIGN)])
+    (dict(E=2, offsets=P, stride_w=2056), G.GLU_EALIGN)])
 def test_linear_refusals(kw, status):
     assert _status("glu_block8_linear", B.Linear8Args, LINEAR, kw) == status
 
@@ -102,7 +102,7 @@ def test_linear_workspace():
     assert _status("glu_block8_linear", B.Linear8Args, LINEAR, dict(M=200, **big, workspace=P + 8, workspace_bytes=n)) == G.GLU_EALIGN
 
 
-DW = dict(C=3, N=48, K=64, ld_dy=48, ld_x=64, ld_dw=64, stride_dw=3072, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2)
+DW = dict(C=3, N=32, K=64, ld_dy=32, ld_x=64, ld_dw=64, stride_dw=2048, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2)
 
 
 @pytest.mark.parametrize("kw,status", [
