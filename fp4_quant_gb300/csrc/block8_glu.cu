@@ -2,9 +2,9 @@
 // those (glu_block8.h).  Every operand is read and every result written once; 16
 // lanes share a row of 128 columns, eight each.  What binds is the issue of
 // instructions, at 55 to 65 % of its rate, not DRAM: 30 per value forward (4096 x
-// 7168 in 40 us, 5.1 TB/s), 50 for the bf16 backward of a ragged width (8191 x 1462
-// in 31 us, a fifth of it for dUp's rows, which begin inside 16 bytes), about 40 for
-// the quantised one (32768 x 1024 of 64 experts in 82 us).
+// 7168 in 40 us, 5.1 TB/s), about 40 for the quantised backward (32768 x 1024 of 64
+// experts in 82 us).  The bf16 one takes 31 us for 8191 x 1462, where dUp's rows
+// begin inside 16 bytes, and three quarters of that for a width of 1464.
 #include "block8_act.cuh"
 
 namespace gq {
@@ -116,56 +116,55 @@ __device__ __forceinline__ Grads glu_grads(const uint2& gq, float gs, const uint
   return o;
 }
 
-template <int FIRST>
-__device__ __forceinline__ void shifted(const uint32_t (&all)[8], bool odd, uint32_t (&w)[4]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = odd ? __funnelshift_r(all[FIRST + j], all[FIRST + j + 1], 16) : all[FIRST + j];
-}
-
 // A row's chunks of eight bf16, one per lane of 16 (`left` elements from the lane's
 // first on), to where the row begins `off` elements (1 .. 7) behind 16 bytes: a
 // lane stores the 16 bytes in which its chunk begins, with the last `off` elements
-// of the lane before it.  What fills no 16 bytes here goes element by element.
-// `row`: the lane's first element.  All 32 lanes take part.
-__device__ __forceinline__ void put_shifted(uint16_t* row, int off, int left, bool store, uint4 v, int c8) {
-  uint32_t all[8] = {0, 0, 0, 0, v.x, v.y, v.z, v.w};  // the lane before's, its own
-#pragma unroll
-  for (int j = 0; j < 4; ++j) all[j] = __shfl_up_sync(0xFFFFFFFFu, all[4 + j], 1, 16);
+// of the lane before it, from `buf` (the half-warp's own, four words ahead of the
+// row's 64).  What fills no 16 bytes here goes in words or elements.  `row`: the
+// lane's first element.  All 32 lanes take part.  WHOLE: the sixteen chunks are
+// all there.
+template <bool WHOLE>
+__device__ __forceinline__ void put_shifted(uint16_t* row, int off, int left, bool store, const uint4& v, int c8, uint32_t* buf) {
+  __syncwarp();
+  *reinterpret_cast<uint4*>(buf + 4 + 4 * c8) = v;
+  __syncwarp();
   if (!store) return;
-  const int n = min(left, 8);
+  const int n = WHOLE ? 8 : min(left, 8);
   const bool whole = c8 > 0 && n >= 8 - off;
-  // word j of the 16 bytes has elements 2 j - off and the next of its own, and `all`
-  // has element e in the half (e + 8) % 2 of word (e + 8) / 2
-  uint32_t w[4];
-  switch ((8 - off) >> 1) {
-    case 0: shifted<0>(all, off & 1, w); break;
-    case 1: shifted<1>(all, off & 1, w); break;
-    case 2: shifted<2>(all, off & 1, w); break;
-    default: shifted<3>(all, off & 1, w); break;
+  const uint32_t* from = buf + 4 + 4 * c8 - (off + 1) / 2;
+  uint32_t w[5];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) w[j] = from[j];
+  if (off & 1) {
+    w[4] = from[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
   }
   if (whole) stg_once(row - off, make_uint4(w[0], w[1], w[2], w[3]));
-  // the rest: the chunk's elements up to its 16 bytes' end, and those behind it where
-  // no lane follows, two at a time where the half begins on four bytes
-  const bool last = c8 == 15 || left <= 8;
-  if (whole && !last) return;
-  const int end = 8 - off, lo = whole ? end : c8 > 0 ? -off : 0, hi = last ? n : min(n, end);
-#pragma unroll
-  for (int e = -6; e < 8; e += 2) {
-    const uint32_t word = all[(e + 8) >> 1];
-    if (off % 2 == 0 && e >= lo && e + 1 < hi) {
-      *reinterpret_cast<uint32_t*>(row + e) = word;
-    } else {
-      if (e >= lo && e < hi) row[e] = uint16_t(word);
-      if (e + 1 >= lo && e + 1 < hi) row[e + 1] = uint16_t(word >> 16);
+  if (WHOLE && off % 2 == 0) {
+    // what is left of the first and of the last chunk, (8 - off) / 2 and off / 2 words
+    // of the same numbers 0 .. 3: lane c8 < 4 stores word c8
+    if (c8 < 4) {
+      const int at = c8 < (8 - off) / 2 ? c8 : 60 + c8;  // word of the row
+      *reinterpret_cast<uint32_t*>(row - 8 * c8 + 2 * at) = buf[4 + at];
     }
+    return;
   }
-  if (lo <= -7 && hi > -7) row[-7] = uint16_t(all[0] >> 16);
+  // the chunk's elements up to its 16 bytes' end where they were not stored, and
+  // those behind it where no lane follows
+  const int end = 8 - off;
+  const int lo = whole ? end : c8 > 0 ? -off : 0, hi = c8 == 15 || left <= 8 ? n : min(n, end);
+  const uint16_t* element = reinterpret_cast<const uint16_t*>(buf + 4 + 4 * c8);
+  for (int e = lo; e < hi; ++e) row[e] = element[e];
 }
 
 constexpr int kBwdRows = 4;
 
+// 64 words of dUp's chunks per half-warp, and four ahead of them.
+using ShiftBuf = uint32_t[2 * kGluWarps][4 + 64];
+
 template <int ACT, bool WHOLE>
-__device__ __forceinline__ void glu_bwd_tile(const GluBwdP& p, int32_t tile, int32_t kt) {
+__device__ __forceinline__ void glu_bwd_tile(const GluBwdP& p, ShiftBuf& buf, int32_t tile, int32_t kt) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.H - k;
   const int64_t row0 = (int64_t(tile) * kGluWarps + warp) * 2 * kBwdRows + (lane >> 4) * kBwdRows;
@@ -197,16 +196,17 @@ __device__ __forceinline__ void glu_bwd_tile(const GluBwdP& p, int32_t tile, int
       if (off == 0) put8(p.d + r * p.ld_d + p.H + k, left, du);
       if (p.h) put8(p.h + r * p.ld_h + k, left, packed(o.h));
     }
-    if (off != 0) put_shifted(p.d + r * p.ld_d + p.H + k, off, WHOLE ? p.H - k : left, store, du, c8);
+    if (off != 0) put_shifted<WHOLE>(p.d + r * p.ld_d + p.H + k, off, WHOLE ? p.H - k : left, store, du, c8, buf[2 * warp + (lane >> 4)]);
   }
 }
 
 template <int ACT>
 __global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __grid_constant__ GluBwdP p) {
+  __shared__ __align__(16) ShiftBuf buf;
   const int32_t tile = blockIdx.x / p.k_tiles, kt = blockIdx.x - tile * p.k_tiles;
   after_previous();
-  if ((kt + 1) * kBlock8 <= p.H) glu_bwd_tile<ACT, true>(p, tile, kt);
-  else glu_bwd_tile<ACT, false>(p, tile, kt);
+  if ((kt + 1) * kBlock8 <= p.H) glu_bwd_tile<ACT, true>(p, buf, tile, kt);
+  else glu_bwd_tile<ACT, false>(p, buf, tile, kt);
 }
 
 // Backward, quantised: blocks of 16 warps, one per SM, walk tiles of 128 rows by
