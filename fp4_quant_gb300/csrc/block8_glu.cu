@@ -244,23 +244,25 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
   auto rows_of = [&](int32_t w) { return row_tile(p.offsets ? sh.offsets : nullptr, p.E, p.M, w / p.k_tiles); };
   auto load = [&](int32_t w, const RowTile& t, TileIn& in) {
     const int32_t kt = w % p.k_tiles, k = kt * kBlock8, rows = t.r1 - t.r0;
-    // rows of no tile are not read (their first row's address stands in)
+    // a warp copies the eight rows that it will read; rows of no tile are not read
+    // (their first row's address stands in)
+    const int first = warp * 8;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int q = threadIdx.x + j * kThreads, r = q >> 4, c = (q & 15) * 8;
+      const int r = first + 2 * j + (lane >> 4), c = (lane & 15) * 8;
       copy16(&in.dh[r][c], p.dh + int64_t(r < rows ? t.r0 + r : 0) * p.ld_dh + k + c, r < rows ? 16u : 0u);
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int q = threadIdx.x + j * kThreads, r = q >> 3, c = (q & 7) * 16;
+      const int r = first + 4 * j + (lane >> 3), c = (lane & 7) * 16;
       const int64_t m = r < rows ? t.r0 + r : 0;
       copy16(&in.g[r][c], p.gq + m * p.ld_gq + k + c, r < rows ? 16u : 0u);
       copy16(&in.u[r][c], p.uq + m * p.ld_uq + k + c, r < rows ? 16u : 0u);
     }
-    if (threadIdx.x < 2 * kBlock8) {
-      const int r = threadIdx.x % kBlock8;
-      const float* s = (threadIdx.x < kBlock8 ? p.gs : p.us) + int64_t(kt) * p.M + (r < rows ? t.r0 + r : 0);
-      copy4(threadIdx.x < kBlock8 ? &in.gs[r] : &in.us[r], s, r < rows);
+    if (lane < 16) {
+      const int r = first + (lane & 7);
+      const float* s = (lane < 8 ? p.gs : p.us) + int64_t(kt) * p.M + (r < rows ? t.r0 + r : 0);
+      copy4(lane < 8 ? &in.gs[r] : &in.us[r], s, r < rows);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
     } else {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
     }
-    __syncthreads();
+    __syncwarp();  // the other lanes' copies
     const TileIn& in = sh.in[buf];
     const int32_t tile = w / p.k_tiles, kt = w - tile * p.k_tiles, k = kt * kBlock8 + c8 * 8, rows = t.r1 - t.r0 - row0;
     F8 v[3][kTileRows];
@@ -361,9 +363,8 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
 #pragma unroll
         for (int i = 0; i < kTileRows; ++i) put_bytes8(out + i * ld, 8, codes8<false>(v[x][i], r));
       }
-    } else {
-      __syncthreads();  // this tile's operands are read before the next but one's arrive
     }
+    __syncwarp();  // the warp has read its rows before those of the next tile but one arrive
     t = next;
   }
 }
