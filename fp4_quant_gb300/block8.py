@@ -139,8 +139,8 @@ def _experts(offsets, device):
 def _row_form(x, name):
     """(M, K, device) of a row form, its codes checked to be on the current device."""
     q = x["q"]
-    if q.dim() != 2:
-        raise ValueError(f"{name}['q'] must be a matrix")
+    if q is None or q.dim() != 2:
+        raise ValueError(f"{name} must have a row form, {name}['q'] a matrix")
     device = _device(q, f"{name}['q']")
     return q.shape[0], q.shape[1], device
 
@@ -255,8 +255,8 @@ def linear8_dw(dy8, x8, *, offsets=None, dtype=torch.bfloat16, out=None, stream=
     if stream is not None:
         return _on(stream, linear8_dw, dy8, x8, offsets=offsets, dtype=dtype, out=out)
     dyq, xq = dy8["qc"], x8["qc"]
-    if dyq.dim() != 2 or xq.dim() != 2 or dyq.shape[0] != xq.shape[0] or dyq.shape[0] % 128:
-        raise ValueError("dy8['qc'] and x8['qc'] must be matrices of the same number of rows, a multiple of 128")
+    if dyq is None or xq is None or dyq.dim() != 2 or xq.dim() != 2 or dyq.shape[0] != xq.shape[0] or dyq.shape[0] % 128:
+        raise ValueError("dy8 and x8 must have column forms: dy8['qc'] and x8['qc'] of the same number of rows, a multiple of 128")
     if dtype not in (_BF16, _F32):
         raise TypeError(f"dtype must be bfloat16 or float32, got {dtype}")
     device = _device(dyq, "dy8['qc']")

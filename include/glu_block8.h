@@ -26,8 +26,9 @@
  *   weights  w [N, K], or a stack of E: 128 x 128.  q as w, s [ceil(N / 128),
  *            ceil(K / 128)], or a stack of E.
  *
- * Code matrices have a row stride (ld, in bytes) that is a multiple of 16;
- * scales and offsets are contiguous.  offsets [E + 1]: device int32, from 0,
+ * Code matrices have a row stride (ld, in bytes) that is a multiple of 16, their
+ * base 16-byte aligned; scales and offsets are contiguous, their base 4-byte
+ * aligned (one matrix of a stack's serves).  offsets [E + 1]: device int32, from 0,
  * not falling, up to M; others are bounded (results are then undefined, no
  * access leaves the operands).  1 <= E <= 1024 by expert, E = 0 and offsets
  * NULL dense.  Outputs are fully overwritten up to the matrices' widths.

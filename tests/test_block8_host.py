@@ -56,7 +56,7 @@ QUANT = dict(M=300, K=64, ld_x=64, ld_xq=64, ld_q=64, ld_qc=64, x=P, q=P, s=P, q
     (dict(E=-1), G.GLU_EINVAL), (dict(E=4), G.GLU_EINVAL), (dict(offsets=P), G.GLU_EINVAL), (dict(E=4, offsets=P, qc=None, sc=None), G.GLU_EINVAL),
     (dict(E=1025, offsets=P), G.GLU_ESHAPE), (dict(M=1 << 31), G.GLU_ESHAPE), (dict(K=(1 << 23) + 1), G.GLU_ESHAPE), (dict(ld_q=32), G.GLU_ESHAPE),
     (dict(M=(1 << 31) - 1025, K=1 << 23, ld_x=1 << 23, ld_q=1 << 23, ld_qc=1 << 23), G.GLU_ESHAPE),
-    (dict(ld_qc=72), G.GLU_EALIGN), (dict(ld_x=68), G.GLU_EALIGN), (dict(x=P + 8), G.GLU_EALIGN), (dict(sc=P + 4), G.GLU_EALIGN)])
+    (dict(ld_qc=72), G.GLU_EALIGN), (dict(ld_x=68), G.GLU_EALIGN), (dict(x=P + 8), G.GLU_EALIGN), (dict(sc=P + 2), G.GLU_EALIGN)])
 def test_quant_refusals(kw, status):
     assert _status("glu_block8_quant", B.Quant8Args, QUANT, kw) == status
 
@@ -80,7 +80,7 @@ LINEAR = dict(M=64, N=32, K=64, ld_x=64, ld_w=64, stride_w=2048 + 64, ld_y=64, x
     (dict(M=0), G.GLU_EINVAL), (dict(grad=2), G.GLU_EINVAL), (dict(xs=None), G.GLU_EINVAL), (dict(ws=None), G.GLU_EINVAL), (dict(y=None), G.GLU_EINVAL),
     (dict(E=2), G.GLU_EINVAL), (dict(offsets=P), G.GLU_EINVAL), (dict(M=1 << 31), G.GLU_ESHAPE), (dict(N=(1 << 23) + 1), G.GLU_ESHAPE),
     (dict(ld_x=48), G.GLU_ESHAPE), (dict(grad=1, ld_y=56), G.GLU_ESHAPE), (dict(E=2, offsets=P, stride_w=1024), G.GLU_ESHAPE),
-    (dict(ld_w=72), G.GLU_EALIGN), (dict(ld_y=68), G.GLU_EALIGN), (dict(xq=P + 8), G.GLU_EALIGN), (dict(ws=P + 4), G.GLU_EALIGN),
+    (dict(ld_w=72), G.GLU_EALIGN), (dict(ld_y=68), G.GLU_EALIGN), (dict(xq=P + 8), G.GLU_EALIGN), (dict(ws=P + 2), G.GLU_EALIGN),
     (dict(E=2, offsets=P, stride_w=2056), G.GLU_EALIGN)])
 def test_linear_refusals(kw, status):
     assert _status("glu_block8_linear", B.Linear8Args, LINEAR, kw) == status
@@ -108,7 +108,7 @@ DW = dict(C=3, N=32, K=64, ld_dy=32, ld_x=64, ld_dw=64, stride_dw=2048, dyq=P, d
 @pytest.mark.parametrize("kw,status", [
     (dict(C=0), G.GLU_EINVAL), (dict(dw_fmt=0), G.GLU_EINVAL), (dict(dys=None), G.GLU_EINVAL), (dict(dw=None), G.GLU_EINVAL),
     (dict(E=2), G.GLU_EINVAL), (dict(E=4, offsets=P), G.GLU_EINVAL), (dict(C=1 << 24), G.GLU_ESHAPE), (dict(ld_dw=56), G.GLU_ESHAPE),
-    (dict(E=2, offsets=P, stride_dw=1024), G.GLU_ESHAPE), (dict(ld_dy=56), G.GLU_EALIGN), (dict(ld_dw=68), G.GLU_EALIGN), (dict(xs=P + 4), G.GLU_EALIGN)])
+    (dict(E=2, offsets=P, stride_dw=1024), G.GLU_ESHAPE), (dict(ld_dy=56), G.GLU_EALIGN), (dict(ld_dw=68), G.GLU_EALIGN), (dict(xs=P + 2), G.GLU_EALIGN)])
 def test_linear_dw_refusals(kw, status):
     assert _status("glu_block8_linear_dw", B.Linear8DwArgs, DW, kw) == status
 
@@ -120,7 +120,7 @@ GLU = dict(M=64, H=48, ld_gate=48, ld_up=48, ld_h=48, ld_hq=48, ld_gq=48, ld_uq=
     (dict(act=5), G.GLU_EINVAL), (dict(act=16), G.GLU_EINVAL), (dict(M=0), G.GLU_EINVAL), (dict(gate=None), G.GLU_EINVAL), (dict(us=None), G.GLU_EINVAL),
     (dict(h=P), G.GLU_EINVAL), (dict(hq=None), G.GLU_EINVAL), (dict(hs=None), G.GLU_EINVAL), (dict(reserved=1), G.GLU_EINVAL),
     (dict(H=(1 << 23) + 1), G.GLU_ESHAPE), (dict(ld_up=40), G.GLU_ESHAPE), (dict(ld_gq=56), G.GLU_EALIGN), (dict(ld_gate=52), G.GLU_EALIGN),
-    (dict(gs=P + 4), G.GLU_EALIGN)])
+    (dict(gs=P + 2), G.GLU_EALIGN)])
 def test_glu_refusals(kw, status):
     assert _status("glu_block8_glu", B.Glu8Args, GLU, kw) == status
 
@@ -134,7 +134,7 @@ PLAIN, QUANTISED = dict(d=P, h=P), dict(dq=P, ds=P, dqc=P, dsc=P, hqc=P, hsc=P)
     (dict(**PLAIN, E=1, offsets=P), G.GLU_EINVAL), (dict(**{**QUANTISED, "ds": None}), G.GLU_EINVAL), (dict(**{**QUANTISED, "hsc": None}), G.GLU_EINVAL),
     (dict(**QUANTISED, h=P), G.GLU_EINVAL), (dict(**QUANTISED, E=3), G.GLU_EINVAL), (dict(**QUANTISED, H=64), G.GLU_ESHAPE),
     (dict(**PLAIN, H=(1 << 22) + 128), G.GLU_ESHAPE), (dict(**PLAIN, ld_d=248), G.GLU_ESHAPE), (dict(**QUANTISED, ld_hqc=112), G.GLU_ESHAPE),
-    (dict(**QUANTISED, ld_dq=264), G.GLU_EALIGN), (dict(**PLAIN, ld_dh=132), G.GLU_EALIGN), (dict(**{**QUANTISED, "dsc": P + 4}), G.GLU_EALIGN)])
+    (dict(**QUANTISED, ld_dq=264), G.GLU_EALIGN), (dict(**PLAIN, ld_dh=132), G.GLU_EALIGN), (dict(**{**QUANTISED, "dsc": P + 2}), G.GLU_EALIGN)])
 def test_glu_bwd_refusals(kw, status):
     assert _status("glu_block8_glu_bwd", B.Glu8BwdArgs, GLU_BWD, kw) == status
 
@@ -177,5 +177,9 @@ def test_binding_refuses_on_the_cpu():
         G.linear8(row, {"q": torch.zeros(2, 4, 16, dtype=torch.float8_e4m3fn), "s": torch.ones(2, 1, 1)})
     with pytest.raises(TypeError, match="dtype"):
         G.linear8_dw({"qc": torch.zeros(128, 16)}, {"qc": torch.zeros(128, 16)}, dtype=torch.float16)
+    with pytest.raises(ValueError, match="row form"):
+        G.linear8({"q": None, "s": None}, row)
+    with pytest.raises(ValueError, match="column forms"):
+        G.linear8_dw({"qc": None, "sc": None}, {"qc": None, "sc": None})
     with pytest.raises(ValueError, match="128"):
         G.linear8_dw({"qc": torch.zeros(100, 16)}, {"qc": torch.zeros(100, 16)})

@@ -68,6 +68,7 @@ def _calls(seed):
     x, dy = _rand(210, 256, seed=seed), _rand(210, 128, seed=seed + 1)
     w = G.quant8_weight(_rand(4, 128, 256, seed=seed + 2, scale=0.1))
     gate, up, dh = (_rand(210, 256, seed=seed + 3 + i) for i in range(3))
+    deep, deep_w = G.quant8(_rand(64, 4096, seed=seed + 6)), G.quant8_weight(_rand(264, 4096, seed=seed + 7, scale=0.1))  # a sum in parts
 
     def run():
         x8 = G.quant8(x, cols=True, offsets=off)
@@ -79,7 +80,7 @@ def _calls(seed):
         few = {"q": x8["q"][:1], "s": x8["s"][:, :1].contiguous()}
         one = {"q": w["q"][0], "s": w["s"][0]}
         return [x8["q"], x8["s"], x8["qc"], x8["sc"], k["qc"], k["sc"], G.linear8(x8, w, offsets=off), G.linear8_dx(d8, w, offsets=off),
-                G.linear8_dw(d8, x8, offsets=off), G.linear8_dw(d8, x8, offsets=off, dtype=torch.float32), G.linear8(few, one), G.linear8(x8, one),
+                G.linear8_dw(d8, x8, offsets=off), G.linear8_dw(d8, x8, offsets=off, dtype=torch.float32), G.linear8(few, one), G.linear8(x8, one), G.linear8(deep, deep_w),
                 a["h"]["q"], a["h"]["s"], a["gate"]["q"], a["up"]["s"], *b["d"].values(), *b["h"].values(), p["d"], p["h"],
                 w["q"], w["s"]]
     return run
@@ -233,3 +234,23 @@ def test_offsets_out_of_range_stay_inside():
         G.glu8_bwd(g["gate"], g["up"], x, quant=True, offsets=off)
     torch.cuda.synchronize()
     assert torch.equal(G.linear8(a, w, offsets=good), G.linear8(a, w, offsets=wild))
+
+
+def test_one_expert_of_a_stack():
+    """Matrices and scales out of a stack's, whose scales begin at any word."""
+    w = G.quant8_weight(_rand(3, 300, 136, seed=40))  # 3 x 2 scales each
+    x = G.quant8(_rand(1, 136, seed=41))
+    many = G.quant8(_rand(151, 136, seed=42), cols=True)
+    for e in range(3):
+        one = {"q": w["q"][e], "s": w["s"][e]}
+        q = torch.zeros(300, 144, dtype=torch.uint8, device=DEV)[:, :136]
+        own = {"q": q.copy_(w["q"][e].view(torch.uint8)).view(F8), "s": w["s"][e].clone()}
+        assert torch.equal(G.linear8(x, one), G.linear8(x, own)) and torch.equal(G.linear8(many, one), G.linear8(many, own))
+    # one block of a row form's columns, one block of a column form's rows
+    part = {"q": many["q"][:, 128:], "s": many["s"][1:]}
+    whole = torch.zeros(151, 16, dtype=torch.uint8, device=DEV)[:, :8].copy_(part["q"].view(torch.uint8))
+    a, b = G.quant8(part, rows=False, cols=True), G.quant8({"q": whole.view(F8), "s": many["s"][1:].clone()}, rows=False, cols=True)
+    assert _equal([a["qc"], a["sc"]], [b["qc"], b["sc"]])
+    d = {"qc": many["qc"][128:], "sc": many["sc"][1:]}
+    own = {"qc": d["qc"], "sc": d["sc"].clone()}
+    assert torch.equal(G.linear8_dw(d, d), G.linear8_dw(own, own))
