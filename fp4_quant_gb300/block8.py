@@ -52,7 +52,8 @@ class Linear8Args(ctypes.Structure):
 
 class Linear8DwArgs(ctypes.Structure):
     """Mirror of ``glu_block8_linear_dw_args``."""
-    _fields_ = _fields("C N K ld_dy ld_x ld_dw stride_dw", "dyq dys xq xs offsets dw", [("E", _i32), ("dw_fmt", _i32)])
+    _fields_ = _fields("C N K ld_dy ld_x ld_dw stride_dw", "dyq dys xq xs offsets dw workspace",
+                       [("workspace_bytes", _size), ("E", _i32), ("dw_fmt", _i32)])
 
 
 class Glu8Args(ctypes.Structure):
@@ -70,6 +71,7 @@ _SIGNATURES = {
     "glu_block8_quant": [ctypes.POINTER(Quant8Args), _ptr], "glu_block8_quant_weight": [ctypes.POINTER(Quant8WeightArgs), _ptr],
     "glu_block8_linear": [ctypes.POINTER(Linear8Args), _ptr], "glu_block8_linear_dw": [ctypes.POINTER(Linear8DwArgs), _ptr],
     "glu_block8_linear_workspace": [ctypes.POINTER(Linear8Args), ctypes.POINTER(_size)],
+    "glu_block8_linear_dw_workspace": [ctypes.POINTER(Linear8DwArgs), ctypes.POINTER(_size)],
     "glu_block8_glu": [ctypes.POINTER(Glu8Args), _ptr], "glu_block8_glu_bwd": [ctypes.POINTER(Glu8BwdArgs), _ptr],
     "glu_block8_abi_version": [],
 }
@@ -266,8 +268,12 @@ def linear8_dw(dy8, x8, *, offsets=None, dtype=torch.bfloat16, out=None, stream=
     dys, xs = _scales(dy8["sc"], "dy8['sc']", (C, N), device), _scales(x8["sc"], "x8['sc']", (C, K), device)
     dw = _result(None if out is None else {"out": out}, "out", (E, N, K) if E else (N, K), dtype, device)
     ld = _ld(dw)
-    a = Linear8DwArgs(C, N, K, ld_dy, ld_x, ld, _stack(dw, E, N, ld), dyq.data_ptr(), dys, xq.data_ptr(), xs, off, dw.data_ptr(), E,
-                      FMT_FP32 if dtype is _F32 else FMT_BF16)
+    a = Linear8DwArgs(C, N, K, ld_dy, ld_x, ld, _stack(dw, E, N, ld), dyq.data_ptr(), dys, xq.data_ptr(), xs, off, dw.data_ptr(), None, 0,
+                      E, FMT_FP32 if dtype is _F32 else FMT_BF16)
+    n = _size(0)
+    _call("glu_block8_linear_dw_workspace", a, n)
+    ws = _scratch(n.value)
+    a.workspace, a.workspace_bytes = _p(ws), n.value
     _call("glu_block8_linear_dw", a, _handle(device))
     return dw
 

@@ -30,6 +30,7 @@ bool linear8_few(const glu_block8_linear_args& a);
 cudaError_t launch_linear8_few(const glu_block8_linear_args& a, cudaStream_t s);
 size_t linear8_workspace(const glu_block8_linear_args& a);
 cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s, const DevInfo& d);
+size_t linear8_dw_workspace(const glu_block8_linear_dw_args& a);
 cudaError_t read_err_linear8(uint32_t* v, bool clear);
 
 }  // namespace gq

@@ -109,12 +109,15 @@ int check_linear(const glu_block8_linear_args* a, bool query) {
   return c.status;
 }
 
-int check_linear_dw(const glu_block8_linear_dw_args* a) {
+int check_linear_dw(const glu_block8_linear_dw_args* a, bool query) {
   if (a == nullptr || (a->dw_fmt != GLU_FMT_BF16 && a->dw_fmt != GLU_FMT_FP32) || a->C <= 0) return GLU_EINVAL;
   int st = check_weight_size(a->N, a->K, a->E);
   if (st != GLU_OK) return st;
   if (a->C > kMostRows / gq::kBlock8) return GLU_ESHAPE;
+  if (query) return a->C < a->E ? GLU_EINVAL : GLU_OK;
   if (!a->dyq || !a->dys || !a->xq || !a->xs || !a->dw || (a->offsets != nullptr) != (a->E > 0) || a->C < a->E) return GLU_EINVAL;
+  const size_t need = gq::linear8_dw_workspace(*a);
+  if (need > 0 && (a->workspace == nullptr || a->workspace_bytes < need)) return GLU_EINVAL;
   const int64_t rows = a->C * gq::kBlock8;
   const int size = a->dw_fmt == GLU_FMT_FP32 ? 4 : 2;
   Check c;
@@ -122,6 +125,7 @@ int check_linear_dw(const glu_block8_linear_dw_args* a) {
   c.matrix(a->xq, rows, a->K, a->ld_x, 1);
   c.stack(a->dw, a->E, a->N, a->K, a->ld_dw, a->stride_dw, size);
   for (const void* p : {static_cast<const void*>(a->dys), static_cast<const void*>(a->xs), static_cast<const void*>(a->offsets)}) c.words(p);
+  if (need > 0 && !aligned16(a->workspace)) c.fail(GLU_EALIGN);
   return c.status;
 }
 
@@ -188,7 +192,7 @@ extern "C" int glu_block8_linear(const glu_block8_linear_args* a, void* stream) 
   GQ_ENTRY(check_linear(a, false), gq::launch_linear8(*a, s, d));
 }
 extern "C" int glu_block8_linear_dw(const glu_block8_linear_dw_args* a, void* stream) {
-  GQ_ENTRY(check_linear_dw(a), gq::launch_linear8_dw(*a, s, d));
+  GQ_ENTRY(check_linear_dw(a, false), gq::launch_linear8_dw(*a, s, d));
 }
 extern "C" int glu_block8_glu(const glu_block8_glu_args* a, void* stream) { GQ_ENTRY(check_glu(a), gq::launch_glu8(*a, s)); }
 extern "C" int glu_block8_glu_bwd(const glu_block8_glu_bwd_args* a, void* stream) {
@@ -198,6 +202,12 @@ extern "C" int glu_block8_linear_workspace(const glu_block8_linear_args* a, size
   if (bytes == nullptr) return GLU_EINVAL;
   const int st = check_linear(a, true);
   if (st == GLU_OK) *bytes = gq::linear8_workspace(*a);
+  return st;
+}
+extern "C" int glu_block8_linear_dw_workspace(const glu_block8_linear_dw_args* a, size_t* bytes) {
+  if (bytes == nullptr) return GLU_EINVAL;
+  const int st = check_linear_dw(a, true);
+  if (st == GLU_OK) *bytes = gq::linear8_dw_workspace(*a);
   return st;
 }
 extern "C" int glu_block8_abi_version(void) { return GLU_BLOCK8_ABI_VERSION; }

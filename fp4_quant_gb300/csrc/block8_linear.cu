@@ -115,11 +115,19 @@ struct Tile8 : Tile {
 template <int PROD, bool ROWS>
 __device__ __forceinline__ Tile8 tile8_at(const Linear8P& p, const TilePlan& plan, int32_t t) {
   Tile8 x;
-  static_cast<Tile&>(x) = tile_at<PROD, kBK8>(p, plan, t);
+  const bool parts = PROD == kGradW && p.splits > 1;
+  const int32_t whole = parts ? t / p.splits : t, split = t - whole * p.splits;
+  static_cast<Tile&>(x) = tile_at<PROD, kBK8>(p, plan, whole);
   if (PROD == kGradW && p.offsets) {
     const int32_t rows = x.k_end - x.k0;
     x.k0 = (x.k0 / kBK8 + x.e) * kBK8;
     x.k_end = x.k0 + (rows + kBK8 - 1) / kBK8 * kBK8;
+  }
+  if (parts) {  // whole blocks, as equal as they go (at most 2^24 of them, and 16 parts)
+    const int32_t blocks = (x.k_end - x.k0) / kBK8, first = x.k0 / kBK8;
+    x.split = split;
+    x.k0 = (first + blocks * split / p.splits) * kBK8;
+    x.k_end = (first + blocks * (split + 1) / p.splits) * kBK8;
   }
   x.a_end = p.width;
   if (ROWS) {
@@ -202,7 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
   cluster_sync();
   tc::fence_after();
   const uint32_t tmem = ctl->tmem;
-  const int32_t tiles = ctl->plan.first[p.offsets ? p.E : 1];
+  const int32_t tiles = ctl->plan.first[p.offsets ? p.E : 1] * (PROD == kGradW ? p.splits : 1);
 
   if (warp < kLoadWarps) {
     fewer_regs<kFewRegs>();
@@ -506,7 +514,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads8, 1) linear
           put_row(static_cast<uint16_t*>(p.out) + int64_t(x.b0 + er) * p.ld_out + cta0, out_rows + er * kTokenPitch, left * 2, 2);
         bulk_commit();
       } else {
-        const int64_t base = x.e * p.stride_out + int64_t(cta0) * p.ld_out + x.b0;
+        // the parts of a split sum follow each other
+        const int64_t base = (int64_t(x.split) * p.E + x.e) * p.stride_out + int64_t(cta0) * p.ld_out + x.b0;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // fp32: the columns of either group in turn
           if (!p.f32 && h == 1) break;
@@ -571,7 +580,7 @@ cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
   p.n_at = (p.width + kTile - 1) / kTile;
   // by expert the device counts the tiles: no more than one token tile per
   // expert above the dense count
-  const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E
+  const int64_t most = PROD == kGradW ? int64_t(p.n_at) * ((p.cols + kTile - 1) / kTile) * p.E * p.splits
                                       : p.n_at * ((int64_t(p.rows) + p.most - 1) / p.most + (p.offsets ? p.E : 0)) * p.splits;
   int pairs = 0;
   e = pairs_at_once(known8, reinterpret_cast<const void*>(kern), kThreads8, kSmem8, d, &pairs);
@@ -612,7 +621,61 @@ TokenPlan8 plan8(const glu_block8_linear_args& a) {
   return a.grad ? token_plan8(a.M, a.K, a.N) : token_plan8(a.M, a.N, a.K);
 }
 
+// dw from the fp32 parts of split sums, added in order: a thread has eight columns of
+// a row.
+struct JoinDwP {
+  const float* part;  // [splits, E N, ld_part]
+  void* dw;
+  int64_t ld_part, ld_dw, stride_dw, rows;
+  int32_t N, K, splits, f32;
+};
+__global__ void __launch_bounds__(256) join_dw8_kernel(const __grid_constant__ JoinDwP p) {
+  const int64_t chunks = (p.K + 7) / 8, q = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  after_previous();
+  if (q >= p.rows * chunks) return;
+  const int64_t row = q / chunks, e = row / p.N;
+  const int32_t c = int32_t(q - row * chunks) * 8;
+  float v[8] = {};
+  for (int i = 0; i < p.splits; ++i) {  // the parts' rows are whole chunks; what lies past K in them is not stored
+    const float4* f = reinterpret_cast<const float4*>(p.part + (i * p.rows + row) * p.ld_part + c);
+    const float4 a = f[0], b = f[1];
+    v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w, v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+  }
+  const int64_t at = e * p.stride_dw + (row - e * p.N) * p.ld_dw + c;
+  const int32_t left = p.K - c;
+  if (!p.f32) {
+    store8(static_cast<uint16_t*>(p.dw) + at, left, v);
+  } else {
+    float* o = static_cast<float*>(p.dw) + at;  // rows begin on 16 bytes
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) o[i] = v[i];
+  }
+}
+int64_t part_ld8(int64_t K) { return (K + 7) / 8 * 8; }
+
+// Parts of a dw's token sum, where its tiles are fewer than the 76 pairs: the number
+// with the least estimated time.  A block of the sum takes 0.67 us, a tile's results 2,
+// the join reads and writes the parts (64 MB at most).
+int dw_splits8(const glu_block8_linear_dw_args& a) {
+  const int64_t E = a.E > 0 ? a.E : 1, tiles = (a.N + kTile - 1) / kTile * ((a.K + kTile - 1) / kTile) * E;
+  const int64_t blocks = (a.C - (a.E > 0 ? E : 0)) / E + 1, size = E * a.N * part_ld8(a.K) * 4;
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= 16 && (n == 1 || (blocks / n >= 2 && n * size <= (int64_t(64) << 20))); ++n) {
+    double us = double((tiles * n + 75) / 76) * (double((blocks + n - 1) / n) * 0.67 + 2.0);
+    if (n > 1) us += 3.0 + double(n) * double(size) * 2e-6 / 4.0;
+    if (us < least * 0.95) least = us, best = n;
+  }
+  return best;
+}
+
 }  // namespace
+
+size_t linear8_dw_workspace(const glu_block8_linear_dw_args& a) {
+  const int n = dw_splits8(a);
+  return n > 1 ? size_t(n) * size_t(a.E > 0 ? a.E : 1) * size_t(a.N) * size_t(part_ld8(a.K)) * 4 : 0;
+}
 
 size_t linear8_workspace(const glu_block8_linear_args& a) {
   const int splits = plan8(a).splits;
@@ -673,15 +736,33 @@ cudaError_t launch_linear8_dw(const glu_block8_linear_dw_args& a, cudaStream_t s
   p.width = int32_t(a.N);
   p.cols = int32_t(a.K);
   p.most = kTile;
-  p.splits = 1;
+  p.splits = dw_splits8(a);
   p.sa = a.dys;
   p.sb = a.xs;
   p.ld_sb = a.K;
   p.out = a.dw;
   p.ld_out = a.ld_dw;
-  p.stride_out = a.stride_dw;
+  p.stride_out = a.E > 0 ? a.stride_dw : 0;
   p.f32 = a.dw_fmt == GLU_FMT_FP32;
-  return launch8<kGradW, false>(p, s, d);
+  if (p.splits == 1) return launch8<kGradW, false>(p, s, d);
+  JoinDwP j;
+  j.part = static_cast<const float*>(a.workspace);
+  j.dw = a.dw;
+  j.ld_part = part_ld8(a.K);
+  j.ld_dw = a.ld_dw;
+  j.stride_dw = p.stride_out;
+  j.rows = int64_t(p.E) * a.N;
+  j.N = p.width;
+  j.K = p.cols;
+  j.splits = p.splits;
+  j.f32 = p.f32;
+  p.out = a.workspace;
+  p.ld_out = j.ld_part;
+  p.stride_out = a.N * j.ld_part;
+  p.f32 = 1;
+  e = launch8<kGradW, false>(p, s, d);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(join_dw8_kernel, unsigned((j.rows * ((a.K + 7) / 8) + 255) / 256), 256, 0, s, j, true);
 }
 
 cudaError_t read_err_linear8(uint32_t* v, bool clear) {

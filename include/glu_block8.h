@@ -102,7 +102,8 @@ typedef struct glu_block8_linear_args {
 
 /* dw = dy^T x ([N, K], or by expert [E, N, K]; bf16 or fp32, dw_fmt), dy [.., N]
  * and x [.., K] in column form of C blocks, with the same experts.  Experts
- * without rows get 0. */
+ * without rows get 0.  The workspace (16-byte aligned; NULL where the query says
+ * 0) joins the parts of sums that are split where N and K are small. */
 typedef struct glu_block8_linear_dw_args {
   int64_t C, N, K;
   int64_t ld_dy, ld_x, ld_dw, stride_dw;
@@ -112,6 +113,8 @@ typedef struct glu_block8_linear_dw_args {
   const float* xs;
   const int32_t* offsets;
   void* dw;
+  void* workspace;
+  size_t workspace_bytes;
   int32_t E;
   int32_t dw_fmt; /* GLU_FMT_BF16 or GLU_FMT_FP32 */
 } glu_block8_linear_dw_args;
@@ -119,6 +122,7 @@ typedef struct glu_block8_linear_dw_args {
 GLU_API int glu_block8_linear(const glu_block8_linear_args* args, void* stream);
 GLU_API int glu_block8_linear_workspace(const glu_block8_linear_args* args, size_t* bytes);
 GLU_API int glu_block8_linear_dw(const glu_block8_linear_dw_args* args, void* stream);
+GLU_API int glu_block8_linear_dw_workspace(const glu_block8_linear_dw_args* args, size_t* bytes);
 
 /* ---- glu8 --------------------------------------------------------------
  * h = act(gate) .* up from gate, up bf16 [M, H], as bf16 (h) or in row form

@@ -102,7 +102,22 @@ def test_linear_workspace():
     assert _status("glu_block8_linear", B.Linear8Args, LINEAR, dict(M=200, **big, workspace=P + 8, workspace_bytes=n)) == G.GLU_EALIGN
 
 
-DW = dict(C=3, N=32, K=64, ld_dy=32, ld_x=64, ld_dw=64, stride_dw=2048, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2)
+DW = dict(C=3, N=32, K=64, ld_dy=32, ld_x=64, ld_dw=64, stride_dw=2048, dyq=P, dys=P, xq=P, xs=P, dw=P, dw_fmt=2, workspace=P, workspace_bytes=1 << 40)
+
+
+def test_linear_dw_workspace():
+    """Parts of split sums where the tiles are few and the sum is long."""
+    def need(**kw):
+        n = ctypes.c_size_t(99)
+        assert B._func("glu_block8_linear_dw_workspace")(ctypes.byref(B.Linear8DwArgs(**{**DW, **kw})), ctypes.byref(n)) == G.GLU_OK
+        return n.value
+    few = dict(C=32, N=1024, K=1023, ld_dy=1024, ld_x=1024, ld_dw=1024)
+    n = need(**few)
+    assert n > 0 and n % (1024 * 1024 * 4) == 0 and need(**{**few, "dw_fmt": 3}) == n
+    assert need(**{**few, "C": 3}) == 0 and need(C=32, N=8192, K=8192) == 0 and need(C=300, N=2048, K=2048, E=64) == 0
+    assert need(C=260, N=300, K=300, E=4) % (4 * 300 * 304 * 4) == 0 and need(C=260, N=300, K=300, E=4) > 0
+    for kw, status in [(dict(workspace=None), G.GLU_EINVAL), (dict(workspace_bytes=n - 1), G.GLU_EINVAL), (dict(workspace=P + 8), G.GLU_EALIGN)]:
+        assert _status("glu_block8_linear_dw", B.Linear8DwArgs, DW, {**few, **kw}) == status
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -141,8 +156,9 @@ def test_glu_bwd_refusals(kw, status):
 
 def test_null_arguments():
     for name in B._SIGNATURES:
-        if name == "glu_block8_linear_workspace":
-            assert B._func(name)(ctypes.byref(B.Linear8Args(**LINEAR)), None) == G.GLU_EINVAL
+        if name.endswith("_workspace"):
+            a = B.Linear8DwArgs(**DW) if "dw" in name else B.Linear8Args(**LINEAR)
+            assert B._func(name)(ctypes.byref(a), None) == G.GLU_EINVAL
         elif name != "glu_block8_abi_version":
             assert B._func(name)(None, None) == G.GLU_EINVAL
 

@@ -345,6 +345,16 @@ def test_weight_gradients(M, N, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,N,K,E,spare,empty", [(4096, 256, 256, 0, 0, ()), (3000, 300, 513, 0, 0, ()), (2050, 17, 1000, 0, 0, ()),
+                                                 (6000, 260, 200, 3, 100, (1,)), (5000, 128, 384, 2, 0, ())])
+def test_weight_gradients_in_parts(M, N, K, E, spare, empty, dtype):
+    """Long sums of few tiles, cut into parts (more of them than an expert has blocks) and joined."""
+    off = _offsets(M, E, M, spare, empty) if E else None
+    dy, x = (G.quant8(_x(M, n, M + n), rows=False, cols=True, offsets=off) for n in (N, K))
+    _check_dw(G.linear8_dw(dy, x, offsets=off, dtype=dtype), dy, x, off, E)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,N,K,E,spare,empty", EXPERTS)
 def test_weight_gradients_by_expert(M, N, K, E, spare, empty, dtype):
     off = _offsets(M, E, M, spare, empty)
