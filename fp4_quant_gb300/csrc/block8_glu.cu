@@ -3,7 +3,7 @@
 // lanes share a row of 128 columns, eight each.  What binds is the issue of
 // instructions, at 55 to 65 % of its rate, not DRAM: 30 per value forward (4096 x
 // 7168 in 40 us, 5.1 TB/s), about 40 for the quantised backward (32768 x 1024 of 64
-// experts in 82 us).  The bf16 one takes 31 us for 8191 x 1462, where dUp's rows
+// experts in 81 us).  The bf16 one takes 28 us for 8191 x 1462, where dUp's rows
 // begin inside 16 bytes, and three quarters of that for a width of 1464.
 #include "block8_act.cuh"
 
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kGluWarps * 32, 3) glu8_bwd_kernel(const __gri
 // of its 32 elements in registers while the maxima of rows and columns are found;
 // the next tile's operands are on their way into shared memory meanwhile (a block
 // per tile: 113 us for 32768 x 1024, this way 94, with cheaper activations and
-// scales 82).
+// scales 81).
 constexpr int kTileWarps = 16, kTileRows = 4;
 
 struct TileIn {
