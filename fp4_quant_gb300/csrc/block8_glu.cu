@@ -28,6 +28,7 @@ constexpr int kFwdRows = 2;
 // WHOLE (here and below): the strip's 128 columns are all there.
 template <int ACT, bool H8, bool WHOLE>
 __device__ __forceinline__ void glu_tile(const GluP& p, int32_t tile, int32_t kt) {
+  constexpr bool kExact = ACT == GLU_ACT_RELU || ACT == GLU_ACT_IDENTITY;  // h is a product of two bf16, not rounded
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane & 15;
   const int32_t k = kt * kBlock8 + c8 * 8, left = WHOLE ? 8 : p.H - k;
   const int64_t row0 = (int64_t(tile) * kGluWarps + warp) * 2 * kFwdRows + (lane >> 4) * kFwdRows;
@@ -59,20 +60,22 @@ __device__ __forceinline__ void glu_tile(const GluP& p, int32_t tile, int32_t kt
     m[4 * i + 2] = H8 ? amax8(h[i]) : 0.0f;
     m[4 * i + 3] = 0.0f;
   }
-  const Fit8 f = fit8(scatter_max(m, lane));
+  const Fit8 f = fit8<true>(scatter_max(m, lane));
   {
     float* s = (c8 & 3) == 0 ? p.gs : (c8 & 3) == 1 ? p.us : H8 && (c8 & 3) == 2 ? p.hs : nullptr;
     if (s && c8 < 4 * kFwdRows && c8 / 4 < have) s[int64_t(kt) * p.M + row0 + c8 / 4] = f.s;
   }
 #pragma unroll
   for (int i = 0; i < kFwdRows; ++i) {
-    const float rg = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i, 16), ru = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i + 1, 16);
-    const float rh = H8 ? __shfl_sync(0xFFFFFFFFu, f.r, 4 * i + 2, 16) : 0.0f;
+    const float rg = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i, 16), lg = __shfl_sync(0xFFFFFFFFu, f.lo, 4 * i, 16);
+    const float ru = __shfl_sync(0xFFFFFFFFu, f.r, 4 * i + 1, 16), lu = __shfl_sync(0xFFFFFFFFu, f.lo, 4 * i + 1, 16);
+    const float rh = H8 ? __shfl_sync(0xFFFFFFFFu, kExact ? f.r : f.r + f.lo, 4 * i + 2, 16) : 0.0f;
+    const float lh = H8 && kExact ? __shfl_sync(0xFFFFFFFFu, f.lo, 4 * i + 2, 16) : 0.0f;
     if (i >= rows) continue;
     const int64_t r = row0 + i;
-    put_bytes8(p.gq + r * p.ld_gq + k, left, codes8<true>(pairs(g[i]), rg));
-    put_bytes8(p.uq + r * p.ld_uq + k, left, codes8<true>(pairs(u[i]), ru));
-    if (H8) put_bytes8(p.hq + r * p.ld_hq + k, left, codes8<false>(h[i], rh));
+    put_bytes8(p.gq + r * p.ld_gq + k, left, codes8(pairs(g[i]), rg, lg));
+    put_bytes8(p.uq + r * p.ld_uq + k, left, codes8(pairs(u[i]), ru, lu));
+    if (H8) put_bytes8(p.hq + r * p.ld_hq + k, left, kExact ? codes8(h[i], rh, lh) : codes8(h[i], rh));
     else put8(p.h + r * p.ld_h + k, left, packed(h[i]));
   }
 }
@@ -299,14 +302,14 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
         m[2 * i + 1] = amax8(o.du);
       }
       // rows of d: lane 2 i + x of eight fits row i of dGate (x = 0) or dUp
-      const Fit8 f = fit8(scatter_max(m, lane));
+      const Fit8 f = fit8<false>(scatter_max(m, lane));
       if (c8 < 2 * kTileRows && c8 / 2 < rows) p.ds[int64_t(kt + (c8 & 1) * p.k_tiles) * p.M + t.r0 + row0 + c8 / 2] = f.s;
 #pragma unroll
       for (int i = 0; i < kTileRows; ++i)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const float r = __shfl_sync(0xFFFFFFFFu, f.r, 2 * i + x, 16);
-          if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8<false>(v[x][i], r));
+          if (i < rows) put_bytes8(p.dq + (t.r0 + row0 + i) * p.ld_dq + x * p.H + k, 8, codes8(v[x][i], r));
         }
     } else {  // none of the warp's rows: zeros, for the columns
 #pragma unroll
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
         float a = sh.part[x][0][c];
 #pragma unroll
         for (int i = 1; i < kTileWarps; ++i) a = max_nan(a, sh.part[x][i][c]);
-        const Fit8 fc = fit8(a);
+        const Fit8 fc = fit8<false>(a);
         sh.r[x][c] = fc.r;
         if (x < 2) p.dsc[int64_t(tile) * 2 * p.H + x * p.H + kt * kBlock8 + c] = fc.s;
         else if (p.hsc) p.hsc[int64_t(tile) * p.H + kt * kBlock8 + c] = fc.s;
@@ -361,7 +364,7 @@ __global__ void __launch_bounds__(kTileWarps * 32, 1) glu8_bwd_tile_kernel(const
         uint8_t* out = x < 2 ? p.dqc + row * p.ld_dqc + x * p.H + k : p.hqc + row * p.ld_hqc + k;
         const int64_t ld = x < 2 ? p.ld_dqc : p.ld_hqc;
 #pragma unroll
-        for (int i = 0; i < kTileRows; ++i) put_bytes8(out + i * ld, 8, codes8<false>(v[x][i], r));
+        for (int i = 0; i < kTileRows; ++i) put_bytes8(out + i * ld, 8, codes8(v[x][i], r));
       }
     }
     __syncwarp();  // the warp has read its rows before those of the next tile but one arrive

@@ -34,7 +34,7 @@ struct QuantShared {
   uint8_t in[2][kBlock8][kBlock8 * (KEPT ? 1 : 2)];
   float in_s[2][KEPT ? kBlock8 : 4];
   float part[kQuantWarps][kBlock8];  // maxima that each warp found of its rows
-  float r[kBlock8];                  // what the columns' codes are made with
+  float r[kBlock8], lo[KEPT ? 4 : kBlock8];  // what the columns' codes are made with
 };
 
 // Half-precision pairs as fp32: exact.
@@ -86,13 +86,13 @@ __device__ __forceinline__ void quant_tile(const QuantP& p, QuantShared<KEPT>& s
       if (c8 == i) mine = __uint_as_float(m << 16);
       if (c8 == i + 1) mine = __uint_as_float(m & 0xFFFF0000u);
     }
-    const Fit8 f = fit8(mine);
+    const Fit8 f = fit8<true>(mine);
     if (c8 < kRowsPerLane && c8 < rows) p.s[int64_t(kt) * p.M + t.r0 + row0 + c8] = f.s;
     uint8_t* out = p.q + int64_t(t.r0 + row0) * p.ld_q + k;
 #pragma unroll
     for (int i = 0; i < kRowsPerLane; ++i) {
-      const float r = __shfl_sync(0xFFFFFFFFu, f.r, i, 16);
-      if (i < rows && left > 0) put_bytes8(out, left, codes8<true>(pairs(w[i]), r));
+      const float r = __shfl_sync(0xFFFFFFFFu, f.r, i, 16), lo = __shfl_sync(0xFFFFFFFFu, f.lo, i, 16);
+      if (i < rows && left > 0) put_bytes8(out, left, codes8(pairs(w[i]), r, lo));
       out += p.ld_q;
     }
   }
@@ -140,18 +140,22 @@ __device__ __forceinline__ void quant_tile(const QuantP& p, QuantShared<KEPT>& s
     float a = sh.part[0][threadIdx.x];
 #pragma unroll
     for (int i = 1; i < kQuantWarps; ++i) a = max_nan(a, sh.part[i][threadIdx.x]);
-    const Fit8 f = fit8(a);
+    const Fit8 f = fit8<!KEPT>(a);
     sh.r[threadIdx.x] = f.r;
+    if (!KEPT) sh.lo[threadIdx.x] = f.lo;
     if (WHOLE || kt * kBlock8 + int32_t(threadIdx.x) < p.K) p.sc[int64_t(tile) * p.K + kt * kBlock8 + threadIdx.x] = f.s;
   }
   __syncthreads();
-  float2 r[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) r[j] = *reinterpret_cast<const float2*>(&sh.r[c8 * 8 + 2 * j]);
   uint8_t* out = p.qc + (int64_t(tile) * kBlock8 + row0) * p.ld_qc + k;
+  float2 r[4], lo[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = *reinterpret_cast<const float2*>(&sh.r[c8 * 8 + 2 * j]);
+    if (!KEPT) lo[j] = *reinterpret_cast<const float2*>(&sh.lo[c8 * 8 + 2 * j]);
+  }
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i) {
-    if (left > 0) put_bytes8(out, left, codes8<!KEPT>(value(i), r));
+    if (left > 0) put_bytes8(out, left, KEPT ? codes8(value(i), r) : codes8(value(i), r, lo));
     out += p.ld_qc;
   }
 }
@@ -244,12 +248,12 @@ __global__ void __launch_bounds__(kQuantWarps * 32, 4) weight8_kernel(const __gr
   float a = 0.0f;
 #pragma unroll
   for (int i = 0; i < kQuantWarps; ++i) a = max_nan(a, part[i]);
-  const Fit8 f = fit8(a);
+  const Fit8 f = fit8<true>(a);
   if (threadIdx.x == 0) p.s[int64_t(rt) * p.k_tiles + kt] = f.s;
   uint8_t* dst = p.q + e * p.stride_q + int64_t(row0) * p.ld_q + k;
 #pragma unroll
   for (int i = 0; i < kRowsPerLane; ++i)
-    if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8<true>(pairs(w[i]), f.r));
+    if (i < rows && left > 0) put_bytes8(dst + i * p.ld_q, left, codes8(pairs(w[i]), f.r, f.lo));
 }
 
 }  // namespace

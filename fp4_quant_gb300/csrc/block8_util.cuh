@@ -16,19 +16,25 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
-// What a block's codes are made with (values times r, rounded) and its scale;
-// both NaN where it holds a NaN or an infinity, which makes its codes NaN too.  s
-// is a / 448 rounded once: the product with the rounded 1 / 448, corrected by its
-// remainder (Markstein, 1990).  r is 1 / s, which stays in range for all a.
+// What a block's codes are made with and its scale; all NaN where it holds a NaN or
+// an infinity, which makes its codes NaN too.  s is a / 448 rounded once: the product
+// with the rounded 1 / 448, corrected by its remainder (Markstein, 1990).  r is 448 / a,
+// the reciprocal of s corrected in the same way: rounded once (lo is 0), or, EXACT, in
+// two parts that are within 2^-45 of it together, r rounded down and what that leaves,
+// which is never negative (so that a zero keeps its sign).  All is in range for all a.
+// Once per block, by the lane that has its maximum.
 struct Fit8 {
-  float r, s;
+  float r, lo, s;
 };
+template <bool EXACT>
 __device__ __forceinline__ Fit8 fit8(float amax) {
   constexpr float kInv = 1.0f / kTop8;
   const float a = amax <= 3.402823466e38f ? fmaxf(amax, kLeast8) : __uint_as_float(0x7FC00000u), q = a * kInv;
   Fit8 f;
   f.s = fmaf(fmaf(-q, kTop8, a), kInv, q);
-  f.r = rcp_fast(f.s);
+  const float y = rcp_fast(f.s), rest = fmaf(-y, a, kTop8), step = y * kInv;
+  f.r = EXACT ? __fmaf_rd(rest, step, y) : fmaf(rest, step, y);
+  f.lo = EXACT ? fmaxf(fmaf(-f.r, a, kTop8), 0.0f) * step : 0.0f;
   return f;
 }
 
@@ -38,31 +44,35 @@ __device__ __forceinline__ uint32_t e4m3x2_of(float2 v) {
   return r;
 }
 
-// Codes of eight values, scaled by r (a pair for each two of them).  SNAP: the
-// values are bf16.  Then the exact quotient 448 v / a is either the midpoint of two
-// codes or 2^-13 (relative) away from it at least: with 8-bit integers m, a' and
-// an odd one of 5 bits t, |7 m 2^x - t a'| is 0 or 1 at least, and t a' < 2^13.
-// v r is within 2^-22 + 2^-24 of it (s, r and the product are rounded), so rounded to 16 significant bits it is on
-// the quotient's side of every midpoint, and on the midpoint where that is.  The
-// rounding is Veltkamp's: t 257 - (t 257 - t), two values at a time.
-template <bool SNAP>
+// Codes of values of a block whose maximum is a, by their quotients 448 v / a rounded
+// to fp32.  With both parts of 448 / a they are rounded once (v r + v lo is within
+// 2^-45 of them before that), and one that is a midpoint of two codes stays one.  A
+// quotient of bf16 values is 2^-13 (relative) away from every other midpoint at least:
+// with 8-bit integers m, a' and an odd one of 5 bits t, |7 m 2^x - t a'| is 1 at
+// least, and t a' < 2^13; one of products of two bf16 is 2^-21 away in the same way.
+// So either gets the exact quotient's code.  Values that are rounded themselves, by
+// 2^-24 at least, are multiplied with 448 / a rounded to one number, which adds a
+// rounding of 2^-24 and no more (in two parts: the kept rows of 32768 x 2048 46 us
+// instead of 41, the quantised backward of 32768 x 1024 94 instead of 86, cold).
+__device__ __forceinline__ uint2 codes8(const F8& v, const float2 (&r)[4], const float2 (&lo)[4]) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = e4m3x2_of(fma_2(v.v[i], r[i], mul_2(v.v[i], lo[i])));
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
 __device__ __forceinline__ uint2 codes8(const F8& v, const float2 (&r)[4]) {
   uint32_t h[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float2 t = mul_2(v.v[i], r[i]);
-    if (SNAP) {
-      const float2 p = mul_2(t, both(257.0f)), d = fma_2(t, both(-1.0f), p);
-      t = fma_2(d, both(-1.0f), p);
-    }
-    h[i] = e4m3x2_of(t);
-  }
+  for (int i = 0; i < 4; ++i) h[i] = e4m3x2_of(mul_2(v.v[i], r[i]));
   return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
 }
-template <bool SNAP>
+__device__ __forceinline__ uint2 codes8(const F8& v, float r, float lo) {
+  const float2 q[4] = {both(r), both(r), both(r), both(r)}, l[4] = {both(lo), both(lo), both(lo), both(lo)};
+  return codes8(v, q, l);
+}
 __device__ __forceinline__ uint2 codes8(const F8& v, float r) {
   const float2 q[4] = {both(r), both(r), both(r), both(r)};
-  return codes8<SNAP>(v, q);
+  return codes8(v, q);
 }
 
 // What eight codes stand for without their scale, exact in fp32.

@@ -563,3 +563,77 @@ def test_glu_nan_stays_in_its_block():
     bad = torch.isnan(b["d"]["s"])
     assert bool(bad[0, 5]) and bool(bad[2, 5]) and bool(bad[1, 9]) and not bool(bad[3, 9]) and int(bad.sum()) == 3
     assert int(torch.isnan(b["d"]["sc"]).sum()) == 128 * 3 and int(torch.isnan(b["h"]["sc"]).sum()) == 256
+
+
+def test_codes_of_products_of_bf16_are_exact():
+    """h without a rounding ahead of its own (ReLU, identity): products of two bf16 are
+    exact in fp32, so their codes and scales are the definition's, midpoints included."""
+    for act in (G.ACT_RELU, G.ACT_IDENTITY):
+        for H, cut in ((2048, 0xFFFF0000), (2048, 0xFFE00000), (1000, 0xFFFF0000)):  # full mantissas; three bits, where midpoints abound
+            gate, up = ((_x(1000, H, H + s).float().view(torch.int32) & (cut - (1 << 32))).view(F32) for s in (0, 1))
+            gate, up = _padded(gate, BF), _padded(up, BF)
+            h = _act64(act, gate.to(F64))[0] * up.to(F64)
+            o = G.glu8(gate, up, act=act)
+            _check_exact(o["h"]["q"], o["h"]["s"], h, 1, 128, True)
+
+
+def test_kept_rows_with_scales_of_powers_of_two():
+    """Then the kept values are exact in fp32, quotients are midpoints or 2^-9 away from
+    one, and 448 / a rounded once decides all of them: the definition's codes."""
+    q = _rand_codes(1000, 512, 3)
+    s = _power(torch.randint(-9, 9, (4, 1000), generator=_gen(4), device=DEV)).to(F32)
+    x = {"q": q, "s": s}
+    o = G.quant8(x, rows=False, cols=True)
+    v = _cols(_kept(x), None)
+    _check_exact(o["qc"], o["sc"], v, 128, 1, False)
+    t = (v * TOP / _tile(v, 128, 1)[0]).abs()
+    half = _power((torch.frexp(t)[1] - 1).clamp_min(-6) - 4)
+    assert int(((t / half) % 2 == 1).sum()) > 1000  # there were midpoints
+
+
+def test_kept_codes_are_within_four_roundings():
+    """A kept value, its block's maximum, 448 / maximum and their product are rounded to
+    fp32 once each, 2^-24 of them at most, and nothing else comes before the code.  How
+    many codes differ from the definition's says nothing here: rows of bf16 often share a
+    scale s, their values c s are rounded one by one, and a quotient c / c' of two codes
+    of 4 bits that is a midpoint is then passed to either side."""
+    x = G.quant8(_x(4096, 4096, 8))
+    o = G.quant8({"q": x["q"], "s": x["s"]}, rows=False, cols=True)
+    v = _cols(_kept(x), None)
+    t = v * TOP / _tile(v, 128, 1)[0]
+    d = t.abs() * (4 * 2.0 ** -24 + 2.0 ** -45)
+    q = o["qc"].to(F64)
+    assert bool(((q >= _e4m3(t - d)) & (q <= _e4m3(t + d))).all())
+
+
+def test_kept_quotients_next_to_borders():
+    """Codes of 1 stand for their scales, any fp32: 448 / maximum and its product with the
+    value are then the only roundings, 2^-23 of a quotient together.  Values whose
+    quotients are that and a little more from a border between two codes get the
+    definition's code."""
+    blocks, M = 1024, 256
+    g = _gen(12)
+    a = torch.exp(2 * torch.randn(1, blocks, generator=g, device=DEV)).to(F64)
+    odd = 2 * torch.randint(8, 16, (M, blocks), generator=g, device=DEV) + 1
+    q = odd.to(F64) * _power(torch.randint(-6, 4, (M, blocks), generator=g, device=DEV))  # up to 31 * 8, below 448
+    v = (q * a / TOP).to(F32)
+    v = (v.view(torch.int32) + torch.randint(-3, 4, (M, blocks), generator=g, device=DEV, dtype=torch.int32)).view(F32)
+    v[::128] = a.to(F32)
+    x = {"q": torch.ones(M, 128 * blocks, dtype=F8, device=DEV), "s": v.t().contiguous()}
+    o = G.quant8(x, rows=False, cols=True)
+    a = a.to(F32).to(F64)
+    t = v.to(F64) * TOP / a
+    away = (t - q).abs() > q * (2.0 ** -23 + 2.0 ** -40)
+    away[::128] = False  # the maxima themselves
+    got = o["qc"].view(M, blocks, 128).to(F64)
+    assert bool((got == got[:, :, :1]).all()) and bool((got[::128] == TOP).all())
+    assert int(away.sum()) > M * blocks // 4
+    assert torch.equal(got[:, :, 0][away], _e4m3(t)[away])
+
+
+def test_zeros_among_other_values_keep_their_sign():
+    x = _x(130, 256, 21)
+    x[:, ::3], x[:, 1::3] = -0.0, 0.0
+    o = G.quant8(x, rows=True, cols=True)
+    for q in (o["q"], o["qc"][:130], G.quant8_weight(x)["q"], G.glu8(x, x)["gate"]["q"]):
+        assert bool((q[:, ::3].view(torch.uint8) == 0x80).all()) and bool((q[:, 1::3].view(torch.uint8) == 0).all())
