@@ -205,6 +205,11 @@ def _stack(t, E, N, ld):
     return 0 if not E else t.stride(0) if E > 1 else N * ld
 
 
+def _may_split(M, E, grad):
+    """Whether the library may want a workspace: never by expert, nor for y of one token."""
+    return E == 0 and (grad or M > 1)
+
+
 def _product(x8, w8, offsets, out, grad):
     wq = w8["q"]
     if wq.dim() != (2 if offsets is None else 3):
@@ -224,7 +229,7 @@ def _product(x8, w8, offsets, out, grad):
     a = Linear8Args(M, N, K, ld_x, ld_w, _stack(wq, E, N, ld_w), _ld(y), x8["q"].data_ptr(), xs, wq.data_ptr(), ws, off, y.data_ptr(),
                     None, 0, E, int(grad))
     ws = None
-    if E == 0 and M > 1:  # by expert and for one token it takes none
+    if _may_split(M, E, grad):
         n = _size(0)
         _call("glu_block8_linear_workspace", a, n)
         ws = _scratch(n.value)

@@ -199,3 +199,19 @@ def test_binding_refuses_on_the_cpu():
         G.linear8_dw({"qc": None, "sc": None}, {"qc": None, "sc": None})
     with pytest.raises(ValueError, match="128"):
         G.linear8_dw({"qc": torch.zeros(100, 16)}, {"qc": torch.zeros(100, 16)})
+
+
+@pytest.mark.parametrize("N,K", [(512, 300), (2048, 2048), (300, 8192), (8192, 7168)])
+def test_binding_asks_for_every_workspace(N, K):
+    """A call for which the library wants a workspace is one for which the binding asks."""
+    seen = set()
+    for grad in (False, True):
+        for E in (0, 3):
+            for M in (*range(1, 21), 200, 4096):
+                n = ctypes.c_size_t(0)
+                a = B.Linear8Args(M=M, N=N, K=K, E=E, grad=int(grad))
+                assert B._func("glu_block8_linear_workspace")(ctypes.byref(a), ctypes.byref(n)) == G.GLU_OK
+                assert n.value == 0 or B._may_split(M, E, grad), (M, E, grad, n.value)
+                seen.add((M == 1, grad, n.value > 0))
+    if N >= 2048:
+        assert (True, True, True) in seen  # a gradient of one token does take one

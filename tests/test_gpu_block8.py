@@ -637,3 +637,11 @@ def test_zeros_among_other_values_keep_their_sign():
     o = G.quant8(x, rows=True, cols=True)
     for q in (o["q"], o["qc"][:130], G.quant8_weight(x)["q"], G.glu8(x, x)["gate"]["q"]):
         assert bool((q[:, ::3].view(torch.uint8) == 0x80).all()) and bool((q[:, 1::3].view(torch.uint8) == 0).all())
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (1, 4096, 4096), (1, 2049, 1000), (1, 1000, 2049), (1, 8192, 7168), (2, 8192, 7168)])
+def test_products_of_one_and_two_deep_rows(M, N, K, grad):
+    """One token's sum is cut into parts too, where the gradient's is deep."""
+    x, w = _operands(M, N, K, 0, grad, M + N)
+    _check_product((G.linear8_dx if grad else G.linear8)(x, w), x, w, grad, None)
