@@ -79,13 +79,15 @@ _funcs = {}  # name -> function, filled with the first call
 
 
 def _func(name):
-    if not _funcs:
+    f = _funcs.get(name)
+    if f is None:  # another thread may be half-way through the same
         lib = _lib()
         for n, argtypes in _SIGNATURES.items():
             f = getattr(lib, n)
             f.argtypes, f.restype = argtypes, ctypes.c_int
             _funcs[n] = f
-    return _funcs[name]
+        f = _funcs[name]
+    return f
 
 
 def _call(name, *args):

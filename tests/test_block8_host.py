@@ -215,3 +215,12 @@ def test_binding_asks_for_every_workspace(N, K):
                 seen.add((M == 1, grad, n.value > 0))
     if N >= 2048:
         assert (True, True, True) in seen  # a gradient of one token does take one
+
+
+def test_first_calls_from_several_threads(monkeypatch):
+    """A thread may find the table of functions half filled by another one: it fills the rest."""
+    first = next(iter(B._SIGNATURES))
+    monkeypatch.setattr(B, "_funcs", {first: B._func(first)})
+    for name, argtypes in B._SIGNATURES.items():
+        assert B._func(name).argtypes == argtypes
+    assert B._func("glu_block8_abi_version")() == 1
