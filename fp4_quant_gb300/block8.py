@@ -11,8 +11,10 @@ An operand is a dict of E4M3 codes (``torch.float8_e4m3fn``) and fp32 scales:
 
 A block stands for codes times scale; its scale is its largest absolute value (2^-100
 at least) over 448, and a NaN or an infinity makes the whole block NaN.  Checks,
-allocation, streams and errors are those of ``block``; code matrices have a row
-stride that is a multiple of 16 and scales are contiguous.
+allocation, streams and errors are those of ``block``; a matrix of bf16 rows that does
+not begin on 16 bytes is copied first as well, such as the second half of a projection
+of odd width.  Code matrices have a row stride that is a multiple of 16 and scales are
+contiguous.
 """
 from __future__ import annotations
 
@@ -21,7 +23,7 @@ import ctypes
 import torch
 
 from . import ACT_SILU, FMT_BF16, FMT_FP32, GLU_OK, GluQuantError, _lib
-from .block import (_BF16, _F32, _I32, _alloc, _device, _handle, _ld, _matrix, _on, _p, _packed, _result, _rows,
+from .block import (_BF16, _F32, _I32, _alloc, _device, _handle, _ld, _matrix, _new, _on, _p, _packed, _result, _rows,
                     _scratch)
 
 __all__ = ["quant8", "quant8_weight", "linear8", "linear8_dx", "linear8_dw", "glu8", "glu8_bwd", "block8_abi_version"]
@@ -114,6 +116,16 @@ def _scales(t, name, shape, device):
     return _packed(t, name, shape, device, (_F32,))
 
 
+def _bf16_rows(t, name, shape, device):
+    """``_rows``, with a copy too where the base is not on 16 bytes, as the second
+    half's of a projection of odd width is not."""
+    t, ld = _rows(t, name, shape, device)
+    if t.data_ptr() % 16:
+        t = _new(shape, _BF16).copy_(t.detach())
+        ld = _ld(t)
+    return t, ld
+
+
 def _out_codes(out, key, shape, device):
     """A code matrix for an output (the caller's, checked, or a new one) and its row stride."""
     t = None if out is None else out.get(key)
@@ -172,7 +184,7 @@ def quant8(x, *, rows=True, cols=False, offsets=None, out=None, stream=None) -> 
             raise ValueError("x must be a matrix")
         device = _device(x, "x")
         M, K = x.shape
-        src, ld = _rows(x, "x", (M, K), device)
+        src, ld = _bf16_rows(x, "x", (M, K), device)
         xq, xs, ld_xq = None, None, 0
     E, off = _experts(offsets, device)
     C = _col_blocks(M, E)
@@ -299,8 +311,8 @@ def glu8(gate, up, *, act=ACT_SILU, h8=True, out=None, stream=None) -> dict:
         raise ValueError("gate must be a matrix")
     device = _device(gate, "gate")
     M, H = gate.shape
-    gate, ld_gate = _rows(gate, "gate", (M, H), device)
-    up, ld_up = _rows(up, "up", (M, H), device)
+    gate, ld_gate = _bf16_rows(gate, "gate", (M, H), device)
+    up, ld_up = _bf16_rows(up, "up", (M, H), device)
     got, lds = {}, {}
     for key in ("h", "gate", "up") if h8 else ("gate", "up"):
         q, lds[key] = _out_codes(_some(out, key), "q", (M, H), device)
@@ -331,7 +343,7 @@ def glu8_bwd(gate8, up8, dh, *, act=ACT_SILU, quant=False, need_h=True, offsets=
     M, H, device = _row_form(gate8, "gate8")
     ld_gq, ld_uq = _codes(gate8["q"], "gate8['q']", (M, H), device), _codes(up8["q"], "up8['q']", (M, H), device)
     gs, us = _scales(gate8["s"], "gate8['s']", (_blocks(H), M), device), _scales(up8["s"], "up8['s']", (_blocks(H), M), device)
-    dh, ld_dh = _rows(dh, "dh", (M, H), device)
+    dh, ld_dh = _bf16_rows(dh, "dh", (M, H), device)
     if offsets is not None and not quant:
         raise ValueError("offsets cut the column forms of quant=True only")
     E, off = _experts(offsets, device)

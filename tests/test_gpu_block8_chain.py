@@ -254,3 +254,21 @@ def test_one_expert_of_a_stack():
     d = {"qc": many["qc"][128:], "sc": many["sc"][1:]}
     own = {"qc": d["qc"], "sc": d["sc"].clone()}
     assert torch.equal(G.linear8_dw(d, d), G.linear8_dw(own, own))
+
+
+@pytest.mark.parametrize("R,D,H", [(1, 128, 67), (40, 136, 67), (129, 264, 130), (33, 128, 1462), (20, 64, 1)])
+def test_halves_of_a_projection_of_any_width(R, D, H):
+    """The second half of a projection begins on 16 bytes only where its width is a
+    multiple of eight: forward and backward take it as they take an aligned copy."""
+    x8, w8 = G.quant8(_rand(R, D, seed=H)), G.quant8_weight(_rand(2 * H, D, seed=H + 1, scale=0.1))
+    u = G.linear8(x8, w8)
+    dh = G.linear8(x8, w8)[:, H:]
+
+    def aligned(t):
+        buf = torch.zeros(t.shape[0], -(-t.shape[1] // 8) * 8, dtype=BF, device=DEV)[:, :t.shape[1]]
+        return buf.copy_(t)
+    a, b = G.glu8(u[:, :H], u[:, H:]), G.glu8(aligned(u[:, :H]), aligned(u[:, H:]))
+    assert _equal([a[k][n] for k in a for n in ("q", "s")], [b[k][n] for k in b for n in ("q", "s")])
+    c, d = G.glu8_bwd(a["gate"], a["up"], dh), G.glu8_bwd(b["gate"], b["up"], aligned(dh))
+    assert torch.equal(c["d"], d["d"]) and torch.equal(c["h"], d["h"])
+    assert _equal(list(G.quant8(u[:, H:], cols=True).values()), list(G.quant8(aligned(u[:, H:]), cols=True).values()))
