@@ -645,3 +645,27 @@ def test_products_of_one_and_two_deep_rows(M, N, K, grad):
     """One token's sum is cut into parts too, where the gradient's is deep."""
     x, w = _operands(M, N, K, 0, grad, M + N)
     _check_product((G.linear8_dx if grad else G.linear8)(x, w), x, w, grad, None)
+
+
+@pytest.mark.parametrize("M,N,K,E", [(300, 130, 200, 0), (2000, 256, 136, 0), (700, 128, 260, 3)])
+def test_weight_gradients_sum_in_all_of_fp32(M, N, K, E):
+    """Whole numbers whose sums stay below 2^24 are summed exactly where every addition
+    keeps 24 bits: large products next to ones, and scales of powers of two that move
+    whole blocks up and down.  A sum that keeps fewer bits anywhere loses the ones."""
+    off = _offsets(M, E, M, 20) if E else None
+    C = M // 128 + E if E else _b(M)
+    g = _gen(M)
+
+    def codes(n):
+        big = torch.rand(128 * C, n, generator=g, device=DEV) < 0.02
+        v = torch.where(big, TOP, 1.0) * (1 - 2 * torch.randint(0, 2, (128 * C, n), generator=g, device=DEV))
+        return _padded(v.to(F8).float(), F8, 16)
+    s = [2.0 ** torch.randint(-1, 2, (C, 1), generator=g, device=DEV) for _ in range(2)]  # products are multiples of 1 / 4
+    dy, x = ({"qc": codes(n), "sc": c.expand(C, n).contiguous()} for n, c in zip((N, K), s))
+    dv, xv = (o["qc"].to(F64) * o["sc"].to(F64).repeat_interleave(128, 0) for o in (dy, x))
+    dw = G.linear8_dw(dy, x, offsets=off, dtype=F32)
+    spans = [(None, 0, C)] if off is None else [(e, a // 128 + e, a // 128 + e + _b(b - a)) for e, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:]))]
+    for e, b0, b1 in spans:
+        d, v = dv[128 * b0:128 * b1], xv[128 * b0:128 * b1]
+        assert d.numel() == 0 or float((d.abs().t() @ v.abs()).max()) * 4 < 2.0 ** 24  # any order of them is exact
+        assert torch.equal((dw if e is None else dw[e]).to(F64), d.t() @ v)
