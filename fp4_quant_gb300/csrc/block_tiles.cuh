@@ -1,5 +1,5 @@
-// Tiles of 256 rows by up to 256 columns for pairs of CTAs, dense or by expert,
-// and the stores of their accumulators: what the linear layers' kernels share.
+// Tiles of 256 rows by up to 256 columns for pairs of CTAs, dense or by expert, and
+// how many pairs run at once: what the linear layers' kernels share.
 #pragma once
 
 #include <atomic>
@@ -153,78 +153,6 @@ __device__ __forceinline__ void plan_tiles(const P& p, TilePlan& plan, int warp,
       tiles += __shfl_sync(0xFFFFFFFFu, n, 31);
     }
     if (lane == 0) plan.first[p.E] = tiles;
-  }
-}
-
-// Four 16-bit values per lane (two per word) of N independent 4 x 4 blocks,
-// each held by a quad of lanes, transposed: value j of lane l becomes value l %
-// 4 of lane j.  The blocks go through the exchanges together, so that their
-// latencies overlap.
-template <int N>
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[N][2], int lane) {
-  const bool odd = lane & 1, up = lane & 2;
-  uint32_t keep[N], got[N];
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const uint32_t even_half = __byte_perm(w[q][0], w[q][1], 0x5410), odd_half = __byte_perm(w[q][0], w[q][1], 0x7632);
-    keep[q] = odd ? odd_half : even_half;
-    got[q] = __shfl_xor_sync(0xFFFFFFFFu, odd ? even_half : odd_half, 1);
-  }
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    const uint32_t first = odd ? got[q] : keep[q], second = odd ? keep[q] : got[q];  // of the even and the odd lane
-    const uint32_t a = __byte_perm(first, second, 0x5410), b = __byte_perm(first, second, 0x7632);
-    keep[q] = up ? b : a;
-    got[q] = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 2);
-  }
-#pragma unroll
-  for (int q = 0; q < N; ++q) {
-    w[q][0] = up ? got[q] : keep[q];
-    w[q][1] = up ? keep[q] : got[q];
-  }
-}
-
-// Four consecutive bf16 of an output row (8-byte aligned), or its first n.
-__device__ __forceinline__ void store4(uint16_t* o, int n, const uint32_t (&w)[2]) {
-  if (n >= 4) {
-    *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-  } else {
-    if (n > 0) o[0] = uint16_t(w[0]);
-    if (n > 1) o[1] = uint16_t(w[0] >> 16);
-    if (n > 2) o[2] = uint16_t(w[1]);
-  }
-}
-
-// Where a warp's 32 tokens of y, z or the residual begin: the lane's token of
-// each quad, and its four columns.
-struct TokenView {
-  int32_t left;  // of the row from the lane's first column on
-  int32_t rows;  // of the tokens from the lane's first one on
-};
-__device__ __forceinline__ void store_quads(uint16_t* o, int64_t ld, const TokenView& t, uint32_t (&w)[8][2], int lane) {
-  quad_transpose(w, lane);
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    if (4 * q < t.rows) store4(o + 4 * q * ld, t.left, w[q]);
-}
-// The 4 x 4 block of 16-byte pieces that a quad of lanes holds (lane l: pieces
-// 0 .. 3 of a row in w[0..3], w[4..7], ...) transposed: lane l then has piece l
-// % 4 of the quad's four rows.
-__device__ __forceinline__ void piece_transpose(uint32_t (&w)[16], int lane) {
-  const bool odd = lane & 1, up = lane & 2;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {  // pieces 0, 1 and 2, 3 between neighbours
-    const int lo = (i / 4) * 8 + i % 4, hi = lo + 4;
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, odd ? w[lo] : w[hi], 1);
-    if (odd) w[lo] = got;
-    else w[hi] = got;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {  // pieces 0, 2 and 1, 3 between pairs
-    const int lo = i, hi = i + 8;
-    const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? w[lo] : w[hi], 2);
-    if (up) w[lo] = got;
-    else w[hi] = got;
   }
 }
 
