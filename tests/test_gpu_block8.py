@@ -669,3 +669,27 @@ def test_weight_gradients_sum_in_all_of_fp32(M, N, K, E):
         d, v = dv[128 * b0:128 * b1], xv[128 * b0:128 * b1]
         assert d.numel() == 0 or float((d.abs().t() @ v.abs()).max()) * 4 < 2.0 ** 24  # any order of them is exact
         assert torch.equal((dw if e is None else dw[e]).to(F64), d.t() @ v)
+
+
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("M,N,K,E", [(1, 130, 2000, 0), (16, 2000, 300, 0), (40, 2048, 2048, 0), (300, 260, 1000, 0), (200, 256, 384, 3), (700, 128, 512, 2)])
+def test_products_sum_in_all_of_fp32(M, N, K, E, grad):
+    """The same of y and dx: exact sums below 2^24, rounded to bf16 once."""
+    depth, width = (N, K) if grad else (K, N)
+    g = _gen(M)
+
+    def codes(rows, n):
+        big = torch.rand(rows, n, generator=g, device=DEV) < 0.02
+        v = torch.where(big, TOP, 1.0) * (1 - 2 * torch.randint(0, 2, (rows, n), generator=g, device=DEV))
+        return _padded(v.to(F8).float(), F8, 16)
+    q = codes(max(E, 1) * N, K)
+    w = {"q": q.view(E, N, K) if E else q, "s": 2.0 ** torch.randint(-1, 2, (*((E,) if E else ()), _b(N), _b(K)), generator=g, device=DEV)}
+    x = {"q": codes(M, depth), "s": 2.0 ** torch.randint(-1, 2, (_b(depth), M), generator=g, device=DEV)}
+    off = _offsets(M, E, M, 7) if E else None
+    y = (G.linear8_dx if grad else G.linear8)(x, w, offsets=off)
+    xv = _kept(x)
+    for e, a, b in [(None, 0, M)] if off is None else [(e, *off.tolist()[e:e + 2]) for e in range(E)]:
+        wv = _w64(w["q"], w["s"]) if e is None else _w64(w["q"][e], w["s"][e])
+        wv = wv if grad else wv.t()
+        assert a == b or float((xv[a:b].abs() @ wv.abs()).max()) * 4 < 2.0 ** 24
+        assert torch.equal(y[a:b], (xv[a:b] @ wv).to(F32).to(BF))

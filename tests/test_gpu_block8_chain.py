@@ -272,3 +272,91 @@ def test_halves_of_a_projection_of_any_width(R, D, H):
     c, d = G.glu8_bwd(a["gate"], a["up"], dh), G.glu8_bwd(b["gate"], b["up"], aligned(dh))
     assert torch.equal(c["d"], d["d"]) and torch.equal(c["h"], d["h"])
     assert _equal(list(G.quant8(u[:, H:], cols=True).values()), list(G.quant8(aligned(u[:, H:]), cols=True).values()))
+
+
+def _beside(rows, cols, dtype=F8, left=16):
+    """A matrix inside a wider one of sevens, and a check that nothing but it was written."""
+    ld = left + -(-cols // 16) * 16 + 16
+    buf = torch.full((rows + 2, ld * dtype.itemsize), 7, dtype=torch.uint8, device=DEV)
+    t = buf.view(dtype)[1:-1, left:left + cols]
+
+    def kept():
+        b = buf.clone()
+        b.view(dtype)[1:-1, left:left + cols].view(torch.uint8).fill_(7)
+        return bool((b == 7).all())
+    return t, kept
+
+
+@pytest.mark.parametrize("M,H,E", [(70, 128, 0), (70, 256, 3), (300, 384, 5)])
+def test_every_output_may_be_given(M, H, E):
+    """Outputs inside wider matrices are those of calls that allocate them, and what
+    stands around them is left alone."""
+    x, up, dh = (_rand(M, H, seed=M + i) for i in range(3))
+    off = torch.tensor([round(M * e / E * 0.9) for e in range(E + 1)], dtype=torch.int32, device=DEV) if E else None
+    C = M // 128 + E if E else -(-M // 128)
+    checks = []
+
+    def codes(rows, cols):
+        t, kept = _beside(rows, cols)
+        checks.append(kept)
+        return t
+    rows = lambda n: {"q": codes(M, n), "s": torch.empty(-(-n // 128), M, device=DEV)}  # noqa: E731
+    cols = lambda n: {"qc": codes(128 * C, n), "sc": torch.empty(C, n, device=DEV)}  # noqa: E731
+
+    def same(a, b):
+        for k in b:
+            if isinstance(b[k], dict):
+                same(a[k], b[k])
+            elif b[k] is not None:
+                assert _equal([a[k]], [b[k]]), k
+    both = {**rows(H), **cols(H)}
+    x8 = G.quant8(x, cols=True, offsets=off, out=both)
+    assert x8["qc"].data_ptr() == both["qc"].data_ptr()
+    same(x8, G.quant8(x, cols=True, offsets=off))
+    one = {"q": x8["q"].clone(memory_format=torch.contiguous_format), "s": x8["s"]}
+    same(G.quant8(one, rows=False, cols=True, offsets=off, out=cols(H)), G.quant8(one, rows=False, cols=True, offsets=off))
+    given = {"h": rows(H), "gate": rows(H), "up": rows(H)}
+    a = G.glu8(x, up, out=given)
+    same(a, G.glu8(x, up))
+    h, kept = _beside(M, H, BF)
+    checks.append(kept)
+    same(G.glu8(x, up, h8=False, out={"h": h, "gate": given["gate"]}), G.glu8(x, up, h8=False))
+    d = {**rows(2 * H), **cols(2 * H)}
+    same(G.glu8_bwd(a["gate"], a["up"], dh, quant=True, offsets=off, out={"d": d, "h": cols(H)}),
+         G.glu8_bwd(a["gate"], a["up"], dh, quant=True, offsets=off))
+    w = _rand(max(E, 1), 136, H, seed=9)
+    w = w if E else w[0]
+    big = torch.full((max(E, 1), 136 + 3, H + 32), 7, dtype=torch.uint8, device=DEV)
+    q = big[:, 1:-2, 16:16 + H].view(F8)
+    w8 = G.quant8_weight(w, out={"q": q if E else q[0]})
+    same(w8, G.quant8_weight(w))
+    for o, call in ((_beside(M, 136, BF), lambda out: G.linear8(x8, w8, offsets=off, out=out)),
+                    (_beside(M, H, BF), lambda out: G.linear8_dx(G.quant8(_rand(M, 136, seed=3)), w8, offsets=off, out=out))):
+        checks.append(o[1])
+        assert torch.equal(call(o[0]), call(None))
+    big[:, 1:-2, 16:16 + H] = 7
+    assert bool((big == 7).all()) and all(k() for k in checks)
+
+
+def test_a_captured_layer_reads_its_inputs_at_every_replay():
+    R, D, H, E = 600, 264, 256, 5
+    w8 = X.quantise(X.make_weights(D, H, E, seed=1))
+    off = _sorted(R, E, 2)["offsets"]
+    xs, dy = _rand(R, D, seed=3), _rand(R, D, seed=4)
+
+    def step():
+        y, s = X.forward(xs, w8, off)
+        return [y, *X.backward(dy, w8, s, off).values()]
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for seed in (5, 6):
+        xs.copy_(_rand(R, D, seed=seed))
+        dy.copy_(_rand(R, D, seed=seed + 10))
+        off.copy_(_sorted(R, E, seed + 20)["offsets"])
+        g.replay()
+        torch.cuda.synchronize()
+        kept = [t.clone() for t in got]
+        assert _equal(kept, step())
