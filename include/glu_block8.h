@@ -13,9 +13,13 @@
  * Format.  A block of 128 values v (fewer at the end of a dimension, as if
  * zeros followed) has a = max(max |v|, 2^-100), the scale s = a / 448 (fp32)
  * and the codes q = v * 448 / a rounded to E4M3 (to nearest, ties to even); it
- * stands for q * s.  Codes of bf16 values are those of the exact quotient;
- * where the values come from fp32 arithmetic, one within 2^-21 (relative) of a
- * border between two codes may get either.  A NaN or an infinity makes the
+ * stands for q * s.  Codes of bf16 values, and of products of two (glu8's h of ReLU
+ * and the identity), are those of the exact quotient.  Others come from fp32
+ * arithmetic: theirs are those of values within its error, to which the quotient adds
+ * 2^-23 (relative).  That error is a few 2^-24 of a value, |t| 2^-21 where the
+ * activation decays as e^-|t|, and relative to its terms where those cancel (dGate
+ * next to a zero of act').  Quotients of codes, which have few bits, are often
+ * midpoints between two codes, and may then get either.  A NaN or an infinity makes the
  * block's scale and codes NaN.  Three ways of cutting a matrix into blocks:
  *   rows     x [M, K]: 1 x 128.  q [M, K], s [ceil(K / 128), M].
  *   columns  x [M, K]: 128 x 1, for sums over the rows.  q [128 C, K], s
@@ -80,8 +84,10 @@ GLU_API int glu_block8_quant_weight(const glu_block8_quant_weight_args* args, vo
 /* ---- linear8 -----------------------------------------------------------
  * y = x W^T (grad 0: x [M, K] in row form, y bf16 [M, N]) or y = x W (grad 1,
  * the gradient of the input: x [M, N], y [M, K]), W [N, K] as weights.  The
- * tensor cores sum each block's 128 products; the blocks' sums are scaled and
- * added in fp32, in an order that depends on the shapes only.  By expert rows
+ * tensor cores sum each block's 128 products; the blocks' sums are scaled, by the
+ * fp32 product of the two scales, and added in fp32, in an order that depends on the
+ * shapes only (a product of scales below 2^-126 loses bits, which is 2^-125 of a
+ * result at most per block, and one above 2^128 is infinite).  By expert rows
  * offsets[e] .. offsets[e + 1] - 1 take W[e], rows from offsets[E] on give 0.
  * N, K <= 2^23.  The workspace (16-byte aligned; NULL where the query says 0)
  * joins the parts of sums that are split when there are few rows. */
@@ -150,8 +156,8 @@ typedef struct glu_block8_glu_args {
  * as bf16 (d; h or NULL), or quantised, without a rounding to bf16 between:
  * d in row form (dq, ds) and in column form (dqc, dsc), h in column form (hqc,
  * hsc, or both NULL).  The latter wants H a multiple of 128; offsets and E are
- * those of the column forms.  act' of SiLU and the GELUs is 0 and 1 at -inf
- * and +inf, ReLU's is 0 up to 0. */
+ * those of the column forms.  Far out act' of SiLU and the GELUs is 0 and 1;
+ * ReLU's is 0 up to 0. */
 typedef struct glu_block8_glu_bwd_args {
   int64_t M, H;
   int64_t ld_gq, ld_uq, ld_dh, ld_d, ld_h, ld_dq, ld_dqc, ld_hqc;
