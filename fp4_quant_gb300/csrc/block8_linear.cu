@@ -18,8 +18,8 @@
 // What a thread has of the accumulator decides what its scales cost.  With the
 // tokens as the rows of D (ROWS: many tokens) it has one row of 128 columns, where
 // the token's scale and the weight's are one number per block: 4096 x 8192 x 7168
-// takes 174 us (2760 TFLOP/s), its dx 168, 32768 rows of 64 uneven experts x 2048 x
-// 2048 158.  With few tokens they are the columns, whose number the instruction
+// takes 174 to 191 us with the clocks that the power limit leaves (2760 to 2520
+// TFLOP/s), its dx 168 to 187, 32768 rows of 64 uneven experts x 2048 x 2048 153 to 167.  With few tokens they are the columns, whose number the instruction
 // leaves free in steps of 32, and so they are in the columns' place for dw, whose
 // rows and columns both have scales of their own.  A thread with one row would need
 // all the columns' scales then, 128 KB out of shared memory per block at 128 bytes a
@@ -597,8 +597,9 @@ cudaError_t launch8(Linear8P& p, cudaStream_t s, const DevInfo& d) {
 // and 80, 256 rows 109 and 117, 512 158 and 180.  Dense the plan with the least
 // estimated time: a block of the sum takes 0.42 us with the tokens as rows (7168 deep,
 // 4096 x 8192: 174 us), as columns 0.4 us for 32 of them and 0.55 for 256 (8192 deep,
-// 7168 wide: 31 us for 32 tokens; 4096 tokens 203), the busiest pair's tiles follow
-// each other, and the join of split sums reads and writes the fp32 parts.
+// 7168 wide: one part for 32 tokens 31 us, two parts, as the plan has it, 22.5; 4096
+// tokens 203), the busiest pair's tiles follow each other, and the join of split sums
+// reads and writes the fp32 parts.
 struct TokenPlan8 {
   int most, splits;
   bool rows;

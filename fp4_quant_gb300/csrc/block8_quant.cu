@@ -4,12 +4,14 @@
 // Rows and columns: blocks of 256 threads walk tiles of 128 x 128 values, three per
 // SM.  The next tile is on its way into shared memory while this one's maxima are
 // found, of rows by 16 lanes and of columns through shared memory, and its codes
-// are stored: 4096 x 7168 as rows and columns 24.6 us (117 MB, 4.8 TB/s), 32768 x
-// 2048 kept rows of 64 experts as columns 38.  The copies are hidden (one block per
-// tile with its values in registers: 24.8 and 41.9); what binds is the issue of 13
-// to 17 instructions per value, at two thirds of the rate, where the sums, maxima
-// and roundings themselves are about ten.  Weights need one maximum per tile, and a
-// block for each: 64 x 2048 x 2048 in 126 us, 6.4 TB/s.
+// are stored: 4096 x 7168 as rows and columns in calls of 20.9 us (119 MB, 5.7 TB/s),
+// 32768 x 2048 kept rows of 64 experts as columns 35.7.  The copies are hidden (one
+// block per tile with its values in registers: 24.8 and 41.9).  No unit is full: warps
+// issue in 60 and 66 % of the cycles, the integer pipe works in 62 and 54 %, DRAM in 36
+// and 17 %.  Five warps per scheduler are too few to fill the rest: of the 8 cycles
+// between a warp's instructions it waits 1.4 and 1.1 for that pipe, 1.1 and 1.3 for the
+// result before, 0.9 and 0.6 for memory, 0.7 and 0.9 at the barriers.  Weights need one
+// maximum per tile, and a block for each: 64 x 2048 x 2048 in 119 us, 6.8 TB/s.
 #include "block8_util.cuh"
 
 namespace gq {
