@@ -1,11 +1,12 @@
 // The gated activation's values for the operators in 8 bits: act(z) and act'(z)
 // in fp32, two at a time, from ex2.approx and rcp.approx (2^-22 and 2^-23): good to a
 // few 2^-23, and to |t| 2^-24 more where they go as e^-|t| (the exponent t log2 e is
-// rounded once; the tanh GELU's t is a polynomial of five roundings more).  The blocks' codes have four bits, and it is their borders that an
-// error crosses: with the exponent's rounding made up for and the reciprocal corrected,
-// 177 instead of 182 codes of h in 1e8 differ from 64 bits (SiLU of N(0, 1) gates; fp32
-// functions and divisions 167), for 47 instead of 44 us (GELU 53 instead of 45, the
-// quantised backward 95 instead of 86, cold).
+// rounded once; the tanh GELU's t is a polynomial of five roundings more).  The
+// blocks' codes have four bits, and it is their borders that an error crosses: with the
+// exponent's rounding made up for and the reciprocal corrected, 177 instead of 182 codes
+// of h in 1e8 differ from 64 bits (SiLU of N(0, 1) gates; fp32 functions and divisions
+// 167), for 47 instead of 44 us (GELU 53 instead of 45, the quantised backward 95
+// instead of 86, cold).
 #pragma once
 
 #include "block8_util.cuh"

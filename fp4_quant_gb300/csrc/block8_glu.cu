@@ -5,11 +5,11 @@
 // per place of a tile (80.2 us for 32768 x 1024 of 64 experts).  The bf16 one takes
 // 27.5 us for 8191 x 1462, where dUp's rows begin inside 16 bytes, and three quarters of
 // that for a width of 1464.  No unit is full: in that order warps issue in 64, 58 and
-// 62 % of the cycles, the integer pipe works in 49, 51 and 41 %, DRAM in 53, 26 and 29 %.  Of the 10.6, 6.9 and 8.2 cycles between a
-// warp's instructions it waits for loads most where the kernel has no copies ahead (4.1
-// forward, 2.3 in the bf16 backward); the quantised backward, four warps per scheduler,
-// waits 1.2 for the result before, 0.9 each for the pipe and for shared memory and 0.7
-// at the barriers.
+// 62 % of the cycles, the integer pipe works in 49, 51 and 41 %, DRAM in 53, 26 and
+// 29 %.  Of the 10.6, 6.9 and 8.2 cycles between a warp's instructions it waits for loads
+// most where the kernel has no copies ahead (4.1 forward, 2.3 in the bf16 backward); the
+// quantised backward, four warps per scheduler, waits 1.2 for the result before, 0.9
+// each for the pipe and for shared memory and 0.7 at the barriers.
 #include "block8_act.cuh"
 
 namespace gq {
